@@ -12,7 +12,8 @@
  * "量化", BitsAndBytesConfig bullets).  Around the initialisation the library
  * also merges an adapter into the quantized weights and takes it out again
  * (PEFT guide "量化"), and runs the QLoRA forward of an adapted layer on the
- * bf16 matrix cores ("参数高效微调：LoRA、Adapter 与 QLoRA", §2.2 and §4.3).
+ * bf16 matrix cores ("参数高效微调：LoRA、Adapter 与 QLoRA", §2.2 and §4.3).  For
+ * training it adds dropout and the layer's gradient, for serving MXFP4.
  *
  * Conventions for every call:
  *   - Matrices are row-major.  W is rows x cols (d x k); B is rows x r and A is
@@ -201,6 +202,123 @@ loftq_status_t loftq_qlora_forward_noalloc(const void* X, int64_t n_tok, int64_t
                                            const float* dq_scale, int32_t bits, const float* B, const float* A,
                                            int32_t r, float alpha, float* Y, void* stream);
 size_t loftq_qlora_forward_noalloc_max_bytes(void);
+
+/* ---- Training and serving an adapted layer ----
+ *
+ * What follows the initialisation: dropout (LoraConfig's lora_dropout, "参数高效微调：
+ * LoRA、Adapter 与 QLoRA" §2), the training forward and the gradient of an adapted layer over a
+ * frozen 4-bit base ("QLoRA论文概述": gradients are back-propagated through the frozen
+ * 4-bit model into the adapter), and MXFP4, the 4-bit format that the matrix cores
+ * multiply without decoding.  The conventions above hold, but for one: an infinity or a
+ * NaN in X or dY reaches the outputs that it takes part in, and none that it does not;
+ * what the dropout drops takes part in nothing. */
+
+/* A dropout mask is a function of (p, seed, offset, element index) and is never stored:
+ * a backward call with the same values uses its forward's mask.  thr = round(2^16 p)
+ * (halves up); the call's key is output offset + *step (output numbers from 0) of the
+ * SplitMix64 sequence started at seed; element i of the row-major flattening is dropped
+ * where 16 bits, lane i % 4 from the low end of output i / 4 of the sequence started at
+ * key, are below thr.  Kept elements are scaled by s = 2^16 / (2^16 - thr), the inverse of
+ * the share that is kept (s = 0 where everything is dropped). */
+typedef struct {
+  float p;               /* 0 <= p <= 1 */
+  uint64_t seed, offset; /* a new offset for every call that wants a mask of its own */
+  const uint64_t* step;  /* [device] 8-byte aligned, added to offset when the kernels run, so that a
+                            captured graph draws new masks as the caller counts it on; or NULL */
+} loftq_dropout_t;
+
+/* Y = s X where the mask keeps and 0 where it drops, whatever X holds there; in fp32,
+ * rounded once.  The gradient is the same call with dY in X's place.
+ *   X     [device] n elements of dtype dt
+ *   drop  [host]
+ *   Y     [device] n elements of dtype dt out; may be X */
+loftq_status_t loftq_dropout(const void* X, loftq_dtype_t dt, int64_t n, const loftq_dropout_t* drop, void* Y,
+                             void* stream);
+
+/* Training forward of one adapted layer: loftq_qlora_forward with dropout on the adapter's
+ * input and a choice of output type,
+ *   Y = X bf16(deq(Q))^T + alpha s (keep(X) bf16(A)^T) bf16(B)^T,
+ * keep(X) being X where the mask keeps element (token cols + column) and 0 elsewhere.
+ * Arguments as loftq_qlora_forward, and
+ *   drop   [host] or NULL (no dropout)
+ *   Y      [device] n_tok x rows of dtype ydt out
+ *   ws     [device] loftq_qlora_forward_dropout_workspace_bytes(n_tok, rows, cols, r) bytes
+ *          (it holds bf16(deq(Q)) during the call)
+ * Without B and A there is no adapter term and drop has no effect.
+ * UNSUPPORTED: cols % 64 != 0, r > 64, or a launch of 2^32 work-items. */
+loftq_status_t loftq_qlora_forward_dropout(const void* X, int64_t n_tok, int64_t rows, int64_t cols,
+                                           const uint8_t* packed, const float* absmax, const int8_t* qabsmax,
+                                           const float* dq_scale, int32_t bits, const float* B, const float* A,
+                                           int32_t r, float alpha, const loftq_dropout_t* drop, void* Y,
+                                           loftq_dtype_t ydt, void* ws, size_t ws_bytes, void* stream);
+size_t loftq_qlora_forward_dropout_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t r);
+
+/* Its gradient, with G = dY and the forward's drop:
+ *   dX = G bf16(deq(Q)) + alpha s keep((G bf16(B)) bf16(A))
+ *   dB = alpha s G^T (keep(X) bf16(A)^T)
+ *   dA = alpha s (G bf16(B))^T keep(X)
+ * keep() drops the elements that the forward dropped from X.  Sums are in fp32; the n_tok x r
+ * products between them are kept to 24 bits.  The outputs are overwritten, not added to.
+ *   dY      [device] n_tok x rows bf16
+ *   X       [device] n_tok x cols bf16, the forward's input; may be NULL without dB and dA
+ *   dX      [device] n_tok x cols of dtype xdt out, or NULL
+ *   dB, dA  [device] fp32 rows x r and r x cols out, or both NULL (always without B and A)
+ *   ws      [device] loftq_qlora_backward_workspace_bytes(n_tok, rows, cols, r) bytes
+ * n_tok = 0 writes zeros to dB and dA.  UNSUPPORTED as the forward, and rows = 0. */
+loftq_status_t loftq_qlora_backward(const void* dY, const void* X, int64_t n_tok, int64_t rows, int64_t cols,
+                                    const uint8_t* packed, const float* absmax, const int8_t* qabsmax,
+                                    const float* dq_scale, int32_t bits, const float* B, const float* A, int32_t r,
+                                    float alpha, const loftq_dropout_t* drop, void* dX, loftq_dtype_t xdt, float* dB,
+                                    float* dA, void* ws, size_t ws_bytes, void* stream);
+size_t loftq_qlora_backward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t r);
+
+/* MXFP4 (OCP Microscaling Formats v1.0): FP4 e2m1 values (0, .5, 1, 1.5, 2, 3, 4, 6 and
+ * their negatives) that share one power of two per 32 consecutive columns of a row (the
+ * row's last block may be shorter).  Scale byte of a block whose largest magnitude is a:
+ * max(0, floor(log2 a) - 2 + 127), 0 for a = 0, the scale being 2^(byte - 127); code: x /
+ * scale to the nearest value, ties to the even code, magnitudes past 6 to 6.  A block that
+ * holds an infinity or a NaN gets byte 255 and reads back as NaN.
+ *   packed  [device] loftq_mxfp4_packed_bytes(rows, cols) bytes: row after row, each padded with
+ *           zeros to whole steps of 256 columns (128 bytes); element 2i in the high nibble, code
+ *           = 8 for negative + the magnitude's index above
+ *   scales  [device] loftq_mxfp4_scale_bytes(rows, cols) bytes: step after step, 8 bytes per row,
+ *           so that block j of row i is at ((j / 8) rows + i) 8 + j % 8 */
+size_t loftq_mxfp4_packed_bytes(int64_t rows, int64_t cols);
+size_t loftq_mxfp4_scale_bytes(int64_t rows, int64_t cols);
+
+/* Quantization of R = W - B A (B, A both NULL: R = W) to MXFP4, the counterpart of
+ * loftq_nf4_quantize for LoftQ over this format; R is formed in fp32, its r products added
+ * in the order of the rank.  Any rows and cols; W, B, A, r as there. */
+loftq_status_t loftq_mxfp4_quantize(const void* W, loftq_dtype_t wdt, int64_t rows, int64_t cols, const float* B,
+                                    const float* A, int32_t r, uint8_t* packed, uint8_t* scales, void* stream);
+
+/* out = deq (W == NULL) or W - deq, formed in fp32 and rounded to odt.
+ *   W    [device] rows x cols of dtype wdt, or NULL
+ *   out  [device] rows x cols of dtype odt out; may be W where the types are the same */
+loftq_status_t loftq_mxfp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t rows, int64_t cols,
+                                      const void* W, loftq_dtype_t wdt, void* out, loftq_dtype_t odt, void* stream);
+
+/* Forward of an adapted layer over an MXFP4 base, multiplied in that format:
+ *   Y = MX(X) deq(Q)^T + alpha s (keep(X) bf16(A)^T) bf16(B)^T
+ * MX(X) is X quantized by rows as in loftq_mxfp4_quantize, for one token as for many; the
+ * adapter reads X itself.
+ * Products accumulate in fp32.  drop, Y, ydt as loftq_qlora_forward_dropout (serving: NULL).
+ *   X       [device] n_tok x cols bf16
+ *   ws      [device] loftq_mxfp4_forward_workspace_bytes(n_tok, rows, cols, r) bytes
+ * UNSUPPORTED: cols % 32 != 0, r > 64, or a launch of 2^32 work-items. */
+loftq_status_t loftq_mxfp4_forward(const void* X, int64_t n_tok, int64_t rows, int64_t cols, const uint8_t* packed,
+                                   const uint8_t* scales, const float* B, const float* A, int32_t r, float alpha,
+                                   const loftq_dropout_t* drop, void* Y, loftq_dtype_t ydt, void* ws, size_t ws_bytes,
+                                   void* stream);
+size_t loftq_mxfp4_forward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t r);
+
+/* Its gradient: loftq_qlora_backward over the MXFP4 weight's bf16 values (the rounding of X
+ * passes the gradient as it is).  UNSUPPORTED as the forward, and rows = 0. */
+loftq_status_t loftq_mxfp4_backward(const void* dY, const void* X, int64_t n_tok, int64_t rows, int64_t cols,
+                                    const uint8_t* packed, const uint8_t* scales, const float* B, const float* A,
+                                    int32_t r, float alpha, const loftq_dropout_t* drop, void* dX, loftq_dtype_t xdt,
+                                    float* dB, float* dA, void* ws, size_t ws_bytes, void* stream);
+size_t loftq_mxfp4_backward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t r);
 
 /* Low-rank step ("LoftQ...", §2.3: best rank-r approximation of W - Q from its
  * r largest singular triplets, Delta = U_r S_r V_r^T).  exact = 1: the SVD of E

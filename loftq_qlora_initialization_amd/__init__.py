@@ -15,6 +15,9 @@ _BINDING_NAMES = {
     "default_config", "nf4_codebook", "nf_codebook", "exported_symbols", "workspace_bytes", "lowrank_workspace_bytes",
     "InitBuffers", "LoftqConfig", "LoftqError", "LIB_PATH", "EXPORTS", "profile_enable", "profile_collect", "profile_calibrate",
     "loftq_init_batch", "BatchRunner", "LoftqMatrix", "loftq_qlora_forward_noalloc", "qlora_forward_noalloc_max_bytes",
+    "loftq_dropout", "loftq_qlora_forward_dropout", "loftq_qlora_backward", "loftq_mxfp4_quantize", "loftq_mxfp4_dequantize",
+    "loftq_mxfp4_forward", "loftq_mxfp4_backward", "LoftqDropout", "qlora_forward_dropout_workspace_bytes",
+    "qlora_backward_workspace_bytes", "mxfp4_forward_workspace_bytes", "mxfp4_backward_workspace_bytes",
 }
 
 

@@ -8,7 +8,8 @@ built library raises ImportError: there is no CPU fallback.
 The functions carry the C entry points' names (see include/loftq.h):
     loftq_nf4_quantize, loftq_double_quant, loftq_nf4_dequantize,
     loftq_nf4_merge, loftq_nf4_unmerge, loftq_lowrank_svd, loftq_init,
-    loftq_qlora_forward
+    loftq_qlora_forward, loftq_dropout, loftq_qlora_forward_dropout, loftq_qlora_backward,
+    loftq_mxfp4_quantize, loftq_mxfp4_dequantize, loftq_mxfp4_forward, loftq_mxfp4_backward
 and return freshly allocated torch tensors on the input's device (or fill the
 caller's ``out`` / ``buffers`` where those are given).
 """
@@ -37,7 +38,11 @@ EXPORTS = ["loftq_init_batch", "loftq_batch_workspace_bytes", "loftq_nf4_quantiz
            "loftq_lowrank_svd_workspace_bytes", "loftq_init", "loftq_workspace_bytes", "loftq_default_config",
            "loftq_status_string", "loftq_nf4_codebook", "loftq_nf_codebook", "loftq_qlora_forward",
            "loftq_qlora_forward_workspace_bytes", "loftq_qlora_forward_noalloc", "loftq_qlora_forward_noalloc_max_bytes",
-           "loftq_profile_enable", "loftq_profile_collect", "loftq_profile_calibrate"]
+           "loftq_profile_enable", "loftq_profile_collect", "loftq_profile_calibrate",
+           "loftq_dropout", "loftq_qlora_forward_dropout", "loftq_qlora_forward_dropout_workspace_bytes",
+           "loftq_qlora_backward", "loftq_qlora_backward_workspace_bytes", "loftq_mxfp4_packed_bytes",
+           "loftq_mxfp4_scale_bytes", "loftq_mxfp4_quantize", "loftq_mxfp4_dequantize", "loftq_mxfp4_forward",
+           "loftq_mxfp4_forward_workspace_bytes", "loftq_mxfp4_backward", "loftq_mxfp4_backward_workspace_bytes"]
 
 
 class LoftqConfig(ctypes.Structure):
@@ -54,6 +59,10 @@ _P, _I64, _I32, _U64, _SZ = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, cty
 class LoftqMatrix(ctypes.Structure):
     _fields_ = [("W", _P), ("rows", _I64), ("cols", _I64), ("packed", _P), ("absmax", _P), ("qabsmax", _P),
                 ("dq_scale", _P), ("B", _P), ("A", _P), ("objective", _P), ("sigma", _P)]
+
+
+class LoftqDropout(ctypes.Structure):
+    _fields_ = [("p", ctypes.c_float), ("seed", _U64), ("offset", _U64), ("step", _P)]
 
 
 def _sig(name, res, args):
@@ -77,6 +86,29 @@ _c_fwd_ws = _sig("loftq_qlora_forward_workspace_bytes", _SZ, [_I64, _I32])
 _c_fwd_na = _sig("loftq_qlora_forward_noalloc", ctypes.c_int,
                  [_P, _I64, _I64, _I64, _P, _P, _P, _P, _I32, _P, _P, _I32, ctypes.c_float, _P, _P])
 _c_fwd_na_max = _sig("loftq_qlora_forward_noalloc_max_bytes", _SZ, [])
+_DROP = ctypes.POINTER(LoftqDropout)
+_NF_ARGS = [_P, _P, _P, _P, _I32]                       # packed, absmax, qabsmax, dq_scale, bits
+_MX_ARGS = [_P, _P]                                     # packed, scales
+_ADAPTER_ARGS = [_P, _P, _I32, ctypes.c_float, _DROP]   # B, A, r, alpha, drop
+_FWD_OUT = [_P, ctypes.c_int, _P, _SZ, _P]
+_BWD_OUT = [_P, ctypes.c_int, _P, _P, _P, _SZ, _P]
+_c_dropout = _sig("loftq_dropout", ctypes.c_int, [_P, ctypes.c_int, _I64, _DROP, _P, _P])
+_c_fwd_drop = _sig("loftq_qlora_forward_dropout", ctypes.c_int,
+                   [_P, _I64, _I64, _I64] + _NF_ARGS + _ADAPTER_ARGS + _FWD_OUT)
+_c_bwd = _sig("loftq_qlora_backward", ctypes.c_int, [_P, _P, _I64, _I64, _I64] + _NF_ARGS + _ADAPTER_ARGS + _BWD_OUT)
+_c_mx_fwd = _sig("loftq_mxfp4_forward", ctypes.c_int, [_P, _I64, _I64, _I64] + _MX_ARGS + _ADAPTER_ARGS + _FWD_OUT)
+_c_mx_bwd = _sig("loftq_mxfp4_backward", ctypes.c_int,
+                 [_P, _P, _I64, _I64, _I64] + _MX_ARGS + _ADAPTER_ARGS + _BWD_OUT)
+_LAYER_WS = [_I64, _I64, _I64, _I32]
+_c_fwd_drop_ws = _sig("loftq_qlora_forward_dropout_workspace_bytes", _SZ, _LAYER_WS)
+_c_bwd_ws = _sig("loftq_qlora_backward_workspace_bytes", _SZ, _LAYER_WS)
+_c_mx_fwd_ws = _sig("loftq_mxfp4_forward_workspace_bytes", _SZ, _LAYER_WS)
+_c_mx_bwd_ws = _sig("loftq_mxfp4_backward_workspace_bytes", _SZ, _LAYER_WS)
+_c_mx_packed = _sig("loftq_mxfp4_packed_bytes", _SZ, [_I64, _I64])
+_c_mx_scales = _sig("loftq_mxfp4_scale_bytes", _SZ, [_I64, _I64])
+_c_mx_quant = _sig("loftq_mxfp4_quantize", ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _P, _P, _I32, _P, _P, _P])
+_c_mx_deq = _sig("loftq_mxfp4_dequantize", ctypes.c_int,
+                 [_P, _P, _I64, _I64, _P, ctypes.c_int, _P, ctypes.c_int, _P])
 _c_svd = _sig("loftq_lowrank_svd", ctypes.c_int,
               [_P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _U64, _I32, _P, _P, _P, _P, _SZ, _P])
 _c_svd_ws = _sig("loftq_lowrank_svd_workspace_bytes", _SZ, [_I64, _I64, _I32, _I32, _I32])
@@ -300,6 +332,257 @@ def loftq_qlora_forward_noalloc(X: torch.Tensor, packed: torch.Tensor, shape, ab
            _c_fwd_na(_ptr(X), n_tok, rows, cols, _ptr(packed), _ptr(absmax), _ptr(qabsmax), _ptr(dq_scale),
                      int(bits), _ptr(B), _ptr(A), r, float(alpha), _ptr(out), _stream(stream)))
     return out
+
+
+# ---- training and serving an adapted layer ----
+
+def _dropout(p, seed, offset, step, X):
+    if step is not None:
+        _expect(step, "step", X, torch.int64, (1,))
+    return LoftqDropout(float(p), int(seed) & (2 ** 64 - 1), int(offset) & (2 ** 64 - 1),
+                        None if step is None else step.data_ptr())
+
+
+def _expect(t, what, like, dtype, shape=None, least=None):
+    """A contiguous tensor of the given type on `like`'s device, of a shape or of at least so many elements."""
+    _contig(t, what)
+    if t.device != like.device:
+        raise ValueError(f"{what} must be on {like.device}")
+    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+        raise TypeError(f"{what} must be {dtype}")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{what} must have the shape {tuple(shape)}")
+    if least is not None and t.numel() < least:
+        raise ValueError(f"{what} must hold {least} elements")
+    return t
+
+
+def _on(X, stream):
+    """The tensor's device for a call and its stream there (the device's current one by default)."""
+    return torch.cuda.device(X.device), _stream(torch.cuda.current_stream(X.device) if stream is None else stream)
+
+
+def _out_dtype(t, dtype):
+    dtype = t.dtype if t is not None else dtype
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("outputs are float32 or bfloat16")
+    return dtype
+
+
+def _nf_args(X, packed, rows, cols, absmax, qabsmax, dq_scale, bits):
+    nb = (rows * cols + 63) // 64
+    _expect(packed, "packed", X, torch.uint8, least=(rows * cols + 1) // 2)
+    if qabsmax is not None or dq_scale is not None:
+        if qabsmax is None or dq_scale is None:
+            raise ValueError("qabsmax and dq_scale are given together")
+        _expect(qabsmax, "qabsmax", X, torch.int8, least=nb)
+        _expect(dq_scale, "dq_scale", X, torch.float32, least=(nb + 255) // 256)
+    elif absmax is None:
+        raise ValueError("absmax, or qabsmax and dq_scale, must be given")
+    else:
+        _expect(absmax, "absmax", X, torch.float32, least=nb)
+    return [_ptr(packed), _ptr(absmax), _ptr(qabsmax), _ptr(dq_scale), int(bits)]
+
+
+def _mx_args(X, packed, scales, rows, cols):
+    _expect(packed, "packed", X, torch.uint8, least=_c_mx_packed(rows, cols))
+    _expect(scales, "scales", X, torch.uint8, least=_c_mx_scales(rows, cols))
+    return [_ptr(packed), _ptr(scales)]
+
+
+def _adapter_args(X, B, A, rows, cols, alpha, drop):
+    if (B is None) != (A is None):
+        raise ValueError("B and A are given together")
+    r = 0
+    if B is not None:
+        r = B.shape[1] if B.dim() == 2 else -1
+        _expect(B, "B", X, torch.float32, (rows, r))
+        _expect(A, "A", X, torch.float32, (r, cols))
+    return r, [_ptr(B), _ptr(A), r, float(alpha), ctypes.byref(drop)]
+
+
+def _workspace(ws, need, X):
+    if ws is None:
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
+    _contig(ws, "ws")
+    if ws.device != X.device:
+        raise ValueError(f"ws must be on {X.device}")
+    return ws, ws.numel() * ws.element_size()
+
+
+def _layer_forward(name, c_fn, c_ws, X, base, rows, cols, B, A, alpha, drop, out, out_dtype, ws, stream):
+    n = X.shape[0]
+    out_dtype = _out_dtype(out, out_dtype)
+    r, adapter = _adapter_args(X, B, A, rows, cols, alpha, drop)
+    if out is None:
+        out = torch.empty((n, rows), dtype=out_dtype, device=X.device)
+    _expect(out, "out", X, out_dtype, (n, rows))
+    ws, ws_bytes = _workspace(ws, int(c_ws(n, rows, cols, r)), X)
+    device, st = _on(X, stream)
+    with device:
+        _check(name, c_fn(_ptr(X), n, rows, cols, *base, *adapter, _ptr(out), _wdtype(out), _ptr(ws), ws_bytes, st))
+    return out
+
+
+def _layer_backward(name, c_fn, c_ws, dY, X, base, rows, cols, B, A, alpha, drop, need_dx, out, dx_dtype, ws, stream):
+    n = dY.shape[0]
+    r, adapter = _adapter_args(dY, B, A, rows, cols, alpha, drop)
+    dX, dB, dA = out if out is not None else (None, None, None)
+    if out is None:
+        if need_dx:
+            dX = torch.empty((n, cols), dtype=_out_dtype(None, dx_dtype), device=dY.device)
+        if B is not None:
+            dB, dA = torch.empty_like(B), torch.empty_like(A)
+    if X is None and dB is not None:
+        raise ValueError("X must be given for dB and dA")
+    if X is not None:
+        _expect(X, "X", dY, torch.bfloat16, (n, cols))
+    if dX is not None:
+        _expect(dX, "dX", dY, (torch.float32, torch.bfloat16), (n, cols))
+    if dB is not None:
+        _expect(dB, "dB", dY, torch.float32, (rows, r))
+    if dA is not None:
+        _expect(dA, "dA", dY, torch.float32, (r, cols))
+    ws, ws_bytes = _workspace(ws, int(c_ws(n, rows, cols, r)), dY)
+    device, st = _on(dY, stream)
+    with device:
+        _check(name, c_fn(_ptr(dY), _ptr(X), n, rows, cols, *base, *adapter, _ptr(dX),
+                          _wdtype(dX) if dX is not None else LOFTQ_BF16, _ptr(dB), _ptr(dA), _ptr(ws), ws_bytes, st))
+    return dX, dB, dA
+
+
+def _tokens(X, what, width):
+    _contig(X, what)
+    if X.dtype != torch.bfloat16:
+        raise TypeError(f"{what} must be bfloat16")
+    if X.dim() != 2 or X.shape[1] != width:
+        raise ValueError(f"{what} must have {width} columns")
+    return X
+
+
+def loftq_dropout(X: torch.Tensor, p: float, seed: int, offset: int = 0, step: Optional[torch.Tensor] = None,
+                  out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """X / (1 - p) where the mask of (p, seed, offset + step) keeps, else 0; the gradient is the same call
+    on dY.  `step` is a one-element int64 device tensor that is read when the kernel runs.  `out` may be X."""
+    _contig(X, "X")
+    if out is None:
+        out = torch.empty_like(X)
+    _expect(out, "out", X, X.dtype, X.shape)
+    drop = _dropout(p, seed, offset, step, X)
+    device, st = _on(X, stream)
+    with device:
+        _check("loftq_dropout", _c_dropout(_ptr(X), _wdtype(X), X.numel(), ctypes.byref(drop), _ptr(out), st))
+    return out
+
+
+def qlora_forward_dropout_workspace_bytes(n_tok: int, rows: int, cols: int, r: int) -> int:
+    return int(_c_fwd_drop_ws(n_tok, rows, cols, r))
+
+
+def qlora_backward_workspace_bytes(n_tok: int, rows: int, cols: int, r: int) -> int:
+    return int(_c_bwd_ws(n_tok, rows, cols, r))
+
+
+def mxfp4_forward_workspace_bytes(n_tok: int, rows: int, cols: int, r: int) -> int:
+    return int(_c_mx_fwd_ws(n_tok, rows, cols, r))
+
+
+def mxfp4_backward_workspace_bytes(n_tok: int, rows: int, cols: int, r: int) -> int:
+    return int(_c_mx_bwd_ws(n_tok, rows, cols, r))
+
+
+def loftq_qlora_forward_dropout(X: torch.Tensor, packed: torch.Tensor, shape, absmax: Optional[torch.Tensor] = None,
+                                qabsmax: Optional[torch.Tensor] = None, dq_scale: Optional[torch.Tensor] = None,
+                                B: Optional[torch.Tensor] = None, A: Optional[torch.Tensor] = None,
+                                alpha: float = 1.0, p: float = 0.0, seed: int = 0, offset: int = 0,
+                                step: Optional[torch.Tensor] = None, bits: int = 4,
+                                out: Optional[torch.Tensor] = None, out_dtype=torch.float32,
+                                ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = X bf16(deq(Q))^T + alpha / (1 - p) (keep(X) bf16(A)^T) bf16(B)^T for bf16 X (n_tok x cols)."""
+    rows, cols = shape
+    _tokens(X, "X", cols)
+    return _layer_forward("loftq_qlora_forward_dropout", _c_fwd_drop, _c_fwd_drop_ws, X,
+                          _nf_args(X, packed, rows, cols, absmax, qabsmax, dq_scale, bits), rows, cols, B, A, alpha,
+                          _dropout(p, seed, offset, step, X), out, out_dtype, ws, stream)
+
+
+def loftq_qlora_backward(dY: torch.Tensor, X: Optional[torch.Tensor], packed: torch.Tensor, shape,
+                         absmax: Optional[torch.Tensor] = None, qabsmax: Optional[torch.Tensor] = None,
+                         dq_scale: Optional[torch.Tensor] = None, B: Optional[torch.Tensor] = None,
+                         A: Optional[torch.Tensor] = None, alpha: float = 1.0, p: float = 0.0, seed: int = 0,
+                         offset: int = 0, step: Optional[torch.Tensor] = None, bits: int = 4, need_dx: bool = True,
+                         out=None, dx_dtype=torch.bfloat16, ws: Optional[torch.Tensor] = None, stream=None):
+    """(dX, dB, dA) of loftq_qlora_forward_dropout for bf16 dY (n_tok x rows) and the forward's X and mask.
+    `out`: the three tensors to fill, None for one that is not wanted (dB and dA both or neither)."""
+    rows, cols = shape
+    _tokens(dY, "dY", rows)
+    return _layer_backward("loftq_qlora_backward", _c_bwd, _c_bwd_ws, dY, X,
+                           _nf_args(dY, packed, rows, cols, absmax, qabsmax, dq_scale, bits), rows, cols, B, A, alpha,
+                           _dropout(p, seed, offset, step, dY), need_dx, out, dx_dtype, ws, stream)
+
+
+def loftq_mxfp4_quantize(W: torch.Tensor, B: Optional[torch.Tensor] = None, A: Optional[torch.Tensor] = None,
+                         packed: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
+    """W - B A (or W) in MXFP4: codes (rows x 128-byte steps of 256 columns) and scales (steps x rows x 8)."""
+    _contig(W, "W")
+    if W.dim() != 2:
+        raise ValueError("W must be a matrix")
+    rows, cols = W.shape
+    steps = (cols + 255) // 256
+    r, adapter = _adapter_args(W, B, A, rows, cols, 1.0, LoftqDropout())
+    if packed is None:
+        packed = torch.empty((rows, steps * 128), dtype=torch.uint8, device=W.device)
+    if scales is None:
+        scales = torch.empty((steps, rows, 8), dtype=torch.uint8, device=W.device)
+    base = _mx_args(W, packed, scales, rows, cols)
+    device, st = _on(W, stream)
+    with device:
+        _check("loftq_mxfp4_quantize", _c_mx_quant(_ptr(W), _wdtype(W), rows, cols, *adapter[:3], *base, st))
+    return packed, scales
+
+
+def loftq_mxfp4_dequantize(packed: torch.Tensor, scales: torch.Tensor, shape, W: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None, out_dtype=torch.float32, stream=None) -> torch.Tensor:
+    """deq(Q), or W - deq(Q) when W is given; formed in fp32 and rounded to out_dtype."""
+    rows, cols = shape
+    base = _mx_args(packed, packed, scales, rows, cols)
+    if W is not None:
+        _expect(W, "W", packed, (torch.float32, torch.bfloat16), (rows, cols))
+    out_dtype = _out_dtype(out, out_dtype)
+    if out is None:
+        out = torch.empty((rows, cols), dtype=out_dtype, device=packed.device)
+    _expect(out, "out", packed, out_dtype, (rows, cols))
+    device, st = _on(packed, stream)
+    with device:
+        _check("loftq_mxfp4_dequantize", _c_mx_deq(*base, rows, cols, _ptr(W), _wdtype(W) if W is not None else
+                                                   LOFTQ_F32, _ptr(out), _wdtype(out), st))
+    return out
+
+
+def loftq_mxfp4_forward(X: torch.Tensor, packed: torch.Tensor, scales: torch.Tensor, shape,
+                        B: Optional[torch.Tensor] = None, A: Optional[torch.Tensor] = None, alpha: float = 1.0,
+                        p: float = 0.0, seed: int = 0, offset: int = 0, step: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, out_dtype=torch.float32,
+                        ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """Y = MX(X) deq(Q)^T + alpha / (1 - p) (keep(X) bf16(A)^T) bf16(B)^T for bf16 X (n_tok x cols)."""
+    rows, cols = shape
+    _tokens(X, "X", cols)
+    return _layer_forward("loftq_mxfp4_forward", _c_mx_fwd, _c_mx_fwd_ws, X, _mx_args(X, packed, scales, rows, cols),
+                          rows, cols, B, A, alpha, _dropout(p, seed, offset, step, X), out, out_dtype, ws, stream)
+
+
+def loftq_mxfp4_backward(dY: torch.Tensor, X: Optional[torch.Tensor], packed: torch.Tensor, scales: torch.Tensor,
+                         shape, B: Optional[torch.Tensor] = None, A: Optional[torch.Tensor] = None,
+                         alpha: float = 1.0, p: float = 0.0, seed: int = 0, offset: int = 0,
+                         step: Optional[torch.Tensor] = None, need_dx: bool = True, out=None,
+                         dx_dtype=torch.bfloat16, ws: Optional[torch.Tensor] = None, stream=None):
+    """(dX, dB, dA) of loftq_mxfp4_forward, the rounding of X passing the gradient as it is; `out` as in
+    loftq_qlora_backward."""
+    rows, cols = shape
+    _tokens(dY, "dY", rows)
+    return _layer_backward("loftq_mxfp4_backward", _c_mx_bwd, _c_mx_bwd_ws, dY, X,
+                           _mx_args(dY, packed, scales, rows, cols), rows, cols, B, A, alpha,
+                           _dropout(p, seed, offset, step, dY), need_dx, out, dx_dtype, ws, stream)
 
 
 def lowrank_workspace_bytes(rows: int, cols: int, r: int, oversample: int, exact: bool) -> int:

@@ -1,0 +1,387 @@
+// C-ABI entry points of the adapted layer's training and serving path (dropout, MXFP4, the
+// training forward, the gradient): argument validation, workspace layout, then launches.
+#include <cmath>
+
+#include "layer.h"
+
+using namespace loftq;
+
+namespace {
+
+typedef int64_t i64;
+
+// Consecutive 256-byte aligned pieces of a workspace; with a null base it only counts.
+struct Arena {
+  char* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(i64 count) {
+    T* p = base != nullptr ? reinterpret_cast<T*>(base + used) : nullptr;
+    used += (static_cast<size_t>(count) * sizeof(T) + 255) / 256 * 256;
+    return p;
+  }
+};
+
+int rank_pad(int r) { return (r + 15) / 16 * 16; }
+i64 pad_to(i64 n, i64 m) { return (n + m - 1) / m * m; }
+
+struct ForwardSpace {
+  __bf16* W;        // NormalFloat base: bf16(deq)
+  uint8_t* xq;      // MXFP4 base: the activations' codes and scales
+  uint8_t* xs;
+  __bf16 *Ab, *Bb, *S;
+  float* partials;
+  int ks;
+  size_t bytes;
+};
+
+ForwardSpace forward_space(void* ws, i64 n, i64 rows, i64 cols, int r, bool mx) {
+  Arena a{static_cast<char*>(ws)};
+  ForwardSpace f{};
+  if (mx) {
+    f.xq = a.take<uint8_t>(n * mx_steps(cols) * (kMxStep / 2));
+    f.xs = a.take<uint8_t>(n * mx_steps(cols) * 8);
+  } else {
+    f.W = a.take<__bf16>(rows * cols);
+  }
+  if (r > 0) {
+    const int rp = rank_pad(r);
+    f.ks = down_splits(n, cols);
+    f.Ab = a.take<__bf16>(rp * cols);
+    f.Bb = a.take<__bf16>(rows * rp);
+    f.S = a.take<__bf16>(n * 3 * rp);
+    f.partials = a.take<float>(static_cast<i64>(f.ks) * n * rp);
+  }
+  f.bytes = a.used;
+  return f;
+}
+
+struct BackwardSpace {
+  __bf16 *G, *Wt, *Ab, *At, *Bt, *Ht, *Pt, *Ps;
+  float* partials;   // of one thin product at a time
+  int ks_h, ks_p, ts_b, ts_a;
+  size_t bytes;
+};
+
+BackwardSpace backward_space(void* ws, i64 n, i64 rows, i64 cols, int r) {
+  Arena a{static_cast<char*>(ws)};
+  BackwardSpace f{};
+  const i64 rows_pad = pad_to(rows, 64), n_pad = pad_to(n, 32);
+  if (rows_pad != rows) f.G = a.take<__bf16>(n * rows_pad);
+  f.Wt = a.take<__bf16>(cols * rows_pad);
+  if (r > 0) {
+    const int rp = rank_pad(r);
+    f.ks_h = down_splits(n, cols);
+    f.ks_p = down_splits(n, rows_pad);
+    f.ts_b = grad_splits(n, rows_pad);
+    f.ts_a = grad_splits(n, cols);
+    f.Ab = a.take<__bf16>(rp * cols);
+    f.At = a.take<__bf16>(cols * rp);
+    f.Bt = a.take<__bf16>(rp * rows_pad);
+    f.Ht = a.take<__bf16>(3 * rp * n_pad);
+    f.Pt = a.take<__bf16>(3 * rp * n_pad);
+    f.Ps = a.take<__bf16>(n * 3 * rp);
+    i64 most = static_cast<i64>(f.ks_h > f.ks_p ? f.ks_h : f.ks_p) * n;
+    if (f.ts_b * rows_pad > most) most = f.ts_b * rows_pad;
+    if (f.ts_a * cols > most) most = f.ts_a * cols;
+    f.partials = a.take<float>(most * rp);
+  }
+  f.bytes = a.used;
+  return f;
+}
+
+// Every launch of a call stays below 2^32 work-items.
+bool layer_shape_ok(i64 n, i64 rows, i64 cols, int r) {
+  const i64 limit = (i64(1) << 32) - 1024, rp = rank_pad(r), rows_pad = pad_to(rows, 64), n_pad = pad_to(n, 64);
+  return tile_product_shape_ok(n, rows) && tile_product_shape_ok(n, cols) && n_pad * 64 < limit &&
+         rows_pad * (cols / 8 + 8) < limit && n * (rows_pad / 8) < limit && n * mx_steps(cols) * 32 < limit &&
+         rp * 2 * (cols + rows_pad) < limit && (rows_pad + cols) * 32 < limit;
+}
+
+bool drop_ok(const loftq_dropout_t* d) {
+  return d == nullptr || (std::isfinite(d->p) && d->p >= 0.f && d->p <= 1.f &&
+                          (reinterpret_cast<uintptr_t>(d->step) & 7u) == 0);
+}
+
+DropArg drop_arg(const loftq_dropout_t* d) {
+  if (d == nullptr) return DropArg{0, 0, nullptr, 0, 1.f};
+  const uint32_t thr = static_cast<uint32_t>(static_cast<double>(d->p) * 65536.0 + 0.5);
+  const float scale = thr >= 65536u ? 0.f : static_cast<float>(65536.0 / (65536.0 - thr));
+  return DropArg{d->seed, d->offset, d->step, thr, scale};
+}
+
+bool dtype_ok(loftq_dtype_t t) { return t == LOFTQ_F32 || t == LOFTQ_BF16; }
+
+// What the training calls share: sizes, the base, the adapter, the dropout.
+loftq_status_t check_layer(i64 n, i64 rows, i64 cols, const Base4& b, bool mx, const float* B, const float* A, int r,
+                           float alpha, const loftq_dropout_t* drop) {
+  if (!shape_ok(rows, cols) || n < 0 || n >= (i64(1) << 31)) return LOFTQ_ERR_INVALID_ARG;
+  if (!mx) {
+    if (b.bits != 2 && b.bits != 3 && b.bits != 4) return LOFTQ_ERR_UNSUPPORTED;
+    if (!nf_tables(b.bits).valid) return LOFTQ_ERR_UNSUPPORTED;
+    if ((b.qabsmax == nullptr) != (b.dq_scale == nullptr)) return LOFTQ_ERR_INVALID_ARG;
+  }
+  if ((B == nullptr) != (A == nullptr)) return LOFTQ_ERR_INVALID_ARG;
+  if (B != nullptr && r < 1) return LOFTQ_ERR_INVALID_ARG;
+  if (!std::isfinite(alpha) || !drop_ok(drop)) return LOFTQ_ERR_INVALID_ARG;
+  return LOFTQ_OK;
+}
+
+loftq_status_t check_layer_buffers(i64 n, i64 rows, i64 cols, const Base4& b, bool mx, const float* B, const float* A,
+                                   int r) {
+  if (cols == 0 || cols % (mx ? kMxBlock : 64) != 0 || (B != nullptr && r > 64)) return LOFTQ_ERR_UNSUPPORTED;
+  if (!layer_shape_ok(n, rows, cols, B ? r : 0)) return LOFTQ_ERR_UNSUPPORTED;
+  if (!b.packed || !aligned16(b.packed)) return LOFTQ_ERR_INVALID_ARG;
+  if (mx) {
+    if (!b.mx || !aligned16(b.mx)) return LOFTQ_ERR_INVALID_ARG;
+  } else if (b.qabsmax != nullptr) {
+    if (!aligned16(b.qabsmax) || !aligned16(b.dq_scale)) return LOFTQ_ERR_INVALID_ARG;
+  } else if (!b.absmax || !aligned16(b.absmax)) {
+    return LOFTQ_ERR_INVALID_ARG;
+  }
+  if (B && (!aligned16(B) || !aligned16(A))) return LOFTQ_ERR_INVALID_ARG;
+  return LOFTQ_OK;
+}
+
+#define LQ_TRY(call)                                  \
+  do {                                                \
+    const hipError_t lq_e_ = (call);                  \
+    if (lq_e_ != hipSuccess) return LOFTQ_ERR_HIP;    \
+  } while (0)
+
+loftq_status_t layer_forward(const void* X, i64 n, i64 rows, i64 cols, const Base4& base, bool mx, const float* B,
+                             const float* A, int r, float alpha, const loftq_dropout_t* drop, void* Y,
+                             loftq_dtype_t ydt, void* ws, size_t ws_bytes, hipStream_t s) {
+  loftq_status_t st = check_layer(n, rows, cols, base, mx, B, A, r, alpha, drop);
+  if (st != LOFTQ_OK) return st;
+  if (!dtype_ok(ydt)) return LOFTQ_ERR_INVALID_ARG;
+  if (n == 0 || rows == 0) return LOFTQ_OK;   // nothing to write
+  st = check_layer_buffers(n, rows, cols, base, mx, B, A, r);
+  if (st != LOFTQ_OK) return st;
+  if (!X || !Y || !ws || !aligned16(X) || !aligned16(Y) || !aligned16(ws)) return LOFTQ_ERR_INVALID_ARG;
+  if (B == nullptr) r = 0;
+  const ForwardSpace f = forward_space(ws, n, rows, cols, r, mx);
+  if (ws_bytes < f.bytes) return LOFTQ_ERR_WORKSPACE;
+  const __bf16* Xb = static_cast<const __bf16*>(X);
+  const DropArg d = drop_arg(drop);
+  const int rp = rank_pad(r);
+  if (r > 0) {
+    LQ_TRY(launch_adapter_operands(AdapterOperands{A, B, r, rp, rows, cols, rows, f.Ab, nullptr, f.Bb, nullptr}, s));
+    LQ_TRY(launch_down(Xb, n, cols, f.Ab, rp, f.ks, d, f.partials, s));
+    LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks, f.S, nullptr, n, s));
+  }
+  TileProduct t{};
+  t.M = n;
+  t.N = rows;
+  if (mx) {
+    LQ_TRY(launch_mx_quantize(Xb, LOFTQ_BF16, n, cols, nullptr, nullptr, 0, f.xq, f.xs, s));
+    t.W = base.packed;
+    t.X = f.xq;
+    t.steps = static_cast<int>(mx_steps(cols));
+    t.ldw = t.ldx = t.steps * i64(kMxStep / 2);
+    t.wscale = base.mx;
+    t.xscale = f.xs;
+  } else {
+    LQ_TRY(launch_base_bf16(base, rows, cols, f.W, s));
+    t.W = f.W;
+    t.X = Xb;
+    t.steps = static_cast<int>(cols / 64);
+    t.ldw = t.ldx = cols * 2;
+  }
+  if (r > 0) {
+    t.V = f.Bb;
+    t.S = f.S;
+    t.rp = rp;
+    t.gain = alpha * d.scale;
+  }
+  t.out = Y;
+  t.odt = ydt;
+  return from_hip(launch_tile_product(t, mx, s));
+}
+
+loftq_status_t layer_backward(const void* dY, const void* X, i64 n, i64 rows, i64 cols, const Base4& base, bool mx,
+                              const float* B, const float* A, int r, float alpha, const loftq_dropout_t* drop,
+                              void* dX, loftq_dtype_t xdt, float* dB, float* dA, void* ws, size_t ws_bytes,
+                              hipStream_t s) {
+  loftq_status_t st = check_layer(n, rows, cols, base, mx, B, A, r, alpha, drop);
+  if (st != LOFTQ_OK) return st;
+  if (dX && !dtype_ok(xdt)) return LOFTQ_ERR_INVALID_ARG;
+  if ((dB == nullptr) != (dA == nullptr) || (dB && !B)) return LOFTQ_ERR_INVALID_ARG;
+  if (!dX && !dB) return LOFTQ_ERR_INVALID_ARG;
+  if (rows == 0) return LOFTQ_ERR_UNSUPPORTED;
+  st = check_layer_buffers(n, rows, cols, base, mx, B, A, r);
+  if (st != LOFTQ_OK) return st;
+  if ((dX && !aligned16(dX)) || (dB && (!aligned16(dB) || !aligned16(dA)))) return LOFTQ_ERR_INVALID_ARG;
+  if (B == nullptr) r = 0;
+  const int rp = rank_pad(r);
+  if (n == 0) {   // sums over no tokens
+    if (dB) {
+      LQ_TRY(launch_grad_sum(nullptr, rows, rows, r, rp, 0, 0.f, false, dB, s));
+      LQ_TRY(launch_grad_sum(nullptr, cols, cols, r, rp, 0, 0.f, true, dA, s));
+    }
+    return LOFTQ_OK;
+  }
+  if (!dY || !ws || !aligned16(dY) || !aligned16(ws)) return LOFTQ_ERR_INVALID_ARG;
+  if (dB && (!X || !aligned16(X))) return LOFTQ_ERR_INVALID_ARG;
+  const BackwardSpace f = backward_space(ws, n, rows, cols, r);
+  if (ws_bytes < f.bytes) return LOFTQ_ERR_WORKSPACE;
+  const DropArg d = drop_arg(drop), none = drop_arg(nullptr);
+  const float gain = alpha * d.scale;
+  const i64 rows_pad = pad_to(rows, 64), n_pad = pad_to(n, 32);
+  const __bf16* G = static_cast<const __bf16*>(dY);
+  const __bf16* Xb = static_cast<const __bf16*>(X);
+  if (f.G != nullptr) {
+    LQ_TRY(launch_pad_rows(G, n, rows, rows_pad, f.G, s));
+    G = f.G;
+  }
+  if (r > 0) {
+    LQ_TRY(launch_adapter_operands(AdapterOperands{A, B, r, rp, rows, cols, rows_pad, f.Ab, f.At, nullptr, f.Bt}, s));
+    LQ_TRY(launch_down(G, n, rows_pad, f.Bt, rp, f.ks_p, none, f.partials, s));
+    LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks_p, f.Ps, f.Pt, n_pad, s));
+    if (dB) {
+      LQ_TRY(launch_grad(Xb, n, cols, f.Pt, rp, n_pad, f.ts_a, d, f.partials, s));
+      LQ_TRY(launch_grad_sum(f.partials, cols, cols, r, rp, f.ts_a, gain, true, dA, s));
+      LQ_TRY(launch_down(Xb, n, cols, f.Ab, rp, f.ks_h, d, f.partials, s));
+      LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks_h, nullptr, f.Ht, n_pad, s));
+      LQ_TRY(launch_grad(G, n, rows_pad, f.Ht, rp, n_pad, f.ts_b, none, f.partials, s));
+      LQ_TRY(launch_grad_sum(f.partials, rows_pad, rows, r, rp, f.ts_b, gain, false, dB, s));
+    }
+  }
+  if (!dX) return LOFTQ_OK;
+  LQ_TRY(launch_base_bf16_t(base, rows, cols, rows_pad, f.Wt, s));
+  TileProduct t{};
+  t.W = f.Wt;
+  t.X = G;
+  t.ldw = t.ldx = rows_pad * 2;
+  t.M = n;
+  t.N = cols;
+  t.steps = static_cast<int>(rows_pad / 64);
+  if (r > 0) {
+    t.V = f.At;
+    t.S = f.Ps;
+    t.rp = rp;
+    t.gain = gain;
+    t.drop = d;
+  }
+  t.out = dX;
+  t.odt = xdt;
+  return from_hip(launch_tile_product(t, false, s));
+}
+
+Base4 nf_base(const uint8_t* packed, const float* absmax, const int8_t* qabsmax, const float* dq_scale, int32_t bits) {
+  Base4 b;
+  b.packed = packed;
+  b.absmax = absmax;
+  b.qabsmax = qabsmax;
+  b.dq_scale = dq_scale;
+  b.bits = bits;
+  return b;
+}
+
+Base4 mx_base(const uint8_t* packed, const uint8_t* scales) {
+  Base4 b;
+  b.packed = packed;
+  b.mx = scales;
+  return b;
+}
+
+// 0 where a workspace query's sizes are none that the call would take
+bool query_ok(i64 n, i64 rows, i64 cols, int32_t r) {
+  return shape_ok(rows, cols) && n >= 0 && n < (i64(1) << 31) && r >= 0 && r <= 64 && layer_shape_ok(n, rows, cols, r);
+}
+
+}  // namespace
+
+extern "C" {
+
+loftq_status_t loftq_dropout(const void* X, loftq_dtype_t dt, int64_t n, const loftq_dropout_t* drop, void* Y,
+                             void* stream) {
+  if (!dtype_ok(dt) || n < 0 || drop == nullptr || !drop_ok(drop)) return LOFTQ_ERR_INVALID_ARG;
+  if (n == 0) return LOFTQ_OK;
+  if (!X || !Y || !aligned16(X) || !aligned16(Y)) return LOFTQ_ERR_INVALID_ARG;
+  return from_hip(launch_dropout(X, dt, n, drop_arg(drop), Y, static_cast<hipStream_t>(stream)));
+}
+
+size_t loftq_mxfp4_packed_bytes(int64_t rows, int64_t cols) {
+  return shape_ok(rows, cols) ? static_cast<size_t>(rows * mx_steps(cols) * (kMxStep / 2)) : 0;
+}
+
+size_t loftq_mxfp4_scale_bytes(int64_t rows, int64_t cols) {
+  return shape_ok(rows, cols) ? static_cast<size_t>(rows * mx_steps(cols) * (kMxStep / kMxBlock)) : 0;
+}
+
+loftq_status_t loftq_mxfp4_quantize(const void* W, loftq_dtype_t wdt, int64_t rows, int64_t cols, const float* B,
+                                    const float* A, int32_t r, uint8_t* packed, uint8_t* scales, void* stream) {
+  if (!shape_ok(rows, cols) || !dtype_ok(wdt)) return LOFTQ_ERR_INVALID_ARG;
+  if ((B == nullptr) != (A == nullptr)) return LOFTQ_ERR_INVALID_ARG;
+  if (B != nullptr && (r < 1 || r > 4096)) return LOFTQ_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return LOFTQ_OK;
+  if (!mx_shape_ok(rows, cols)) return LOFTQ_ERR_UNSUPPORTED;
+  if (!W || !packed || !scales) return LOFTQ_ERR_INVALID_ARG;
+  if (!aligned16(W) || !aligned16(packed) || !aligned16(scales)) return LOFTQ_ERR_INVALID_ARG;
+  if (B && (!aligned16(B) || !aligned16(A))) return LOFTQ_ERR_INVALID_ARG;
+  return from_hip(launch_mx_quantize(W, wdt, rows, cols, B, A, B ? r : 0, packed, scales,
+                                     static_cast<hipStream_t>(stream)));
+}
+
+loftq_status_t loftq_mxfp4_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t rows, int64_t cols,
+                                      const void* W, loftq_dtype_t wdt, void* out, loftq_dtype_t odt, void* stream) {
+  if (!shape_ok(rows, cols) || !dtype_ok(odt) || (W && !dtype_ok(wdt))) return LOFTQ_ERR_INVALID_ARG;
+  if (rows == 0 || cols == 0) return LOFTQ_OK;
+  if (!mx_shape_ok(rows, cols)) return LOFTQ_ERR_UNSUPPORTED;
+  if (!packed || !scales || !out) return LOFTQ_ERR_INVALID_ARG;
+  if (!aligned16(packed) || !aligned16(scales) || !aligned16(out) || (W && !aligned16(W))) return LOFTQ_ERR_INVALID_ARG;
+  return from_hip(launch_mx_dequantize(packed, scales, rows, cols, W, wdt, out, odt, static_cast<hipStream_t>(stream)));
+}
+
+loftq_status_t loftq_qlora_forward_dropout(const void* X, int64_t n_tok, int64_t rows, int64_t cols,
+                                           const uint8_t* packed, const float* absmax, const int8_t* qabsmax,
+                                           const float* dq_scale, int32_t bits, const float* B, const float* A,
+                                           int32_t r, float alpha, const loftq_dropout_t* drop, void* Y,
+                                           loftq_dtype_t ydt, void* ws, size_t ws_bytes, void* stream) {
+  return layer_forward(X, n_tok, rows, cols, nf_base(packed, absmax, qabsmax, dq_scale, bits), false, B, A, r, alpha,
+                       drop, Y, ydt, ws, ws_bytes, static_cast<hipStream_t>(stream));
+}
+
+loftq_status_t loftq_mxfp4_forward(const void* X, int64_t n_tok, int64_t rows, int64_t cols, const uint8_t* packed,
+                                   const uint8_t* scales, const float* B, const float* A, int32_t r, float alpha,
+                                   const loftq_dropout_t* drop, void* Y, loftq_dtype_t ydt, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  return layer_forward(X, n_tok, rows, cols, mx_base(packed, scales), true, B, A, r, alpha, drop, Y, ydt, ws, ws_bytes,
+                       static_cast<hipStream_t>(stream));
+}
+
+loftq_status_t loftq_qlora_backward(const void* dY, const void* X, int64_t n_tok, int64_t rows, int64_t cols,
+                                    const uint8_t* packed, const float* absmax, const int8_t* qabsmax,
+                                    const float* dq_scale, int32_t bits, const float* B, const float* A, int32_t r,
+                                    float alpha, const loftq_dropout_t* drop, void* dX, loftq_dtype_t xdt, float* dB,
+                                    float* dA, void* ws, size_t ws_bytes, void* stream) {
+  return layer_backward(dY, X, n_tok, rows, cols, nf_base(packed, absmax, qabsmax, dq_scale, bits), false, B, A, r,
+                        alpha, drop, dX, xdt, dB, dA, ws, ws_bytes, static_cast<hipStream_t>(stream));
+}
+
+loftq_status_t loftq_mxfp4_backward(const void* dY, const void* X, int64_t n_tok, int64_t rows, int64_t cols,
+                                    const uint8_t* packed, const uint8_t* scales, const float* B, const float* A,
+                                    int32_t r, float alpha, const loftq_dropout_t* drop, void* dX, loftq_dtype_t xdt,
+                                    float* dB, float* dA, void* ws, size_t ws_bytes, void* stream) {
+  return layer_backward(dY, X, n_tok, rows, cols, mx_base(packed, scales), true, B, A, r, alpha, drop, dX, xdt, dB, dA,
+                        ws, ws_bytes, static_cast<hipStream_t>(stream));
+}
+
+size_t loftq_qlora_forward_dropout_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t r) {
+  return query_ok(n_tok, rows, cols, r) ? forward_space(nullptr, n_tok, rows, cols, r, false).bytes : 0;
+}
+
+size_t loftq_mxfp4_forward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t r) {
+  return query_ok(n_tok, rows, cols, r) ? forward_space(nullptr, n_tok, rows, cols, r, true).bytes : 0;
+}
+
+size_t loftq_qlora_backward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t r) {
+  return query_ok(n_tok, rows, cols, r) ? backward_space(nullptr, n_tok, rows, cols, r).bytes : 0;
+}
+
+size_t loftq_mxfp4_backward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t r) {
+  return loftq_qlora_backward_workspace_bytes(n_tok, rows, cols, r);
+}
+
+}  // extern "C"

@@ -1,0 +1,92 @@
+// The adapted layer's training and serving path: what its translation units share.
+#pragma once
+
+#include "dropout.h"
+#include "internal.h"
+#include "mxfp4.h"
+
+namespace loftq {
+
+// A frozen 4-bit weight (rows x cols): NormalFloat codes with absmax or double-quantized
+// scales, or MXFP4 codes with their scales (then `mx` is set).
+struct Base4 {
+  const uint8_t* packed = nullptr;
+  const float* absmax = nullptr;
+  const int8_t* qabsmax = nullptr;
+  const float* dq_scale = nullptr;
+  const uint8_t* mx = nullptr;
+  int bits = 4;
+};
+
+// One tiled product C[m][n] = sum_k X[m][k] W[n][k] + gain keep(m, n) sum_p S[m][p] V[n][p]
+// (tokens m, features n), both operands with their K in whole 128-byte steps.
+struct TileProduct {
+  const void* W;              // N rows of `steps` 128-byte steps, ldw bytes apart
+  const void* X;              // M rows, ldx bytes apart
+  int64_t ldw, ldx;
+  const uint8_t* wscale;      // MXFP4: 8 bytes per row and step, [steps][N][8] and [steps][M][8]
+  const uint8_t* xscale;
+  int64_t M, N;
+  int steps;
+  const __bf16* V;            // [N][rp], or null
+  const __bf16* S;            // [M][3][rp]: three bf16 pieces of each fp32 value
+  int rp;                     // r rounded up to 16
+  float gain;
+  DropArg drop;               // thr != 0: the second term is kept where the mask keeps (m N + n)
+  void* out;
+  loftq_dtype_t odt;
+};
+
+hipError_t launch_tile_product(const TileProduct& t, bool mx, hipStream_t s);
+bool tile_product_shape_ok(int64_t M, int64_t N);
+
+// ---- adapter and base operands (adapter_kernels.hip) ----
+struct AdapterOperands {
+  const float* A;   // r x cols
+  const float* B;   // rows x r
+  int r, rp;
+  int64_t rows, cols, rows_pad;
+  __bf16* Ab;       // [rp][cols] or null
+  __bf16* At;       // [cols][rp] or null
+  __bf16* Bb;       // [rows][rp] or null
+  __bf16* Bt;       // [rp][rows_pad] or null
+};
+hipError_t launch_adapter_operands(const AdapterOperands& a, hipStream_t s);
+
+// P = keep(X) M^T as K-split partials [ks][n][rp]; then the sum in split order as three
+// bf16 pieces, token-major S [n][3][rp] and / or rank-major St [3][rp][n_pad].
+int down_splits(int64_t n, int64_t K);
+hipError_t launch_down(const __bf16* X, int64_t n, int64_t K, const __bf16* Mb, int rp, int ks, const DropArg& drop,
+                       float* partials, hipStream_t s);
+hipError_t launch_down_sum(const float* partials, int64_t n, int r, int rp, int ks, __bf16* S, __bf16* St,
+                           int64_t n_pad, hipStream_t s);
+
+// out[i][p] = coef sum_t keep(L)[t][i] (fp32 value of St)[p][t], over ts token ranges.
+int grad_splits(int64_t n, int64_t F);
+hipError_t launch_grad(const __bf16* L, int64_t n, int64_t F, const __bf16* St, int rp, int64_t n_pad, int ts,
+                       const DropArg& drop, float* partials, hipStream_t s);
+// the sum of the partials as out[i r + p] (rank_major false) or out[p nf + i], i < nf
+hipError_t launch_grad_sum(const float* partials, int64_t F, int64_t nf, int r, int rp, int ts, float coef,
+                           bool rank_major, float* out, hipStream_t s);
+
+// bf16(deq) of the base: [rows][cols], or transposed [cols][rows_pad] with zeros past `rows`.
+hipError_t launch_base_bf16(const Base4& b, int64_t rows, int64_t cols, __bf16* out, hipStream_t s);
+hipError_t launch_base_bf16_t(const Base4& b, int64_t rows, int64_t cols, int64_t rows_pad, __bf16* out,
+                              hipStream_t s);
+// rows of `cols` elements into rows of `ld` with zeros past `cols`
+hipError_t launch_pad_rows(const __bf16* src, int64_t n, int64_t cols, int64_t ld, __bf16* dst, hipStream_t s);
+
+// ---- MXFP4 (mxfp4_kernels.hip) ----
+bool mx_shape_ok(int64_t rows, int64_t cols);
+hipError_t launch_mx_quantize(const void* W, loftq_dtype_t wdt, int64_t rows, int64_t cols, const float* B,
+                              const float* A, int r, uint8_t* packed, uint8_t* scales, hipStream_t s);
+hipError_t launch_mx_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t rows, int64_t cols,
+                                const void* W, loftq_dtype_t wdt, void* out, loftq_dtype_t odt, hipStream_t s);
+
+hipError_t launch_dropout(const void* X, loftq_dtype_t dt, int64_t n, const DropArg& d, void* Y, hipStream_t s);
+
+bool aligned16(const void* p);
+bool shape_ok(int64_t rows, int64_t cols);
+loftq_status_t from_hip(hipError_t e);
+
+}  // namespace loftq

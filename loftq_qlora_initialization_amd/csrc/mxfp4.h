@@ -1,0 +1,57 @@
+// MXFP4 as the library stores it (OCP Microscaling Formats v1.0: FP4 e2m1 elements, one
+// e8m0 scale per 32): a rows x cols matrix in blocks of 32 consecutive columns of a row.
+//
+// Codes: each row is padded with zeros to whole steps of 256 columns (128 bytes), two
+// codes per byte, element 2i in the high nibble.  Code = sign << 3 | magnitude index.
+// Scales: one byte per block, 2^(byte - 127), 255 = NaN; stored step by step, the 8
+// bytes of row i in step k at (k rows + i) 8, so that the rows of a tile's step are
+// one contiguous run.  A step is the K step of the tiled product: 128 bytes of codes
+// and 8 scales a row, without a tail.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace loftq {
+
+constexpr int kMxBlock = 32, kMxStep = 256;
+
+inline int64_t mx_steps(int64_t cols) { return (cols + kMxStep - 1) / kMxStep; }
+
+namespace {
+
+// The scale byte of a block whose largest magnitude has the bits `amax` (fp32, sign
+// cleared): its exponent less that of 4 (FP4's largest binade), at least 2^-127; NaN
+// where the block holds an infinity or a NaN.  The value below is floor(log2 amax) - 2
+// + 127 for normal amax; subnormal ones have exponent field 0 and give byte 0.
+__device__ __forceinline__ uint32_t mx_scale_byte(uint32_t amax) {
+  const uint32_t e = amax >> 23;
+  return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+// 2^(127 - byte), the factor that takes a block's values to FP4's range (byte <= 252); 0 for a NaN block
+__device__ __forceinline__ float mx_inverse_scale(uint32_t byte) {
+  return byte == 255u ? 0.f : __uint_as_float((254u - byte) << 23);
+}
+// 2^(byte - 127)
+__device__ __forceinline__ float mx_scale(uint32_t byte) {
+  return byte == 255u ? __uint_as_float(0x7FC00000u) : (byte == 0u ? __uint_as_float(0x00400000u)
+                                                                   : __uint_as_float(byte << 23));
+}
+
+// e2m1 code of x: nearest magnitude of {0, .5, 1, 1.5, 2, 3, 4, 6}, ties to the even
+// code, larger magnitudes to 6.
+__device__ __forceinline__ uint32_t fp4_code(float x) {
+  const float m = fabsf(x);
+  const uint32_t c = (m > 0.25f) + (m >= 0.75f) + (m > 1.25f) + (m >= 1.75f) + (m > 2.5f) + (m >= 3.5f) + (m > 5.f);
+  return c | (__float_as_uint(x) >> 28 & 8u);
+}
+__device__ __forceinline__ float fp4_value(uint32_t code) {
+  // magnitude code 0: 0, 1: 0.5, else (1 + m / 2) 2^(e - 1) with e = code >> 1 & 3, m = code & 1
+  const uint32_t e = code >> 1 & 3u, m = code & 1u;
+  const float mag = e == 0u ? 0.5f * static_cast<float>(m)
+                            : __uint_as_float(((126u + e) << 23) | (m << 22));
+  return code & 8u ? -mag : mag;
+}
+
+}  // namespace
+}  // namespace loftq

@@ -1,0 +1,164 @@
+// MXFP4 quantization (optionally of a residual W - B A) and dequantization.
+#include "internal.h"
+#include "mxfp4.h"
+
+namespace loftq {
+namespace {
+
+constexpr int kMxThreads = 256;
+
+// One thread per 8 consecutive columns of the padded matrix; the four lanes of a quad
+// hold one block and exchange its largest magnitude by two quad permutes.  kVec: cols %
+// 8 == 0, so eight elements are 16-byte loads; otherwise they are loaded one by one.
+// R = W - B A is formed in fp32, the r products added in the order of p.
+template <typename T, bool kVec>
+__global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __restrict__ W, int64_t rows, int64_t cols,
+                                                                 int64_t steps, const float* __restrict__ B,
+                                                                 const float* __restrict__ A, int r,
+                                                                 uint8_t* __restrict__ packed,
+                                                                 uint8_t* __restrict__ scales) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kMxThreads + threadIdx.x;
+  const int64_t per_row = steps * (kMxStep / 8);
+  if (id >= rows * per_row) return;   // whole quads: per_row % 32 == 0
+  const int64_t row = id / per_row, c0 = (id - row * per_row) * 8;
+  float x[8];
+  if (kVec) {
+    if (c0 < cols) {
+      typedef T vec __attribute__((ext_vector_type(8)));
+      const vec w = *reinterpret_cast<const vec*>(W + row * cols + c0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(w[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = 0.f;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = c0 + j < cols ? static_cast<float>(W[row * cols + c0 + j]) : 0.f;
+  }
+  if (r > 0) {
+    float ba[8] = {};
+    for (int p = 0; p < r; ++p) {
+      const float b = B[row * r + p];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (c0 + j < cols) ba[j] = fmaf(b, A[static_cast<int64_t>(p) * cols + c0 + j], ba[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] -= ba[j];
+  }
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = __float_as_uint(x[j]) & 0x7FFFFFFFu;
+    amax = b > amax ? b : amax;
+  }
+  const uint32_t o1 = __builtin_amdgcn_mov_dpp(amax, 0xB1, 0xF, 0xF, true);   // quad_perm 1,0,3,2
+  amax = o1 > amax ? o1 : amax;
+  const uint32_t o2 = __builtin_amdgcn_mov_dpp(amax, 0x4E, 0xF, 0xF, true);   // quad_perm 2,3,0,1
+  amax = o2 > amax ? o2 : amax;
+  const uint32_t byte = mx_scale_byte(amax);
+  const float inv = mx_inverse_scale(byte);
+  uint32_t word = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) word |= fp4_code(x[j] * inv) << (8 * (j >> 1) + (j & 1 ? 0 : 4));
+  reinterpret_cast<uint32_t*>(packed)[id] = word;
+  if ((threadIdx.x & 3) == 0) {
+    const int64_t k = c0 / kMxStep;
+    scales[(k * rows + row) * 8 + (c0 % kMxStep) / kMxBlock] = static_cast<uint8_t>(byte);
+  }
+}
+
+// out = deq or W - deq, in fp32 or bf16; one thread per 8 columns.
+template <typename T, typename O, bool kHasW, bool kVec>
+__global__ __launch_bounds__(kMxThreads) void mx_dequantize_kernel(const uint8_t* __restrict__ packed,
+                                                                   const uint8_t* __restrict__ scales, int64_t rows,
+                                                                   int64_t cols, int64_t steps,
+                                                                   const T* __restrict__ W, O* __restrict__ out) {
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kMxThreads + threadIdx.x;
+  const int64_t per_row = (cols + 7) / 8;
+  if (id >= rows * per_row) return;
+  const int64_t row = id / per_row, c0 = (id - row * per_row) * 8;
+  const uint32_t word = *reinterpret_cast<const uint32_t*>(packed + row * steps * (kMxStep / 2) + c0 / 2);
+  const float sc = mx_scale(scales[(c0 / kMxStep * rows + row) * 8 + (c0 % kMxStep) / kMxBlock]);
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = fp4_value(word >> (8 * (j >> 1) + (j & 1 ? 0 : 4)) & 15u) * sc;
+  if (kVec) {
+    typedef T tvec __attribute__((ext_vector_type(8)));
+    typedef O ovec __attribute__((ext_vector_type(8)));
+    ovec o;
+    if (kHasW) {
+      const tvec w = *reinterpret_cast<const tvec*>(W + row * cols + c0);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = static_cast<float>(w[j]) - v[j];
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[j] = static_cast<O>(v[j]);
+    *reinterpret_cast<ovec*>(out + row * cols + c0) = o;
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (c0 + j >= cols) break;
+      const float w = kHasW ? static_cast<float>(W[row * cols + c0 + j]) : 0.f;
+      out[row * cols + c0 + j] = static_cast<O>(kHasW ? w - v[j] : v[j]);
+    }
+  }
+}
+
+unsigned blocks_for(int64_t threads) { return static_cast<unsigned>((threads + kMxThreads - 1) / kMxThreads); }
+
+}  // namespace
+
+bool mx_shape_ok(int64_t rows, int64_t cols) {
+  // one launch has a thread per 8 padded columns: at most 2^32 of them
+  return rows == 0 || mx_steps(cols) * (kMxStep / 8) <= ((int64_t(1) << 32) - kMxThreads) / rows;
+}
+
+hipError_t launch_mx_quantize(const void* W, loftq_dtype_t wdt, int64_t rows, int64_t cols, const float* B,
+                              const float* A, int r, uint8_t* packed, uint8_t* scales, hipStream_t s) {
+  const int64_t steps = mx_steps(cols);
+  const dim3 grid(blocks_for(rows * steps * (kMxStep / 8)));
+#define LQ_MXQ(T, VEC)                                                                                            \
+  LQ_LAUNCH("mx_quantize", (mx_quantize_kernel<T, VEC>), grid, dim3(kMxThreads), 0, s, static_cast<const T*>(W), rows, \
+            cols, steps, B, A, r, packed, scales)
+  const bool vec = cols % 8 == 0;
+  if (wdt == LOFTQ_BF16) {
+    if (vec) LQ_MXQ(__bf16, true);
+    else LQ_MXQ(__bf16, false);
+  } else {
+    if (vec) LQ_MXQ(float, true);
+    else LQ_MXQ(float, false);
+  }
+#undef LQ_MXQ
+  return hipGetLastError();
+}
+
+hipError_t launch_mx_dequantize(const uint8_t* packed, const uint8_t* scales, int64_t rows, int64_t cols,
+                                const void* W, loftq_dtype_t wdt, void* out, loftq_dtype_t odt, hipStream_t s) {
+  const int64_t steps = mx_steps(cols);
+  const dim3 grid(blocks_for(rows * ((cols + 7) / 8)));
+#define LQ_MXD(T, O, HASW, VEC)                                                                                       \
+  LQ_LAUNCH("mx_dequantize", (mx_dequantize_kernel<T, O, HASW, VEC>), grid, dim3(kMxThreads), 0, s, packed, scales, rows, \
+            cols, steps, static_cast<const T*>(W), static_cast<O*>(out))
+#define LQ_MXD_O(O)                                                  \
+  do {                                                               \
+    if (W == nullptr) {                                              \
+      if (cols % 8 == 0) LQ_MXD(float, O, false, true);              \
+      else LQ_MXD(float, O, false, false);                           \
+    } else if (wdt == LOFTQ_BF16) {                                  \
+      if (cols % 8 == 0) LQ_MXD(__bf16, O, true, true);              \
+      else LQ_MXD(__bf16, O, true, false);                           \
+    } else {                                                         \
+      if (cols % 8 == 0) LQ_MXD(float, O, true, true);               \
+      else LQ_MXD(float, O, true, false);                            \
+    }                                                                \
+  } while (0)
+  if (odt == LOFTQ_BF16) LQ_MXD_O(__bf16);
+  else LQ_MXD_O(float);
+#undef LQ_MXD_O
+#undef LQ_MXD
+  return hipGetLastError();
+}
+
+}  // namespace loftq

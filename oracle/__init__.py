@@ -35,6 +35,11 @@ Parity status of each function (pins live in tests/test_oracle_*.py):
   bf16_round              pinned (hand values, ties to even, torch's own conversion)
   qlora_forward           pinned (bf16-exact weights give X W^T + alpha X A^T B^T computed
                           directly; linear in X)
+  keep_mask / dropout     pinned (the first words worked out with Python integers; kept share;
+                          p = 0 and p = 1)
+  mx_quantize             pinned (every FP4 midpoint and its neighbours, scale bytes by hand,
+                          round trip of representable values)
+  layer_forward/backward  pinned (differences of the forward; the mask's closed forms)
   warm_sketch             pinned (T = 1 reduces to the cold start; a warm sketch
                           spanning a rank-r E's row space recovers the exact SVD
                           with no power iteration)
@@ -47,10 +52,15 @@ from .lowrank import householder_qr, jacobi_svd, randomized_svd, exact_svd, lora
 from .loftq import loftq_step, loftq_init, objective, warm_sketch
 from .merge import merge_adapter, unmerge_adapter
 from .forward import bf16_round, qlora_forward
+from .dropout import drop_threshold, drop_scale, keep_mask, dropout
+from .mxfp4 import E2M1, mx_scale_bytes, mx_quantize, mx_values, mx_pack, mx_unpack
+from .layer import layer_forward, layer_backward
 
 __all__ = [
     "nf4_codebook", "nf_codebook", "nf_delta", "norm_ppf", "nf4_midpoints", "block_absmax", "nf4_encode", "pack_nibbles",
     "unpack_nibbles", "dequantize", "quantize_residual", "double_quant", "dq_scales_expand",
     "splitmix64_stream", "rademacher_sketch", "householder_qr", "jacobi_svd", "randomized_svd",
     "exact_svd", "lora_factors", "loftq_step", "loftq_init", "objective", "merge_adapter", "unmerge_adapter", "warm_sketch", "bf16_round", "qlora_forward",
+    "drop_threshold", "drop_scale", "keep_mask", "dropout", "E2M1", "mx_scale_bytes", "mx_quantize", "mx_values", "mx_pack",
+    "mx_unpack", "layer_forward", "layer_backward",
 ]
