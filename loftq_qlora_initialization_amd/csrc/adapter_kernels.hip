@@ -23,30 +23,30 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 // ---- the adapter's bf16 operands, zero past r (and past `rows` in Bt) ----
 __global__ __launch_bounds__(kThreads) void adapter_operands_kernel(AdapterOperands a) {
   int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t nA = a.rp * a.cols, nB = a.rp * a.rows, nBt = a.rp * a.rows_pad;
+  const int64_t nAb = a.rp * a.cols, nAt = a.ld * a.cols, nBb = a.ld * a.rows, nBt = a.rp * a.rows_pad;
   if (a.Ab != nullptr) {
-    if (i < nA) {
+    if (i < nAb) {
       const int64_t p = i / a.cols;
       a.Ab[i] = static_cast<__bf16>(p < a.r ? a.A[i] : 0.f);
       return;
     }
-    i -= nA;
+    i -= nAb;
   }
   if (a.At != nullptr) {
-    if (i < nA) {
-      const int64_t c = i / a.rp, p = i - c * a.rp;
-      a.At[i] = static_cast<__bf16>(p < a.r ? a.A[p * a.cols + c] : 0.f);
+    if (i < nAt) {
+      const int64_t c = i / a.ld, e = i - c * a.ld, p = e % a.rp;
+      a.At[i] = static_cast<__bf16>(p < a.r && e < 3 * a.rp ? a.A[p * a.cols + c] : 0.f);
       return;
     }
-    i -= nA;
+    i -= nAt;
   }
   if (a.Bb != nullptr) {
-    if (i < nB) {
-      const int64_t row = i / a.rp, p = i - row * a.rp;
-      a.Bb[i] = static_cast<__bf16>(p < a.r ? a.B[row * a.r + p] : 0.f);
+    if (i < nBb) {
+      const int64_t row = i / a.ld, e = i - row * a.ld, p = e % a.rp;
+      a.Bb[i] = static_cast<__bf16>(p < a.r && e < 3 * a.rp ? a.B[row * a.r + p] : 0.f);
       return;
     }
-    i -= nB;
+    i -= nBb;
   }
   if (a.Bt != nullptr && i < nBt) {
     const int64_t p = i / a.rows_pad, row = i - p * a.rows_pad;
@@ -205,21 +205,33 @@ __global__ __launch_bounds__(kThreads) void down_kernel(const __bf16* __restrict
 // rounding of what the ones before leave: the three hold 24 bits, so the products they
 // enter lose nothing against fp32; an infinity or NaN is all in the first).  Ranks past r
 // and tokens past n are zeros.
+__device__ __forceinline__ void split3(float x, __bf16 (&h)[3]) {
+#pragma unroll
+  for (int q = 0; q < 3; ++q) {
+    h[q] = static_cast<__bf16>(x);
+    x = __builtin_isfinite(static_cast<float>(h[q])) ? x - static_cast<float>(h[q]) : 0.f;
+  }
+}
 __global__ __launch_bounds__(kThreads) void down_sum_kernel(const float* __restrict__ partials, int64_t n, int r, int rp,
-                                                            int ks, __bf16* __restrict__ S, __bf16* __restrict__ St,
-                                                            int64_t n_pad) {
+                                                            int ks, float gain, int ld, __bf16* __restrict__ S,
+                                                            __bf16* __restrict__ St, int64_t n_pad) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
   if (i >= n_pad * rp) return;
   const int64_t p = i / n_pad, m = i - p * n_pad;
   float x = 0.f;
   if (m < n && p < r)
     for (int q = 0; q < ks; ++q) x += partials[(q * n + m) * rp + p];
+  __bf16 h[3];
+  if (S != nullptr && m < n) {
+    split3(gain * x, h);
 #pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    const __bf16 h = static_cast<__bf16>(x);
-    x = __builtin_isfinite(static_cast<float>(h)) ? x - static_cast<float>(h) : 0.f;
-    if (S != nullptr && m < n) S[(m * 3 + q) * rp + p] = h;
-    if (St != nullptr) St[(q * rp + p) * n_pad + m] = h;
+    for (int q = 0; q < 3; ++q) S[m * ld + q * rp + p] = h[q];
+    if (p < ld - 3 * rp) S[m * ld + 3 * rp + p] = static_cast<__bf16>(0.f);   // ld - 3 rp is rp or 0
+  }
+  if (St != nullptr) {
+    split3(x, h);
+#pragma unroll
+    for (int q = 0; q < 3; ++q) St[(q * rp + p) * n_pad + m] = h[q];
   }
 }
 
@@ -334,7 +346,8 @@ unsigned blocks_for(int64_t threads) { return static_cast<unsigned>((threads + k
 }  // namespace
 
 hipError_t launch_adapter_operands(const AdapterOperands& a, hipStream_t s) {
-  const int64_t n = a.rp * ((a.Ab ? a.cols : 0) + (a.At ? a.cols : 0) + (a.Bb ? a.rows : 0) + (a.Bt ? a.rows_pad : 0));
+  const int64_t n = a.rp * ((a.Ab ? a.cols : 0) + (a.Bt ? a.rows_pad : 0)) +
+                    a.ld * ((a.At ? a.cols : 0) + (a.Bb ? a.rows : 0));
   LQ_LAUNCH("adapter_operands", adapter_operands_kernel, dim3(blocks_for(n)), dim3(kThreads), 0, s, a);
   return hipGetLastError();
 }
@@ -366,10 +379,10 @@ hipError_t launch_down(const __bf16* X, int64_t n, int64_t K, const __bf16* Mb, 
   return hipGetLastError();
 }
 
-hipError_t launch_down_sum(const float* partials, int64_t n, int r, int rp, int ks, __bf16* S, __bf16* St,
+hipError_t launch_down_sum(const float* partials, int64_t n, int r, int rp, int ks, float gain, __bf16* S, __bf16* St,
                            int64_t n_pad, hipStream_t s) {
   LQ_LAUNCH("adapter_down_sum", down_sum_kernel, dim3(blocks_for(n_pad * rp)), dim3(kThreads), 0, s, partials, n, r, rp,
-            ks, S, St, n_pad);
+            ks, gain, adapter_ld(rp), S, St, n_pad);
   return hipGetLastError();
 }
 

@@ -30,7 +30,8 @@ struct ForwardSpace {
   uint8_t* xq;      // MXFP4 base: the activations' codes and scales
   uint8_t* xs;
   __bf16 *Ab, *Bb, *S;
-  float* partials;
+  float* partials;   // of X A^T
+  float* joins;      // of the product's K ranges
   int ks;
   size_t bytes;
 };
@@ -48,10 +49,12 @@ ForwardSpace forward_space(void* ws, i64 n, i64 rows, i64 cols, int r, bool mx) 
     const int rp = rank_pad(r);
     f.ks = down_splits(n, cols);
     f.Ab = a.take<__bf16>(rp * cols);
-    f.Bb = a.take<__bf16>(rows * rp);
-    f.S = a.take<__bf16>(n * 3 * rp);
+    f.Bb = a.take<__bf16>(rows * adapter_ld(rp));
+    f.S = a.take<__bf16>(n * adapter_ld(rp));
     f.partials = a.take<float>(static_cast<i64>(f.ks) * n * rp);
   }
+  const int steps = static_cast<int>(mx ? mx_steps(cols) : cols / 64);
+  f.joins = a.take<float>(plan_tile_product(n, rows, steps, r > 0 ? adapter_ld(rank_pad(r)) / 64 : 0, mx).partial_bytes / 4);
   f.bytes = a.used;
   return f;
 }
@@ -59,6 +62,7 @@ ForwardSpace forward_space(void* ws, i64 n, i64 rows, i64 cols, int r, bool mx) 
 struct BackwardSpace {
   __bf16 *G, *Wt, *Ab, *At, *Bt, *Ht, *Pt, *Ps;
   float* partials;   // of one thin product at a time
+  float* joins;      // of the product's K ranges
   int ks_h, ks_p, ts_b, ts_a;
   size_t bytes;
 };
@@ -76,16 +80,18 @@ BackwardSpace backward_space(void* ws, i64 n, i64 rows, i64 cols, int r) {
     f.ts_b = grad_splits(n, rows_pad);
     f.ts_a = grad_splits(n, cols);
     f.Ab = a.take<__bf16>(rp * cols);
-    f.At = a.take<__bf16>(cols * rp);
+    f.At = a.take<__bf16>(cols * adapter_ld(rp));
     f.Bt = a.take<__bf16>(rp * rows_pad);
     f.Ht = a.take<__bf16>(3 * rp * n_pad);
     f.Pt = a.take<__bf16>(3 * rp * n_pad);
-    f.Ps = a.take<__bf16>(n * 3 * rp);
+    f.Ps = a.take<__bf16>(n * adapter_ld(rp));
     i64 most = static_cast<i64>(f.ks_h > f.ks_p ? f.ks_h : f.ks_p) * n;
     if (f.ts_b * rows_pad > most) most = f.ts_b * rows_pad;
     if (f.ts_a * cols > most) most = f.ts_a * cols;
     f.partials = a.take<float>(most * rp);
   }
+  f.joins = a.take<float>(plan_tile_product(n, cols, static_cast<int>(rows_pad / 64),
+                                            r > 0 ? adapter_ld(rank_pad(r)) / 64 : 0, false).partial_bytes / 4);
   f.bytes = a.used;
   return f;
 }
@@ -93,9 +99,9 @@ BackwardSpace backward_space(void* ws, i64 n, i64 rows, i64 cols, int r) {
 // Every launch of a call stays below 2^32 work-items.
 bool layer_shape_ok(i64 n, i64 rows, i64 cols, int r) {
   const i64 limit = (i64(1) << 32) - 1024, rp = rank_pad(r), rows_pad = pad_to(rows, 64), n_pad = pad_to(n, 64);
-  return tile_product_shape_ok(n, rows) && tile_product_shape_ok(n, cols) && n_pad * 64 < limit &&
+  return tile_product_shape_ok(n, rows, cols) && tile_product_shape_ok(n, cols, rows_pad) && n_pad * 64 < limit &&
          rows_pad * (cols / 8 + 8) < limit && n * (rows_pad / 8) < limit && n * mx_steps(cols) * 32 < limit &&
-         rp * 2 * (cols + rows_pad) < limit && (rows_pad + cols) * 32 < limit;
+         (rp + adapter_ld(static_cast<int>(rp))) * (cols + rows_pad) < limit && (rows_pad + cols) * 32 < limit;
 }
 
 bool drop_ok(const loftq_dropout_t* d) {
@@ -166,9 +172,10 @@ loftq_status_t layer_forward(const void* X, i64 n, i64 rows, i64 cols, const Bas
   const DropArg d = drop_arg(drop);
   const int rp = rank_pad(r);
   if (r > 0) {
-    LQ_TRY(launch_adapter_operands(AdapterOperands{A, B, r, rp, rows, cols, rows, f.Ab, nullptr, f.Bb, nullptr}, s));
+    LQ_TRY(launch_adapter_operands(AdapterOperands{A, B, r, rp, rows, cols, rows, f.Ab, nullptr, f.Bb, nullptr,
+                                                  adapter_ld(rp)}, s));
     LQ_TRY(launch_down(Xb, n, cols, f.Ab, rp, f.ks, d, f.partials, s));
-    LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks, f.S, nullptr, n, s));
+    LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks, alpha * d.scale, f.S, nullptr, n, s));
   }
   TileProduct t{};
   t.M = n;
@@ -191,12 +198,11 @@ loftq_status_t layer_forward(const void* X, i64 n, i64 rows, i64 cols, const Bas
   if (r > 0) {
     t.V = f.Bb;
     t.S = f.S;
-    t.rp = rp;
-    t.gain = alpha * d.scale;
+    t.adapter_steps = adapter_ld(rp) / 64;
   }
   t.out = Y;
   t.odt = ydt;
-  return from_hip(launch_tile_product(t, mx, s));
+  return from_hip(launch_tile_product(t, mx, f.joins, s));
 }
 
 loftq_status_t layer_backward(const void* dY, const void* X, i64 n, i64 rows, i64 cols, const Base4& base, bool mx,
@@ -235,14 +241,15 @@ loftq_status_t layer_backward(const void* dY, const void* X, i64 n, i64 rows, i6
     G = f.G;
   }
   if (r > 0) {
-    LQ_TRY(launch_adapter_operands(AdapterOperands{A, B, r, rp, rows, cols, rows_pad, f.Ab, f.At, nullptr, f.Bt}, s));
+    LQ_TRY(launch_adapter_operands(AdapterOperands{A, B, r, rp, rows, cols, rows_pad, f.Ab, f.At, nullptr, f.Bt,
+                                                  adapter_ld(rp)}, s));
     LQ_TRY(launch_down(G, n, rows_pad, f.Bt, rp, f.ks_p, none, f.partials, s));
-    LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks_p, f.Ps, f.Pt, n_pad, s));
+    LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks_p, gain, f.Ps, f.Pt, n_pad, s));
     if (dB) {
       LQ_TRY(launch_grad(Xb, n, cols, f.Pt, rp, n_pad, f.ts_a, d, f.partials, s));
       LQ_TRY(launch_grad_sum(f.partials, cols, cols, r, rp, f.ts_a, gain, true, dA, s));
       LQ_TRY(launch_down(Xb, n, cols, f.Ab, rp, f.ks_h, d, f.partials, s));
-      LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks_h, nullptr, f.Ht, n_pad, s));
+      LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks_h, gain, nullptr, f.Ht, n_pad, s));
       LQ_TRY(launch_grad(G, n, rows_pad, f.Ht, rp, n_pad, f.ts_b, none, f.partials, s));
       LQ_TRY(launch_grad_sum(f.partials, rows_pad, rows, r, rp, f.ts_b, gain, false, dB, s));
     }
@@ -259,13 +266,12 @@ loftq_status_t layer_backward(const void* dY, const void* X, i64 n, i64 rows, i6
   if (r > 0) {
     t.V = f.At;
     t.S = f.Ps;
-    t.rp = rp;
-    t.gain = gain;
+    t.adapter_steps = adapter_ld(rp) / 64;
     t.drop = d;
   }
   t.out = dX;
   t.odt = xdt;
-  return from_hip(launch_tile_product(t, false, s));
+  return from_hip(launch_tile_product(t, false, f.joins, s));
 }
 
 Base4 nf_base(const uint8_t* packed, const float* absmax, const int8_t* qabsmax, const float* dq_scale, int32_t bits) {

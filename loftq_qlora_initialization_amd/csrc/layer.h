@@ -18,8 +18,8 @@ struct Base4 {
   int bits = 4;
 };
 
-// One tiled product C[m][n] = sum_k X[m][k] W[n][k] + gain keep(m, n) sum_p S[m][p] V[n][p]
-// (tokens m, features n), both operands with their K in whole 128-byte steps.
+// One tiled product C[m][n] = sum_k X[m][k] W[n][k] + keep(m, n) sum_p S[m][p] V[n][p]
+// (tokens m, features n), all operands with their K in whole 128-byte steps.
 struct TileProduct {
   const void* W;              // N rows of `steps` 128-byte steps, ldw bytes apart
   const void* X;              // M rows, ldx bytes apart
@@ -28,17 +28,23 @@ struct TileProduct {
   const uint8_t* xscale;
   int64_t M, N;
   int steps;
-  const __bf16* V;            // [N][rp], or null
-  const __bf16* S;            // [M][3][rp]: three bf16 pieces of each fp32 value
-  int rp;                     // r rounded up to 16
-  float gain;
+  const __bf16* V;            // [N][adapter_steps 64]: the factor, three times over
+  const __bf16* S;            // [M][adapter_steps 64]: three bf16 pieces of each fp32 value
+  int adapter_steps;          // 0: no second term
   DropArg drop;               // thr != 0: the second term is kept where the mask keeps (m N + n)
   void* out;
   loftq_dtype_t odt;
+  int splits;                 // K ranges, set by the launcher
 };
 
-hipError_t launch_tile_product(const TileProduct& t, bool mx, hipStream_t s);
-bool tile_product_shape_ok(int64_t M, int64_t N);
+// How a product is divided: a tile shape, K ranges, and the bytes of their partial outputs.
+struct TilePlan {
+  int shape, splits;
+  size_t partial_bytes;
+};
+TilePlan plan_tile_product(int64_t M, int64_t N, int steps, int adapter_steps, bool mx);
+hipError_t launch_tile_product(TileProduct t, bool mx, float* partials, hipStream_t s);
+bool tile_product_shape_ok(int64_t M, int64_t N, int64_t K);
 
 // ---- adapter and base operands (adapter_kernels.hip) ----
 struct AdapterOperands {
@@ -47,18 +53,22 @@ struct AdapterOperands {
   int r, rp;
   int64_t rows, cols, rows_pad;
   __bf16* Ab;       // [rp][cols] or null
-  __bf16* At;       // [cols][rp] or null
-  __bf16* Bb;       // [rows][rp] or null
+  __bf16* At;       // [cols][ld] or null: the rank three times over, zeros behind it
+  __bf16* Bb;       // [rows][ld] or null, likewise
   __bf16* Bt;       // [rp][rows_pad] or null
+  int ld;           // adapter_ld(rp)
 };
+// elements of a row of the adapter's operands in the tiled product: three times the padded rank, in whole steps
+inline int adapter_ld(int rp) { return (3 * rp + 63) / 64 * 64; }
 hipError_t launch_adapter_operands(const AdapterOperands& a, hipStream_t s);
 
 // P = keep(X) M^T as K-split partials [ks][n][rp]; then the sum in split order as three
-// bf16 pieces, token-major S [n][3][rp] and / or rank-major St [3][rp][n_pad].
+// bf16 pieces, of gain P token-major in S [n][adapter_ld(rp)], of P rank-major in
+// St [3][rp][n_pad] (either may be null).
 int down_splits(int64_t n, int64_t K);
 hipError_t launch_down(const __bf16* X, int64_t n, int64_t K, const __bf16* Mb, int rp, int ks, const DropArg& drop,
                        float* partials, hipStream_t s);
-hipError_t launch_down_sum(const float* partials, int64_t n, int r, int rp, int ks, __bf16* S, __bf16* St,
+hipError_t launch_down_sum(const float* partials, int64_t n, int r, int rp, int ks, float gain, __bf16* S, __bf16* St,
                            int64_t n_pad, hipStream_t s);
 
 // out[i][p] = coef sum_t keep(L)[t][i] (fp32 value of St)[p][t], over ts token ranges.
