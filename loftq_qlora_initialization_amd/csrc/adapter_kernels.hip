@@ -1,6 +1,7 @@
 // Operands and thin products of the adapted layer's training path: the adapter's bf16
 // operands, the base weight in bf16, X A^T and dY B (n x r), and the adapter's
-// gradients (features x r) as products over the tokens.
+// gradients (features x r) as products over the tokens.  A gradient needs two of each,
+// over dY and over X: one launch takes both, as two jobs of one grid.
 //
 // v_mfma_f32_16x16x32_bf16: lane L supplies A[L%16][8(L/16) + j] and
 // B[8(L/16) + j][L%16] (j = 0..7) and receives D[4(L/16) + v][L%16] in element v.
@@ -20,49 +21,76 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }
 
-// ---- the adapter's bf16 operands, zero past r (and past `rows` in Bt) ----
-__global__ __launch_bounds__(kThreads) void adapter_operands_kernel(AdapterOperands a) {
-  int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  const int64_t nAb = a.rp * a.cols, nAt = a.ld * a.cols, nBb = a.ld * a.rows, nBt = a.rp * a.rows_pad;
+// ---- what a call's products read, in one launch ----
+// Work of thread i of the adapter's operands, eight elements each, zeros past r (and past
+// `rows` in Bt).
+__device__ __forceinline__ void adapter_operand(const AdapterOperands& a, uint32_t i) {
+  const uint32_t cols = static_cast<uint32_t>(a.cols), rows = static_cast<uint32_t>(a.rows);
+  const uint32_t rows_pad = static_cast<uint32_t>(a.rows_pad), groups = static_cast<uint32_t>(a.ld) / 8;
+  bf16x8 o;
   if (a.Ab != nullptr) {
-    if (i < nAb) {
-      const int64_t p = i / a.cols;
-      a.Ab[i] = static_cast<__bf16>(p < a.r ? a.A[i] : 0.f);
+    const uint32_t per = cols / 8, n = a.rp * per;
+    if (i < n) {
+      const int p = i / per;
+      const int64_t c = static_cast<int64_t>(i % per) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = static_cast<__bf16>(p < a.r ? a.A[p * a.cols + c + j] : 0.f);
+      *reinterpret_cast<bf16x8*>(a.Ab + p * a.cols + c) = o;
       return;
     }
-    i -= nAb;
+    i -= n;
   }
-  if (a.At != nullptr) {
-    if (i < nAt) {
-      const int64_t c = i / a.ld, e = i - c * a.ld, p = e % a.rp;
-      a.At[i] = static_cast<__bf16>(p < a.r && e < 3 * a.rp ? a.A[p * a.cols + c] : 0.f);
+  if (a.At != nullptr) {   // neighbouring threads take neighbouring columns, whose reads are one run
+    const uint32_t n = groups * cols;
+    if (i < n) {
+      const int64_t c = i % cols;
+      const int e = static_cast<int>(i / cols) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int p = (e + j) % a.rp;
+        o[j] = static_cast<__bf16>(p < a.r && e < 3 * a.rp ? a.A[p * a.cols + c] : 0.f);
+      }
+      *reinterpret_cast<bf16x8*>(a.At + c * a.ld + e) = o;
       return;
     }
-    i -= nAt;
+    i -= n;
   }
   if (a.Bb != nullptr) {
-    if (i < nBb) {
-      const int64_t row = i / a.ld, e = i - row * a.ld, p = e % a.rp;
-      a.Bb[i] = static_cast<__bf16>(p < a.r && e < 3 * a.rp ? a.B[row * a.r + p] : 0.f);
+    const uint32_t n = groups * rows;
+    if (i < n) {
+      const int64_t row = i / groups;
+      const int e = static_cast<int>(i % groups) * 8;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int p = (e + j) % a.rp;
+        o[j] = static_cast<__bf16>(p < a.r && e < 3 * a.rp ? a.B[row * a.r + p] : 0.f);
+      }
+      *reinterpret_cast<bf16x8*>(a.Bb + row * a.ld + e) = o;
       return;
     }
-    i -= nBb;
+    i -= n;
   }
-  if (a.Bt != nullptr && i < nBt) {
-    const int64_t p = i / a.rows_pad, row = i - p * a.rows_pad;
-    a.Bt[i] = static_cast<__bf16>(p < a.r && row < a.rows ? a.B[row * a.r + p] : 0.f);
+  if (a.Bt != nullptr && i < a.rp * (rows_pad / 8)) {   // neighbouring threads take neighbouring ranks
+    const int p = i % a.rp;
+    const int64_t row = static_cast<int64_t>(i / a.rp) * 8;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      o[j] = static_cast<__bf16>(p < a.r && row + j < a.rows ? a.B[(row + j) * a.r + p] : 0.f);
+    *reinterpret_cast<bf16x8*>(a.Bt + p * a.rows_pad + row) = o;
   }
 }
 
-// ---- the base weight in bf16 ----
-// Both sources give 8 consecutive elements of a row (c % 8 == 0) as bf16(fp32 value).
+// Eight elements of the base from e8 on (row-major, 8 | e8) as bf16(fp32 value).
 struct NfSource {
   const uint8_t* packed;
   const float* absmax;
   const int8_t* qabsmax;
   const float* dq_scale;
   __device__ __forceinline__ u32x4 load8(const float* lvl, int64_t row, int64_t c, int64_t rows, int64_t cols) const {
-    const int64_t e = row * cols + c, b = e >> 6;
+    return at(lvl, row * cols + c);
+  }
+  __device__ __forceinline__ u32x4 at(const float* lvl, int64_t e) const {
+    const int64_t b = e >> 6;
     const uint32_t word = *reinterpret_cast<const uint32_t*>(packed + (e >> 1));
     const float sc = qabsmax != nullptr ? static_cast<float>(qabsmax[b]) * dq_scale[b >> 8] : absmax[b];
     bf16x8 o;
@@ -88,58 +116,84 @@ struct Levels {
   float v[16];
 };
 
+// One 64 x 128 tile of the base turned round in LDS: thread t decodes rows 2 (t / 8) and the
+// next, columns 16 (t % 8) .. + 15, and keeps the two rows' values of a column in one word
+// (row stride 33 words: a wave's 64 words fall into 64 banks); then it writes half a column's
+// 64 rows, 64 bytes.
+constexpr int kTurnRows = 64, kTurnCols = 128;
 template <typename Src>
-__global__ __launch_bounds__(kThreads) void base_bf16_kernel(Src src, Levels lv, int64_t rows, int64_t cols,
-                                                             __bf16* __restrict__ out) {
-  __shared__ float lvl[16];
-  if (threadIdx.x < 16) lvl[threadIdx.x] = lv.v[threadIdx.x];
+__device__ __forceinline__ void turn_base(const Src& src, const float* lvl, uint32_t (*tile)[33], int64_t tr, int64_t tc,
+                                          int64_t rows, int64_t cols, int64_t rows_pad, __bf16* __restrict__ out) {
+  const int tid = threadIdx.x, pair = tid / 8, c16 = (tid % 8) * 16;
+  const int64_t row = tr * kTurnRows + 2 * pair;
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+  for (int q = 0; q < 2; ++q) {
+    const int64_t c = tc * kTurnCols + c16 + q * 8;
+    const u32x4 lo = row < rows && c < cols ? src.load8(lvl, row, c, rows, cols) : zero;
+    const u32x4 hi = row + 1 < rows && c < cols ? src.load8(lvl, row + 1, c, rows, cols) : zero;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+      tile[c16 + q * 8 + j][pair] = __builtin_amdgcn_perm(hi[j >> 1], lo[j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
+  }
   __syncthreads();
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 8;
-  if (i >= rows * cols) return;
-  const int64_t row = i / cols;
-  *reinterpret_cast<u32x4*>(out + i) = src.load8(lvl, row, i - row * cols, rows, cols);
+  // 16 bytes of 4 rows' pairs a store, the 8 lanes of a column one run of 128 bytes
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int cc = q * 32 + tid / 8, w0 = (tid % 8) * 4;
+    const int64_t c = tc * kTurnCols + cc;
+    if (c >= cols) continue;
+    const u32x4 v = {tile[cc][w0], tile[cc][w0 + 1], tile[cc][w0 + 2], tile[cc][w0 + 3]};
+    *reinterpret_cast<u32x4*>(out + c * rows_pad + tr * kTurnRows + 2 * w0) = v;
+  }
 }
 
-// One 64 x 64 tile per workgroup, turned round in LDS: thread t reads row t / 4, 16
-// columns, and writes column t / 4, 16 rows.
-template <typename Src>
-__global__ __launch_bounds__(kThreads) void base_bf16_t_kernel(Src src, Levels lv, int64_t rows, int64_t cols,
-                                                               int64_t rows_pad, __bf16* __restrict__ out) {
+// Workgroups 0 .. base_wgs - 1 form the base's operand (transposed, as it lies, or, over
+// MXFP4, the codes of X), the next operand_wgs the adapter's, the rest pads dY's rows.
+template <typename Src, int kBase>   // kBase 0: as it lies, 1: transposed, 2: MXFP4 codes of `x`
+__global__ __launch_bounds__(kThreads) void prepare_kernel(Src src, Levels lv, PrepareArgs p) {
   __shared__ float lvl[16];
-  __shared__ __align__(16) uint16_t tile[64][64 + 8];
+  __shared__ uint32_t tile[kBase == 1 ? kTurnCols : 1][33];
   const int tid = threadIdx.x;
-  if (tid < 16) lvl[tid] = lv.v[tid];
-  __syncthreads();
-  const int64_t ntr = rows_pad / 64;
-  const int64_t tr = blockIdx.x % ntr, tc = blockIdx.x / ntr;
-  const int64_t row = tr * 64 + tid / 4;
+  uint32_t wg = blockIdx.x;
+  if (wg < p.base_wgs) {
+    if constexpr (kBase == 2) {
+      const uint32_t id = wg * kThreads + tid, per_row = static_cast<uint32_t>(p.steps * (kMxStep / 8));
+      const int64_t row = id / per_row, c0 = static_cast<int64_t>(id % per_row) * 8;
+      if (row >= p.n) return;   // whole quads: per_row % 32 == 0
+      float x[8];
+      const bf16x8 v = c0 < p.a.cols ? *reinterpret_cast<const bf16x8*>(p.x + row * p.a.cols + c0) : bf16x8{};
 #pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int cc = (tid % 4) * 16 + q * 8;
-    const int64_t c = tc * 64 + cc;
-    const u32x4 v = row < rows && c < cols ? src.load8(lvl, row, c, rows, cols) : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-    for (int j = 0; j < 8; ++j) tile[cc + j][tid / 4] = static_cast<uint16_t>(v[j >> 1] >> (16 * (j & 1)));
+      for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(v[j]);
+      uint32_t byte;
+      reinterpret_cast<uint32_t*>(p.xq)[id] = mx_encode8(x, byte);
+      if ((tid & 3) == 0) p.xs[(c0 / kMxStep * p.n + row) * 8 + (c0 % kMxStep) / kMxBlock] = static_cast<uint8_t>(byte);
+    } else {
+      if (tid < 16) lvl[tid] = lv.v[tid];
+      __syncthreads();
+      if constexpr (kBase == 1) {
+        const uint32_t ntr = static_cast<uint32_t>(p.a.rows_pad / kTurnRows);
+        turn_base(src, lvl, tile, wg % ntr, wg / ntr, p.a.rows, p.a.cols, p.a.rows_pad, p.base);
+      } else {
+        const int64_t e = (static_cast<int64_t>(wg) * kThreads + tid) * 8;
+        if (e < p.a.rows * p.a.cols) *reinterpret_cast<u32x4*>(p.base + e) = src.at(lvl, e);
+      }
+    }
+    return;
   }
-  __syncthreads();
-  const int64_t c = tc * 64 + tid / 4;
-  if (c >= cols) return;
-#pragma unroll
-  for (int q = 0; q < 2; ++q) {
-    const int rr = (tid % 4) * 16 + q * 8;
-    *reinterpret_cast<u32x4*>(out + c * rows_pad + tr * 64 + rr) = *reinterpret_cast<const u32x4*>(&tile[tid / 4][rr]);
+  wg -= p.base_wgs;
+  if (wg < p.operand_wgs) {
+    adapter_operand(p.a, wg * kThreads + tid);
+    return;
   }
-}
-
-__global__ __launch_bounds__(kThreads) void pad_rows_kernel(const __bf16* __restrict__ src, int64_t n, int64_t cols,
-                                                            int64_t ld, __bf16* __restrict__ dst) {
-  const int64_t i = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) * 8;
-  if (i >= n * ld) return;
-  const int64_t row = i / ld, c = i - row * ld;
+  wg -= p.operand_wgs;
+  const uint32_t id = wg * kThreads + tid, per_row = static_cast<uint32_t>(p.a.rows_pad / 8);
+  const int64_t row = id / per_row, c = static_cast<int64_t>(id % per_row) * 8;
+  if (row >= p.n) return;
   bf16x8 o;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) o[j] = c + j < cols ? src[row * cols + c + j] : static_cast<__bf16>(0.f);
-  *reinterpret_cast<bf16x8*>(dst + i) = o;
+  for (int j = 0; j < 8; ++j) o[j] = c + j < p.a.rows ? p.x[row * p.a.rows + c + j] : static_cast<__bf16>(0.f);
+  *reinterpret_cast<bf16x8*>(p.padded + row * p.a.rows_pad + c) = o;
 }
 
 // 8 values of a masked row, elements e .. e + 7 of the flattening (e % 8 == 0)
@@ -153,58 +207,81 @@ __device__ __forceinline__ u32x4 drop8(u32x4 v, uint64_t key, uint64_t e, uint32
 }
 
 // ---- thin product over the features: partial q of keep(X) M^T over the q-th K range ----
-// One wave per 16 tokens and range; M (rank-major, K along its rows) is shared by the
-// four waves of a workgroup through the caches.  U steps of 32 are loaded before the
-// first product; steps past the range repeat its last one with the tokens zeroed.
-template <int NT, bool kDrop>
-__global__ __launch_bounds__(kThreads) void down_kernel(const __bf16* __restrict__ X, int64_t n, int64_t K,
-                                                        const __bf16* __restrict__ Mb, int ks, DropArg d,
-                                                        float* __restrict__ out) {
-  constexpr int U = NT <= 2 ? 4 : 2;
+// A workgroup takes 32 tokens and one range, which its four waves share U steps of 32 at a
+// time; M (rank-major, K along its rows) serves both 16-token tiles.  All loads of U steps
+// are issued before the first product; steps past the range repeat its last one with the
+// tokens zeroed.  The waves' sums meet in LDS.
+template <int NT>
+__global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n) {
+  constexpr int U = 2;
+  __shared__ float part[3][2 * NT * 4 * 64];
+  const DownJob& jb = jobs.job[blockIdx.x < jobs.job[0].wgs ? 0 : 1];
+  const uint32_t wg = blockIdx.x < jobs.job[0].wgs ? blockIdx.x : blockIdx.x - jobs.job[0].wgs;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
-  const int64_t group = blockIdx.x / ks;
-  const int q = static_cast<int>(blockIdx.x - group * ks);
-  const int64_t m0 = group * 64 + w * 16;
-  if (m0 >= n) return;
-  const int64_t m = m0 + li < n ? m0 + li : n - 1;
-  const int64_t steps = K / 32, per = (steps + ks - 1) / ks;
-  const int64_t begin = q * per, end = begin + per < steps ? begin + per : steps;
-  const uint64_t key = kDrop ? drop_key(d) : 0;
-  f32x4 acc[NT];
+  const int64_t K = jb.K, m0 = static_cast<int64_t>(wg / jb.ks) * 32;
+  const int q = wg % jb.ks, steps = static_cast<int>(K / 32), per = (steps + jb.ks - 1) / jb.ks;
+  const int begin = q * per, end = begin + per < steps ? begin + per : steps;
+  const uint32_t thr = jb.drop.thr;
+  const uint64_t key = thr != 0 ? drop_key(jb.drop) : 0;
+  int64_t m[2];
 #pragma unroll
-  for (int t = 0; t < NT; ++t) acc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int64_t s0 = begin; s0 < end; s0 += U) {
-    u32x4 x[U], b[U][NT];
+  for (int t = 0; t < 2; ++t) m[t] = m0 + 16 * t + li < n ? m0 + 16 * t + li : n - 1;
+  f32x4 acc[2][NT];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int p = 0; p < NT; ++p) acc[t][p] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int s0 = begin + w * U; s0 < end; s0 += 4 * U) {
+    u32x4 x[U][2], b[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t k = (s0 + u < end ? s0 + u : end - 1) * 32 + 8 * lg;
-      x[u] = *reinterpret_cast<const u32x4*>(X + m * K + k);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) b[u][t] = *reinterpret_cast<const u32x4*>(Mb + (t * 16 + li) * K + k);
+      for (int t = 0; t < 2; ++t) x[u][t] = *reinterpret_cast<const u32x4*>(jb.X + m[t] * K + k);
+#pragma unroll
+      for (int p = 0; p < NT; ++p) b[u][p] = *reinterpret_cast<const u32x4*>(jb.M + (p * 16 + li) * K + k);
     }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t k = (s0 + u < end ? s0 + u : end - 1) * 32 + 8 * lg;
-      u32x4 v = s0 + u < end ? x[u] : u32x4{0u, 0u, 0u, 0u};
-      if (kDrop) v = drop8(v, key, static_cast<uint64_t>(m * K + k), d.thr);
 #pragma unroll
-      for (int t = 0; t < NT; ++t) acc[t] = mfma16(v, b[u][t], acc[t]);
+      for (int t = 0; t < 2; ++t) {
+        u32x4 v = s0 + u < end ? x[u][t] : u32x4{0u, 0u, 0u, 0u};
+        if (thr != 0) v = drop8(v, key, static_cast<uint64_t>(m[t] * K + k), thr);
+#pragma unroll
+        for (int p = 0; p < NT; ++p) acc[t][p] = mfma16(v, b[u][p], acc[t][p]);
+      }
     }
   }
-  float* o = out + static_cast<int64_t>(q) * n * (16 * NT);
+  if (w > 0)
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      const int64_t mm = m0 + 4 * lg + v;
-      if (mm < n) o[mm * (16 * NT) + t * 16 + li] = acc[t][v];
-    }
+      for (int p = 0; p < NT; ++p)
+#pragma unroll
+        for (int v = 0; v < 4; ++v) part[w - 1][((t * NT + p) * 4 + v) * 64 + lane] = acc[t][p][v];
+  __syncthreads();
+  if (w > 0) return;
+  float* o = jb.out + static_cast<int64_t>(q) * n * (16 * NT);
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int p = 0; p < NT; ++p)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const int64_t mm = m0 + 16 * t + 4 * lg + v;
+        const int at = ((t * NT + p) * 4 + v) * 64 + lane;
+        const float y = ((acc[t][p][v] + part[0][at]) + part[1][at]) + part[2][at];
+        if (mm < n) o[mm * (16 * NT) + p * 16 + li] = y;
+      }
 }
 
 // The sum of the partials in split order, as three bf16 pieces x = h0 + h1 + h2 (each the
 // rounding of what the ones before leave: the three hold 24 bits, so the products they
 // enter lose nothing against fp32; an infinity or NaN is all in the first).  Ranks past r
-// and tokens past n are zeros.
+// and tokens past n are zeros.  A workgroup takes 32 tokens; the rank-major form is turned
+// round in LDS.
 __device__ __forceinline__ void split3(float x, __bf16 (&h)[3]) {
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
@@ -212,83 +289,124 @@ __device__ __forceinline__ void split3(float x, __bf16 (&h)[3]) {
     x = __builtin_isfinite(static_cast<float>(h[q])) ? x - static_cast<float>(h[q]) : 0.f;
   }
 }
-__global__ __launch_bounds__(kThreads) void down_sum_kernel(const float* __restrict__ partials, int64_t n, int r, int rp,
-                                                            int ks, float gain, int ld, __bf16* __restrict__ S,
-                                                            __bf16* __restrict__ St, int64_t n_pad) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (i >= n_pad * rp) return;
-  const int64_t p = i / n_pad, m = i - p * n_pad;
-  float x = 0.f;
-  if (m < n && p < r)
-    for (int q = 0; q < ks; ++q) x += partials[(q * n + m) * rp + p];
-  __bf16 h[3];
-  if (S != nullptr && m < n) {
-    split3(gain * x, h);
+__global__ __launch_bounds__(kThreads) void down_sum_kernel(DownSumJobs jobs, int64_t n, int r, int rp, int ld,
+                                                            int64_t n_pad) {
+  __shared__ __bf16 turned[3 * 64][32 + 2];
+  const DownSumJob& jb = jobs.job[blockIdx.x < jobs.job[0].wgs ? 0 : 1];
+  const uint32_t wg = blockIdx.x < jobs.job[0].wgs ? blockIdx.x : blockIdx.x - jobs.job[0].wgs;
+  const int64_t m0 = static_cast<int64_t>(wg) * 32;
+  for (int i = threadIdx.x; i < 32 * rp; i += kThreads) {
+    const int tok = i / rp, p = i - tok * rp;
+    const int64_t m = m0 + tok;
+    float x = 0.f;
+    if (m < n && p < r) {
+      const float* src = jb.partials + m * rp + p;
+      int q = 0;
+      for (; q + 4 <= jb.ks; q += 4) {   // four loads in flight, added in order
+        const float a = src[q * n * rp], b = src[(q + 1) * n * rp], c = src[(q + 2) * n * rp], d = src[(q + 3) * n * rp];
+        x = (((x + a) + b) + c) + d;
+      }
+      for (; q < jb.ks; ++q) x += src[q * n * rp];
+    }
+    __bf16 h[3];
+    if (jb.S != nullptr && m < n) {
+      split3(jb.gain * x, h);
 #pragma unroll
-    for (int q = 0; q < 3; ++q) S[m * ld + q * rp + p] = h[q];
-    if (p < ld - 3 * rp) S[m * ld + 3 * rp + p] = static_cast<__bf16>(0.f);   // ld - 3 rp is rp or 0
+      for (int q = 0; q < 3; ++q) jb.S[m * ld + q * rp + p] = h[q];
+      if (p < ld - 3 * rp) jb.S[m * ld + 3 * rp + p] = static_cast<__bf16>(0.f);   // ld - 3 rp is rp or 0
+    }
+    if (jb.St != nullptr) {
+      split3(x, h);
+#pragma unroll
+      for (int q = 0; q < 3; ++q) turned[q * rp + p][tok] = h[q];
+    }
   }
-  if (St != nullptr) {
-    split3(x, h);
-#pragma unroll
-    for (int q = 0; q < 3; ++q) St[(q * rp + p) * n_pad + m] = h[q];
+  if (jb.St == nullptr) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < 3 * rp * 16; i += kThreads) {   // two tokens a store
+    const int p = i / 16, t = (i % 16) * 2;
+    *reinterpret_cast<uint32_t*>(jb.St + p * n_pad + m0 + t) = *reinterpret_cast<const uint32_t*>(&turned[p][t]);
   }
 }
 
 // ---- thin product over the tokens: the adapter's gradients ----
-// out[i][p] = sum_t L[t][i] S[t][p].  The matrix cores want each operand's K (tokens) in
+// out[i][p] = sum_t keep(L)[t][i] S[t][p].  The matrix cores want each operand's K (tokens) in
 // one lane, and L's tokens are rows: lane L loads 8 tokens x 8 features (16 bytes of 8
 // rows) and turns the 8 x 8 block round in its registers, which gives the operands of 8
 // products, the j-th for features 8 (L%16) + j.  A workgroup takes 128 features; its four
-// waves share a token range 32 tokens at a time, and their sums meet in LDS.
-template <int NT, bool kDrop>
-__global__ __launch_bounds__(kThreads) void grad_kernel(const __bf16* __restrict__ L, int64_t n, int64_t F,
-                                                        const __bf16* __restrict__ St, int64_t n_pad, int ts, DropArg d,
-                                                        float* __restrict__ out) {
-  __shared__ float part[2][8 * NT * 4 * 64];
+// waves share a token range 32 tokens at a time, the next step's loads in flight while one
+// is multiplied, and their sums meet in LDS.  kRankMajor (dA): S is the first operand, so a
+// lane holds 8 consecutive features of a rank; else (dB) a lane's rank is L%16.
+template <int NT, bool kRankMajor>
+__device__ __forceinline__ void grad_job(const GradJob& jb, uint32_t wg, int64_t n, int64_t n_pad, int r,
+                                         float (*part)[8 * NT * 4 * 64]) {
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
-  const int64_t group = blockIdx.x / ts;
-  const int q = static_cast<int>(blockIdx.x - group * ts);
+  const int64_t group = wg / jb.ts, F = jb.F;
+  const int q = wg % jb.ts;
   const int64_t f0 = group * 128 + 8 * li, f = f0 < F ? f0 : F - 8;   // F % 8 == 0
-  const int64_t steps = n_pad / 32, per = (steps + ts - 1) / ts;
-  const int64_t begin = q * per, end = begin + per < steps ? begin + per : steps;
-  const uint64_t key = kDrop ? drop_key(d) : 0;
+  const int steps = static_cast<int>(n_pad / 32), per = (steps + jb.ts - 1) / jb.ts;
+  const int begin = q * per, end = begin + per < steps ? begin + per : steps;
+  const uint32_t thr = kRankMajor ? jb.drop.thr : 0;
+  const uint64_t key = thr != 0 ? drop_key(jb.drop) : 0;
   f32x4 acc[8][NT];
 #pragma unroll
   for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int64_t s = begin + w; s < end; s += 4) {
-    const int64_t t0 = s * 32 + 8 * lg;
-    u32x4 x[8], b[3][NT];
-#pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[i] = *reinterpret_cast<const u32x4*>(L + (t0 + i < n ? t0 + i : n - 1) * F + f);
+  // S's operands are loaded ahead too where the registers allow it
+  constexpr int kSets = NT <= 2 ? 2 : 1;
+  u32x4 x[2][8], b[kSets][3][NT];
+  auto load_s = [&](int set, int s) __attribute__((always_inline)) {
+    const int64_t t0 = static_cast<int64_t>(s < end ? s : end - 1) * 32 + 8 * lg;
 #pragma unroll
     for (int h = 0; h < 3; ++h)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        b[h][t] = *reinterpret_cast<const u32x4*>(St + (h * 16 * NT + t * 16 + li) * n_pad + t0);
+        b[set % kSets][h][t] = *reinterpret_cast<const u32x4*>(jb.St + (h * 16 * NT + t * 16 + li) * n_pad + t0);
+  };
+  auto load = [&](int set, int s) __attribute__((always_inline)) {
+    const int64_t t0 = static_cast<int64_t>(s < end ? s : end - 1) * 32 + 8 * lg;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      x[set][i] = *reinterpret_cast<const u32x4*>(jb.L + (t0 + i < n ? t0 + i : n - 1) * F + f);
+    if (kSets == 2) load_s(set, s);
+  };
+  auto multiply = [&](int set, int s) __attribute__((always_inline)) {
+    const int64_t t0 = static_cast<int64_t>(s) * 32 + 8 * lg;
+    if (kSets == 1) load_s(set, s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      if (t0 + i >= n) x[i] = u32x4{0u, 0u, 0u, 0u};
-      if (kDrop) x[i] = drop8(x[i], key, static_cast<uint64_t>((t0 + i) * F + f), d.thr);
+      if (t0 + i >= n) x[set][i] = u32x4{0u, 0u, 0u, 0u};
+      if (thr != 0) x[set][i] = drop8(x[set][i], key, static_cast<uint64_t>((t0 + i) * F + f), thr);
     }
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       u32x4 lo, hi;   // features 2 c and 2 c + 1: tokens 0 .. 7
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        lo[i] = __builtin_amdgcn_perm(x[2 * i + 1][c], x[2 * i][c], 0x05040100u);
-        hi[i] = __builtin_amdgcn_perm(x[2 * i + 1][c], x[2 * i][c], 0x07060302u);
+        lo[i] = __builtin_amdgcn_perm(x[set][2 * i + 1][c], x[set][2 * i][c], 0x05040100u);
+        hi[i] = __builtin_amdgcn_perm(x[set][2 * i + 1][c], x[set][2 * i][c], 0x07060302u);
       }
 #pragma unroll
       for (int h = 0; h < 3; ++h)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          acc[2 * c][t] = mfma16(lo, b[h][t], acc[2 * c][t]);
-          acc[2 * c + 1][t] = mfma16(hi, b[h][t], acc[2 * c + 1][t]);
+          acc[2 * c][t] = kRankMajor ? mfma16(b[set % kSets][h][t], lo, acc[2 * c][t])
+                                     : mfma16(lo, b[set % kSets][h][t], acc[2 * c][t]);
+          acc[2 * c + 1][t] =
+              kRankMajor ? mfma16(b[set % kSets][h][t], hi, acc[2 * c + 1][t])
+                         : mfma16(hi, b[set % kSets][h][t], acc[2 * c + 1][t]);
         }
+    }
+  };
+  if (begin + w < end) {
+    load(0, begin + w);
+    for (int s = begin + w; s < end; s += 8) {
+      load(1, s + 4);
+      multiply(0, s);
+      if (s + 4 >= end) break;
+      load(0, s + 8);
+      multiply(1, s + 4);
     }
   }
   // waves 2 and 3 park their sums, 0 and 1 add them; then 1 parks and 0 adds
@@ -318,110 +436,61 @@ __global__ __launch_bounds__(kThreads) void grad_kernel(const __bf16* __restrict
         for (int v = 0; v < 4; ++v) part[0][at(j, t, v)] = acc[j][t][v];
   __syncthreads();
   if (w != 0) return;
-  float* o = out + static_cast<int64_t>(q) * F * (16 * NT);
+  // one range: the gradient itself; more: a partial sum with whole padded ranks and features
+  const bool whole = jb.ts == 1;
+  const int64_t nf = whole ? jb.nf : F;
+  const int nr = whole ? r : 16 * NT;
+  const float coef = whole ? jb.coef : 1.f;
+  float* o = whole ? jb.out : jb.partials + static_cast<int64_t>(q) * F * (16 * NT);
 #pragma unroll
-  for (int j = 0; j < 8; ++j)
+  for (int t = 0; t < NT; ++t)
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
+    for (int v = 0; v < 4; ++v) {
+      float y[8];
 #pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        const int64_t i = group * 128 + 8 * (4 * lg + v) + j;
-        if (i < F) o[i * (16 * NT) + t * 16 + li] = acc[j][t][v] + part[0][at(j, t, v)];
+      for (int j = 0; j < 8; ++j) y[j] = coef * (acc[j][t][v] + part[0][at(j, t, v)]);
+      if constexpr (kRankMajor) {
+        const int p = t * 16 + 4 * lg + v;   // features f0 .. f0 + 7
+        if (p < nr && f0 < F)                // nf == F here, and 8 | F
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<f32x4*>(o + p * nf + f0 + 4 * h) = f32x4{y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]};
+      } else {
+        const int p = t * 16 + li;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int64_t i = group * 128 + 8 * (4 * lg + v) + j;
+          if (i < nf && p < nr) o[i * nr + p] = y[j];
+        }
       }
+    }
 }
 
-__global__ __launch_bounds__(kThreads) void grad_sum_kernel(const float* __restrict__ partials, int64_t F, int64_t nf,
-                                                            int r, int rp, int ts, float coef, int rank_major,
-                                                            float* __restrict__ out) {
-  const int64_t i = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
+// job 0: dB over dY; job 1: dA over X
+template <int NT>
+__global__ __launch_bounds__(kThreads) void grad_kernel(GradJobs jobs, int64_t n, int64_t n_pad, int r) {
+  __shared__ float part[2][8 * NT * 4 * 64];
+  if (blockIdx.x < jobs.job[0].wgs)
+    grad_job<NT, false>(jobs.job[0], blockIdx.x, n, n_pad, r, part);
+  else
+    grad_job<NT, true>(jobs.job[1], blockIdx.x - jobs.job[0].wgs, n, n_pad, r, part);
+}
+
+// coef times the sum of the partials in range order; job 0 feature-major, job 1 rank-major
+__global__ __launch_bounds__(kThreads) void grad_sum_kernel(GradJobs jobs, int r, int rp) {
+  const uint32_t first = (static_cast<uint32_t>(jobs.job[0].nf) * r + kThreads - 1) / kThreads;
+  const bool rank_major = blockIdx.x >= first;
+  const GradJob& jb = jobs.job[rank_major ? 1 : 0];
+  const uint32_t i = (blockIdx.x - (rank_major ? first : 0)) * kThreads + threadIdx.x, nf = static_cast<uint32_t>(jb.nf);
   if (i >= nf * r) return;
-  const int64_t f = rank_major ? i % nf : i / r, p = rank_major ? i / nf : i % r;
+  const int64_t at = rank_major ? i / nf * jb.F + i % nf : static_cast<int64_t>(i / r) * rp + i % r;
   float x = 0.f;
-  for (int q = 0; q < ts; ++q) x += partials[(q * F + f) * rp + p];
-  out[i] = coef * x;
+  for (int q = 0; q < jb.ts; ++q) x += jb.partials[q * jb.F * rp + at];
+  jb.out[i] = jb.coef * x;
 }
 
 unsigned blocks_for(int64_t threads) { return static_cast<unsigned>((threads + kThreads - 1) / kThreads); }
 
-}  // namespace
-
-hipError_t launch_adapter_operands(const AdapterOperands& a, hipStream_t s) {
-  const int64_t n = a.rp * ((a.Ab ? a.cols : 0) + (a.Bt ? a.rows_pad : 0)) +
-                    a.ld * ((a.At ? a.cols : 0) + (a.Bb ? a.rows : 0));
-  LQ_LAUNCH("adapter_operands", adapter_operands_kernel, dim3(blocks_for(n)), dim3(kThreads), 0, s, a);
-  return hipGetLastError();
-}
-
-int down_splits(int64_t n, int64_t K) {
-  const int64_t groups = n > 64 ? (n + 63) / 64 : 1;
-  int64_t ks = 512 / groups;
-  if (ks > K / 32 / 8) ks = K / 32 / 8;
-  return static_cast<int>(ks < 1 ? 1 : (ks > 16 ? 16 : ks));
-}
-
-hipError_t launch_down(const __bf16* X, int64_t n, int64_t K, const __bf16* Mb, int rp, int ks, const DropArg& drop,
-                       float* partials, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((n + 63) / 64 * ks));
-#define LQ_DOWN(NT)                                                                                                    \
-  do {                                                                                                                 \
-    if (drop.thr != 0)                                                                                                 \
-      LQ_LAUNCH("adapter_down", (down_kernel<NT, true>), grid, dim3(kThreads), 0, s, X, n, K, Mb, ks, drop, partials); \
-    else                                                                                                               \
-      LQ_LAUNCH("adapter_down", (down_kernel<NT, false>), grid, dim3(kThreads), 0, s, X, n, K, Mb, ks, drop, partials); \
-  } while (0)
-  switch (rp / 16) {
-    case 1: LQ_DOWN(1); break;
-    case 2: LQ_DOWN(2); break;
-    case 3: LQ_DOWN(3); break;
-    default: LQ_DOWN(4); break;
-  }
-#undef LQ_DOWN
-  return hipGetLastError();
-}
-
-hipError_t launch_down_sum(const float* partials, int64_t n, int r, int rp, int ks, float gain, __bf16* S, __bf16* St,
-                           int64_t n_pad, hipStream_t s) {
-  LQ_LAUNCH("adapter_down_sum", down_sum_kernel, dim3(blocks_for(n_pad * rp)), dim3(kThreads), 0, s, partials, n, r, rp,
-            ks, gain, adapter_ld(rp), S, St, n_pad);
-  return hipGetLastError();
-}
-
-int grad_splits(int64_t n, int64_t F) {
-  const int64_t groups = F > 128 ? (F + 127) / 128 : 1;
-  int64_t ts = 512 / groups;
-  const int64_t most = (n + 127) / 128;   // at least 128 tokens, one step of each wave
-  if (ts > most) ts = most;
-  return static_cast<int>(ts < 1 ? 1 : (ts > 16 ? 16 : ts));
-}
-
-hipError_t launch_grad(const __bf16* L, int64_t n, int64_t F, const __bf16* St, int rp, int64_t n_pad, int ts,
-                       const DropArg& drop, float* partials, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((F + 127) / 128 * ts));
-#define LQ_GRAD(NT)                                                                                                     \
-  do {                                                                                                                  \
-    if (drop.thr != 0)                                                                                                  \
-      LQ_LAUNCH("adapter_grad", (grad_kernel<NT, true>), grid, dim3(kThreads), 0, s, L, n, F, St, n_pad, ts, drop, partials); \
-    else                                                                                                                \
-      LQ_LAUNCH("adapter_grad", (grad_kernel<NT, false>), grid, dim3(kThreads), 0, s, L, n, F, St, n_pad, ts, drop, partials); \
-  } while (0)
-  switch (rp / 16) {
-    case 1: LQ_GRAD(1); break;
-    case 2: LQ_GRAD(2); break;
-    case 3: LQ_GRAD(3); break;
-    default: LQ_GRAD(4); break;
-  }
-#undef LQ_GRAD
-  return hipGetLastError();
-}
-
-hipError_t launch_grad_sum(const float* partials, int64_t F, int64_t nf, int r, int rp, int ts, float coef,
-                           bool rank_major, float* out, hipStream_t s) {
-  LQ_LAUNCH("adapter_grad_sum", grad_sum_kernel, dim3(blocks_for(nf * r)), dim3(kThreads), 0, s, partials, F, nf, r, rp,
-            ts, coef, rank_major ? 1 : 0, out);
-  return hipGetLastError();
-}
-
-namespace {
 Levels base_levels(const Base4& b) {
   Levels lv{};
   if (b.mx != nullptr) {
@@ -432,31 +501,88 @@ Levels base_levels(const Base4& b) {
   }
   return lv;
 }
+
 }  // namespace
 
-hipError_t launch_base_bf16(const Base4& b, int64_t rows, int64_t cols, __bf16* out, hipStream_t s) {
-  const dim3 grid(blocks_for(rows * cols / 8));
+hipError_t launch_prepare(PrepareArgs p, const Base4& b, PrepareBase kind, hipStream_t s) {
+  const AdapterOperands& a = p.a;
+  p.operand_wgs = a.r == 0 ? 0 : blocks_for((a.Ab ? a.rp * (a.cols / 8) : 0) + (a.Bt ? a.rp * (a.rows_pad / 8) : 0) +
+                                            a.ld / 8 * ((a.At ? a.cols : 0) + (a.Bb ? a.rows : 0)));
+  p.base_wgs = kind == kBaseNone         ? 0
+               : kind == kBaseTransposed ? static_cast<unsigned>((a.rows_pad / kTurnRows) * ((a.cols + kTurnCols - 1) / kTurnCols))
+               : kind == kBaseCodesOfX   ? blocks_for(p.n * p.steps * (kMxStep / 8))
+                                         : blocks_for(a.rows * a.cols / 8);
+  const unsigned pad_wgs = p.padded != nullptr ? blocks_for(p.n * (a.rows_pad / 8)) : 0;
+  const dim3 grid(p.base_wgs + p.operand_wgs + pad_wgs);
+  if (grid.x == 0) return hipSuccess;
   const Levels lv = base_levels(b);
-  LQ_LAUNCH("base_bf16", (base_bf16_kernel<NfSource>), grid, dim3(kThreads), 0, s,
-            (NfSource{b.packed, b.absmax, b.qabsmax, b.dq_scale}), lv, rows, cols, out);
-  return hipGetLastError();
-}
-
-hipError_t launch_base_bf16_t(const Base4& b, int64_t rows, int64_t cols, int64_t rows_pad, __bf16* out,
-                              hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>((rows_pad / 64) * ((cols + 63) / 64)));
-  const Levels lv = base_levels(b);
-  if (b.mx != nullptr)
-    LQ_LAUNCH("base_bf16_t", (base_bf16_t_kernel<MxSource>), grid, dim3(kThreads), 0, s, (MxSource{b.packed, b.mx}), lv,
-              rows, cols, rows_pad, out);
+  const NfSource nf{b.packed, b.absmax, b.qabsmax, b.dq_scale};
+  const MxSource mx{b.packed, b.mx};
+  if (kind == kBaseCodesOfX)
+    LQ_LAUNCH("prepare_layer", (prepare_kernel<MxSource, 2>), grid, dim3(kThreads), 0, s, mx, lv, p);
+  else if (kind == kBaseAsItLies || kind == kBaseNone)
+    LQ_LAUNCH("prepare_layer", (prepare_kernel<NfSource, 0>), grid, dim3(kThreads), 0, s, nf, lv, p);
+  else if (b.mx != nullptr)
+    LQ_LAUNCH("prepare_layer", (prepare_kernel<MxSource, 1>), grid, dim3(kThreads), 0, s, mx, lv, p);
   else
-    LQ_LAUNCH("base_bf16_t", (base_bf16_t_kernel<NfSource>), grid, dim3(kThreads), 0, s,
-              (NfSource{b.packed, b.absmax, b.qabsmax, b.dq_scale}), lv, rows, cols, rows_pad, out);
+    LQ_LAUNCH("prepare_layer", (prepare_kernel<NfSource, 1>), grid, dim3(kThreads), 0, s, nf, lv, p);
   return hipGetLastError();
 }
 
-hipError_t launch_pad_rows(const __bf16* src, int64_t n, int64_t cols, int64_t ld, __bf16* dst, hipStream_t s) {
-  LQ_LAUNCH("pad_rows", pad_rows_kernel, dim3(blocks_for(n * ld / 8)), dim3(kThreads), 0, s, src, n, cols, ld, dst);
+#define LQ_BY_RANK(rp, CALL) \
+  switch ((rp) / 16) {       \
+    case 1: CALL(1); break;  \
+    case 2: CALL(2); break;  \
+    case 3: CALL(3); break;  \
+    default: CALL(4); break; \
+  }
+
+int down_splits(int64_t n, int64_t K) {
+  // about two workgroups per CU, each with at least 8 steps (two per wave)
+  const int64_t groups = n > 32 ? (n + 31) / 32 : 1;
+  int64_t ks = 512 / groups;
+  if (ks > K / 32 / 8) ks = K / 32 / 8;
+  return static_cast<int>(ks < 1 ? 1 : (ks > 32 ? 32 : ks));
+}
+
+hipError_t launch_down(DownJobs jobs, int64_t n, int rp, hipStream_t s) {
+  for (DownJob& j : jobs.job) j.wgs = j.X != nullptr ? static_cast<unsigned>((n + 31) / 32 * j.ks) : 0;
+  const dim3 grid(jobs.job[0].wgs + jobs.job[1].wgs);
+#define LQ_DOWN(NT) LQ_LAUNCH("adapter_down", (down_kernel<NT>), grid, dim3(kThreads), 0, s, jobs, n)
+  LQ_BY_RANK(rp, LQ_DOWN)
+#undef LQ_DOWN
+  return hipGetLastError();
+}
+
+hipError_t launch_down_sum(DownSumJobs jobs, int64_t n, int r, int rp, hipStream_t s) {
+  for (DownSumJob& j : jobs.job) j.wgs = j.partials != nullptr ? static_cast<unsigned>((n + 31) / 32) : 0;
+  LQ_LAUNCH("adapter_down_sum", down_sum_kernel, dim3(jobs.job[0].wgs + jobs.job[1].wgs), dim3(kThreads), 0, s, jobs, n, r,
+            rp, adapter_ld(rp), (n + 31) / 32 * 32);
+  return hipGetLastError();
+}
+
+int grad_splits(int64_t n, int64_t rows_pad, int64_t cols) {
+  // about two workgroups per CU for the two gradients, each with at least 128 tokens (a step per wave)
+  const int64_t groups = (rows_pad + 127) / 128 + (cols + 127) / 128;
+  int64_t ts = groups > 0 ? 512 / groups : 1;
+  const int64_t most = (n + 127) / 128;
+  if (ts > most) ts = most;
+  return static_cast<int>(ts < 1 ? 1 : (ts > 16 ? 16 : ts));
+}
+
+hipError_t launch_grad(GradJobs jobs, int64_t n, int r, int rp, hipStream_t s) {
+  for (GradJob& j : jobs.job) j.wgs = static_cast<unsigned>((j.F + 127) / 128 * j.ts);
+  const dim3 grid(jobs.job[0].wgs + jobs.job[1].wgs);
+#define LQ_GRAD(NT) \
+  LQ_LAUNCH("adapter_grad", (grad_kernel<NT>), grid, dim3(kThreads), 0, s, jobs, n, (n + 31) / 32 * 32, r)
+  LQ_BY_RANK(rp, LQ_GRAD)
+#undef LQ_GRAD
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_sum(const GradJobs& jobs, int r, int rp, hipStream_t s) {
+  const dim3 grid(blocks_for(jobs.job[0].nf * r) + blocks_for(jobs.job[1].nf * r));
+  LQ_LAUNCH("adapter_grad_sum", grad_sum_kernel, grid, dim3(kThreads), 0, s, jobs, r, rp);
   return hipGetLastError();
 }
 

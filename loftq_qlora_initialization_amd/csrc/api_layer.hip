@@ -61,9 +61,9 @@ ForwardSpace forward_space(void* ws, i64 n, i64 rows, i64 cols, int r, bool mx) 
 
 struct BackwardSpace {
   __bf16 *G, *Wt, *Ab, *At, *Bt, *Ht, *Pt, *Ps;
-  float* partials;   // of one thin product at a time
-  float* joins;      // of the product's K ranges
-  int ks_h, ks_p, ts_b, ts_a;
+  float *down_p, *down_h, *grad_b, *grad_a;   // partial sums of the thin products
+  float* joins;                               // of the product's K ranges
+  int ks_p, ks_h, ts;
   size_t bytes;
 };
 
@@ -71,37 +71,38 @@ BackwardSpace backward_space(void* ws, i64 n, i64 rows, i64 cols, int r) {
   Arena a{static_cast<char*>(ws)};
   BackwardSpace f{};
   const i64 rows_pad = pad_to(rows, 64), n_pad = pad_to(n, 32);
+  const int rp = rank_pad(r);
   if (rows_pad != rows) f.G = a.take<__bf16>(n * rows_pad);
   f.Wt = a.take<__bf16>(cols * rows_pad);
   if (r > 0) {
-    const int rp = rank_pad(r);
     f.ks_h = down_splits(n, cols);
     f.ks_p = down_splits(n, rows_pad);
-    f.ts_b = grad_splits(n, rows_pad);
-    f.ts_a = grad_splits(n, cols);
+    f.ts = grad_splits(n, rows_pad, cols);
     f.Ab = a.take<__bf16>(rp * cols);
     f.At = a.take<__bf16>(cols * adapter_ld(rp));
     f.Bt = a.take<__bf16>(rp * rows_pad);
     f.Ht = a.take<__bf16>(3 * rp * n_pad);
     f.Pt = a.take<__bf16>(3 * rp * n_pad);
     f.Ps = a.take<__bf16>(n * adapter_ld(rp));
-    i64 most = static_cast<i64>(f.ks_h > f.ks_p ? f.ks_h : f.ks_p) * n;
-    if (f.ts_b * rows_pad > most) most = f.ts_b * rows_pad;
-    if (f.ts_a * cols > most) most = f.ts_a * cols;
-    f.partials = a.take<float>(most * rp);
+    f.down_p = a.take<float>(f.ks_p * n * rp);
+    f.down_h = a.take<float>(f.ks_h * n * rp);
+    f.grad_b = a.take<float>(f.ts > 1 ? f.ts * rows_pad * rp : 0);
+    f.grad_a = a.take<float>(f.ts > 1 ? f.ts * cols * rp : 0);
   }
-  f.joins = a.take<float>(plan_tile_product(n, cols, static_cast<int>(rows_pad / 64),
-                                            r > 0 ? adapter_ld(rank_pad(r)) / 64 : 0, false).partial_bytes / 4);
+  f.joins = a.take<float>(plan_tile_product(n, cols, static_cast<int>(rows_pad / 64), r > 0 ? adapter_ld(rp) / 64 : 0,
+                                            false).partial_bytes / 4);
   f.bytes = a.used;
   return f;
 }
 
-// Every launch of a call stays below 2^32 work-items.
+// Every launch of a call stays below 2^32 work-items, and so do the element counts that
+// their 32-bit thread numbers run over.
 bool layer_shape_ok(i64 n, i64 rows, i64 cols, int r) {
-  const i64 limit = (i64(1) << 32) - 1024, rp = rank_pad(r), rows_pad = pad_to(rows, 64), n_pad = pad_to(n, 64);
-  return tile_product_shape_ok(n, rows, cols) && tile_product_shape_ok(n, cols, rows_pad) && n_pad * 64 < limit &&
-         rows_pad * (cols / 8 + 8) < limit && n * (rows_pad / 8) < limit && n * mx_steps(cols) * 32 < limit &&
-         (rp + adapter_ld(static_cast<int>(rp))) * (cols + rows_pad) < limit && (rows_pad + cols) * 32 < limit;
+  const i64 limit = (i64(1) << 32) - 4096, rp = rank_pad(r), rows_pad = pad_to(rows, 64);
+  if (!tile_product_shape_ok(n, rows, cols) || !tile_product_shape_ok(n, cols, rows_pad)) return false;
+  const i64 base = rows_pad * (cols / 8 + 16), codes = n * mx_steps(cols) * 32, pad = n * (rows_pad / 8);
+  const i64 operands = (rp + adapter_ld(static_cast<int>(rp))) * (cols + rows_pad);
+  return (base > codes ? base : codes) + pad + operands < limit && pad_to(n, 64) * 64 < limit;
 }
 
 bool drop_ok(const loftq_dropout_t* d) {
@@ -171,29 +172,34 @@ loftq_status_t layer_forward(const void* X, i64 n, i64 rows, i64 cols, const Bas
   const __bf16* Xb = static_cast<const __bf16*>(X);
   const DropArg d = drop_arg(drop);
   const int rp = rank_pad(r);
-  if (r > 0) {
-    LQ_TRY(launch_adapter_operands(AdapterOperands{A, B, r, rp, rows, cols, rows, f.Ab, nullptr, f.Bb, nullptr,
-                                                  adapter_ld(rp)}, s));
-    LQ_TRY(launch_down(Xb, n, cols, f.Ab, rp, f.ks, d, f.partials, s));
-    LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks, alpha * d.scale, f.S, nullptr, n, s));
-  }
+  PrepareArgs p{};
+  p.a = AdapterOperands{A, B, r, rp, rows, cols, rows, f.Ab, nullptr, f.Bb, nullptr, adapter_ld(rp)};
+  p.n = n;
   TileProduct t{};
   t.M = n;
   t.N = rows;
   if (mx) {
-    LQ_TRY(launch_mx_quantize(Xb, LOFTQ_BF16, n, cols, nullptr, nullptr, 0, f.xq, f.xs, s));
+    p.x = Xb;
+    p.xq = f.xq;
+    p.xs = f.xs;
+    p.steps = mx_steps(cols);
     t.W = base.packed;
     t.X = f.xq;
-    t.steps = static_cast<int>(mx_steps(cols));
+    t.steps = static_cast<int>(p.steps);
     t.ldw = t.ldx = t.steps * i64(kMxStep / 2);
     t.wscale = base.mx;
     t.xscale = f.xs;
   } else {
-    LQ_TRY(launch_base_bf16(base, rows, cols, f.W, s));
+    p.base = f.W;
     t.W = f.W;
     t.X = Xb;
     t.steps = static_cast<int>(cols / 64);
     t.ldw = t.ldx = cols * 2;
+  }
+  LQ_TRY(launch_prepare(p, base, mx ? kBaseCodesOfX : kBaseAsItLies, s));
+  if (r > 0) {
+    LQ_TRY(launch_down(DownJobs{{{Xb, f.Ab, f.partials, cols, f.ks, 0, d}, {}}}, n, rp, s));
+    LQ_TRY(launch_down_sum(DownSumJobs{{{f.partials, f.ks, alpha * d.scale, f.S, nullptr, 0}, {}}}, n, r, rp, s));
   }
   if (r > 0) {
     t.V = f.Bb;
@@ -220,11 +226,8 @@ loftq_status_t layer_backward(const void* dY, const void* X, i64 n, i64 rows, i6
   if ((dX && !aligned16(dX)) || (dB && (!aligned16(dB) || !aligned16(dA)))) return LOFTQ_ERR_INVALID_ARG;
   if (B == nullptr) r = 0;
   const int rp = rank_pad(r);
-  if (n == 0) {   // sums over no tokens
-    if (dB) {
-      LQ_TRY(launch_grad_sum(nullptr, rows, rows, r, rp, 0, 0.f, false, dB, s));
-      LQ_TRY(launch_grad_sum(nullptr, cols, cols, r, rp, 0, 0.f, true, dA, s));
-    }
+  if (n == 0) {   // sums over no tokens: no partials, so zeros
+    if (dB) LQ_TRY(launch_grad_sum(GradJobs{{{nullptr, nullptr, nullptr, dB, rows, rows}, {nullptr, nullptr, nullptr, dA, cols, cols}}}, r, rp, s));
     return LOFTQ_OK;
   }
   if (!dY || !ws || !aligned16(dY) || !aligned16(ws)) return LOFTQ_ERR_INVALID_ARG;
@@ -233,29 +236,36 @@ loftq_status_t layer_backward(const void* dY, const void* X, i64 n, i64 rows, i6
   if (ws_bytes < f.bytes) return LOFTQ_ERR_WORKSPACE;
   const DropArg d = drop_arg(drop), none = drop_arg(nullptr);
   const float gain = alpha * d.scale;
-  const i64 rows_pad = pad_to(rows, 64), n_pad = pad_to(n, 32);
+  const i64 rows_pad = pad_to(rows, 64);
   const __bf16* G = static_cast<const __bf16*>(dY);
   const __bf16* Xb = static_cast<const __bf16*>(X);
-  if (f.G != nullptr) {
-    LQ_TRY(launch_pad_rows(G, n, rows, rows_pad, f.G, s));
-    G = f.G;
-  }
+  PrepareArgs p{};
+  p.a = AdapterOperands{A, B, r, rp, rows, cols, rows_pad, dB ? f.Ab : nullptr, dX ? f.At : nullptr, nullptr, f.Bt,
+                        adapter_ld(rp)};
+  p.base = f.Wt;
+  p.n = n;
+  p.x = G;
+  p.padded = f.G;
+  LQ_TRY(launch_prepare(p, base, dX ? kBaseTransposed : kBaseNone, s));
+  if (f.G != nullptr) G = f.G;
   if (r > 0) {
-    LQ_TRY(launch_adapter_operands(AdapterOperands{A, B, r, rp, rows, cols, rows_pad, f.Ab, f.At, nullptr, f.Bt,
-                                                  adapter_ld(rp)}, s));
-    LQ_TRY(launch_down(G, n, rows_pad, f.Bt, rp, f.ks_p, none, f.partials, s));
-    LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks_p, gain, f.Ps, f.Pt, n_pad, s));
+    // P = G B for dX and dA, H = keep(X) A^T for dB
+    DownJobs down{{{G, f.Bt, f.down_p, rows_pad, f.ks_p, 0, none}, {}}};
+    DownSumJobs sum{{{f.down_p, f.ks_p, gain, dX ? f.Ps : nullptr, dB ? f.Pt : nullptr, 0}, {}}};
     if (dB) {
-      LQ_TRY(launch_grad(Xb, n, cols, f.Pt, rp, n_pad, f.ts_a, d, f.partials, s));
-      LQ_TRY(launch_grad_sum(f.partials, cols, cols, r, rp, f.ts_a, gain, true, dA, s));
-      LQ_TRY(launch_down(Xb, n, cols, f.Ab, rp, f.ks_h, d, f.partials, s));
-      LQ_TRY(launch_down_sum(f.partials, n, r, rp, f.ks_h, gain, nullptr, f.Ht, n_pad, s));
-      LQ_TRY(launch_grad(G, n, rows_pad, f.Ht, rp, n_pad, f.ts_b, none, f.partials, s));
-      LQ_TRY(launch_grad_sum(f.partials, rows_pad, rows, r, rp, f.ts_b, gain, false, dB, s));
+      down.job[1] = DownJob{Xb, f.Ab, f.down_h, cols, f.ks_h, 0, d};
+      sum.job[1] = DownSumJob{f.down_h, f.ks_h, gain, nullptr, f.Ht, 0};
+    }
+    LQ_TRY(launch_down(down, n, rp, s));
+    LQ_TRY(launch_down_sum(sum, n, r, rp, s));
+    if (dB) {
+      const GradJobs grad{{{G, f.Ht, f.grad_b, dB, rows_pad, rows, f.ts, gain, 0, none},
+                           {Xb, f.Pt, f.grad_a, dA, cols, cols, f.ts, gain, 0, d}}};
+      LQ_TRY(launch_grad(grad, n, r, rp, s));
+      if (f.ts > 1) LQ_TRY(launch_grad_sum(grad, r, rp, s));
     }
   }
   if (!dX) return LOFTQ_OK;
-  LQ_TRY(launch_base_bf16_t(base, rows, cols, rows_pad, f.Wt, s));
   TileProduct t{};
   t.W = f.Wt;
   t.X = G;

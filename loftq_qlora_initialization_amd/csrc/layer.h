@@ -60,31 +60,70 @@ struct AdapterOperands {
 };
 // elements of a row of the adapter's operands in the tiled product: three times the padded rank, in whole steps
 inline int adapter_ld(int rp) { return (3 * rp + 63) / 64 * 64; }
-hipError_t launch_adapter_operands(const AdapterOperands& a, hipStream_t s);
 
-// P = keep(X) M^T as K-split partials [ks][n][rp]; then the sum in split order as three
-// bf16 pieces, of gain P token-major in S [n][adapter_ld(rp)], of P rank-major in
-// St [3][rp][n_pad] (either may be null).
+
+// What a call's products read: the base's bf16 operand (as it lies, or transposed with zeros
+// past `rows`), or over MXFP4 the codes of X; the adapter's operands; dY with padded rows.
+enum PrepareBase { kBaseNone, kBaseAsItLies, kBaseTransposed, kBaseCodesOfX };
+struct PrepareArgs {
+  AdapterOperands a;       // r = 0: no adapter (rows, cols, rows_pad still hold)
+  __bf16* base;
+  int64_t n;               // tokens
+  const __bf16* x;         // X for its codes, dY for its padding
+  uint8_t *xq, *xs;        // X's codes and scales
+  int64_t steps;           // mx_steps(cols)
+  __bf16* padded;          // dY in rows of rows_pad, or null
+  unsigned base_wgs, operand_wgs;   // set by the launcher
+};
+hipError_t launch_prepare(PrepareArgs p, const Base4& b, PrepareBase kind, hipStream_t s);
+
+// P = keep(X) M^T as K-split partials [ks][n][rp] (X null: no such job); then the sum in split
+// order as three bf16 pieces, of gain P token-major in S [n][adapter_ld(rp)], of P rank-major
+// in St [3][rp][n_pad] (either may be null; n_pad = n in whole 32s).
+struct DownJob {
+  const __bf16 *X, *M;
+  float* out;
+  int64_t K;
+  int ks;
+  unsigned wgs;            // set by the launcher
+  DropArg drop;
+};
+struct DownJobs {
+  DownJob job[2];
+};
+struct DownSumJob {
+  const float* partials;
+  int ks;
+  float gain;
+  __bf16 *S, *St;
+  unsigned wgs;            // set by the launcher
+};
+struct DownSumJobs {
+  DownSumJob job[2];
+};
 int down_splits(int64_t n, int64_t K);
-hipError_t launch_down(const __bf16* X, int64_t n, int64_t K, const __bf16* Mb, int rp, int ks, const DropArg& drop,
-                       float* partials, hipStream_t s);
-hipError_t launch_down_sum(const float* partials, int64_t n, int r, int rp, int ks, float gain, __bf16* S, __bf16* St,
-                           int64_t n_pad, hipStream_t s);
+hipError_t launch_down(DownJobs jobs, int64_t n, int rp, hipStream_t s);
+hipError_t launch_down_sum(DownSumJobs jobs, int64_t n, int r, int rp, hipStream_t s);
 
-// out[i][p] = coef sum_t keep(L)[t][i] (fp32 value of St)[p][t], over ts token ranges.
-int grad_splits(int64_t n, int64_t F);
-hipError_t launch_grad(const __bf16* L, int64_t n, int64_t F, const __bf16* St, int rp, int64_t n_pad, int ts,
-                       const DropArg& drop, float* partials, hipStream_t s);
-// the sum of the partials as out[i r + p] (rank_major false) or out[p nf + i], i < nf
-hipError_t launch_grad_sum(const float* partials, int64_t F, int64_t nf, int r, int rp, int ts, float coef,
-                           bool rank_major, float* out, hipStream_t s);
-
-// bf16(deq) of the base: [rows][cols], or transposed [cols][rows_pad] with zeros past `rows`.
-hipError_t launch_base_bf16(const Base4& b, int64_t rows, int64_t cols, __bf16* out, hipStream_t s);
-hipError_t launch_base_bf16_t(const Base4& b, int64_t rows, int64_t cols, int64_t rows_pad, __bf16* out,
-                              hipStream_t s);
-// rows of `cols` elements into rows of `ld` with zeros past `cols`
-hipError_t launch_pad_rows(const __bf16* src, int64_t n, int64_t cols, int64_t ld, __bf16* dst, hipStream_t s);
+// out[i][p] = coef sum_t keep(L)[t][i] (fp32 value of St)[p][t] for i < nf, p < r: job 0 (dB)
+// feature-major over dY, job 1 (dA) rank-major over X with its mask.  L has F >= nf columns.
+// Over ts > 1 token ranges the sums go to `partials` ([ts][F][rp], [ts][rp][F]) and
+// launch_grad_sum adds them; over one they are written to `out` at once.
+struct GradJob {
+  const __bf16 *L, *St;
+  float *partials, *out;
+  int64_t F, nf;
+  int ts;
+  float coef;
+  unsigned wgs;            // set by the launcher
+  DropArg drop;
+};
+struct GradJobs {
+  GradJob job[2];
+};
+int grad_splits(int64_t n, int64_t rows_pad, int64_t cols);
+hipError_t launch_grad(GradJobs jobs, int64_t n, int r, int rp, hipStream_t s);
+hipError_t launch_grad_sum(const GradJobs& jobs, int r, int rp, hipStream_t s);
 
 // ---- MXFP4 (mxfp4_kernels.hip) ----
 bool mx_shape_ok(int64_t rows, int64_t cols);

@@ -38,12 +38,30 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
                                                                    : __uint_as_float(byte << 23));
 }
 
-// e2m1 code of x: nearest magnitude of {0, .5, 1, 1.5, 2, 3, 4, 6}, ties to the even
-// code, larger magnitudes to 6.
-__device__ __forceinline__ uint32_t fp4_code(float x) {
-  const float m = fabsf(x);
-  const uint32_t c = (m > 0.25f) + (m >= 0.75f) + (m > 1.25f) + (m >= 1.75f) + (m > 2.5f) + (m >= 3.5f) + (m > 5.f);
-  return c | (__float_as_uint(x) >> 28 & 8u);
+// Eight consecutive values of a row (columns c0 .. c0 + 7 of the padded matrix) into a word of
+// codes; the four lanes of a quad hold one block and exchange its largest magnitude by two quad
+// permutes.  The conversion instruction rounds to the nearest e2m1 value, ties to the even code,
+// and takes larger magnitudes to 6; the scale is applied before it, exactly, since the
+// instruction's own scale does not reach 2^-127.
+__device__ __forceinline__ uint32_t mx_encode8(const float (&x)[8], uint32_t& byte) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const uint32_t b = __float_as_uint(x[j]) & 0x7FFFFFFFu;
+    amax = b > amax ? b : amax;
+  }
+  const uint32_t o1 = __builtin_amdgcn_mov_dpp(amax, 0xB1, 0xF, 0xF, true);   // quad_perm 1,0,3,2
+  amax = o1 > amax ? o1 : amax;
+  const uint32_t o2 = __builtin_amdgcn_mov_dpp(amax, 0x4E, 0xF, 0xF, true);   // quad_perm 2,3,0,1
+  amax = o2 > amax ? o2 : amax;
+  byte = mx_scale_byte(amax);
+  const float inv = mx_inverse_scale(byte);
+  uint32_t word = 0;   // the instruction puts its first value into the low nibble
+  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, x[1] * inv, x[0] * inv, 1.f, 0);
+  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, x[3] * inv, x[2] * inv, 1.f, 1);
+  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, x[5] * inv, x[4] * inv, 1.f, 2);
+  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, x[7] * inv, x[6] * inv, 1.f, 3);
+  return word;
 }
 __device__ __forceinline__ float fp4_value(uint32_t code) {
   // magnitude code 0: 0, 1: 0.5, else (1 + m / 2) 2^(e - 1) with e = code >> 1 & 3, m = code & 1

@@ -7,9 +7,8 @@ namespace {
 
 constexpr int kMxThreads = 256;
 
-// One thread per 8 consecutive columns of the padded matrix; the four lanes of a quad
-// hold one block and exchange its largest magnitude by two quad permutes.  kVec: cols %
-// 8 == 0, so eight elements are 16-byte loads; otherwise they are loaded one by one.
+// One thread per 8 consecutive columns of the padded matrix.  kVec: cols % 8 == 0, so eight
+// elements are 16-byte loads; otherwise they are loaded one by one.
 // R = W - B A is formed in fp32, the r products added in the order of p.
 template <typename T, bool kVec>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __restrict__ W, int64_t rows, int64_t cols,
@@ -17,10 +16,10 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __rest
                                                                  const float* __restrict__ A, int r,
                                                                  uint8_t* __restrict__ packed,
                                                                  uint8_t* __restrict__ scales) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kMxThreads + threadIdx.x;
-  const int64_t per_row = steps * (kMxStep / 8);
-  if (id >= rows * per_row) return;   // whole quads: per_row % 32 == 0
-  const int64_t row = id / per_row, c0 = (id - row * per_row) * 8;
+  const uint32_t id = blockIdx.x * kMxThreads + threadIdx.x;   // below 2^32
+  const uint32_t per_row = static_cast<uint32_t>(steps * (kMxStep / 8));
+  const int64_t row = id / per_row, c0 = static_cast<int64_t>(id % per_row) * 8;
+  if (row >= rows) return;   // whole quads: per_row % 32 == 0
   float x[8];
   if (kVec) {
     if (c0 < cols) {
@@ -47,21 +46,8 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __rest
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] -= ba[j];
   }
-  uint32_t amax = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    const uint32_t b = __float_as_uint(x[j]) & 0x7FFFFFFFu;
-    amax = b > amax ? b : amax;
-  }
-  const uint32_t o1 = __builtin_amdgcn_mov_dpp(amax, 0xB1, 0xF, 0xF, true);   // quad_perm 1,0,3,2
-  amax = o1 > amax ? o1 : amax;
-  const uint32_t o2 = __builtin_amdgcn_mov_dpp(amax, 0x4E, 0xF, 0xF, true);   // quad_perm 2,3,0,1
-  amax = o2 > amax ? o2 : amax;
-  const uint32_t byte = mx_scale_byte(amax);
-  const float inv = mx_inverse_scale(byte);
-  uint32_t word = 0;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) word |= fp4_code(x[j] * inv) << (8 * (j >> 1) + (j & 1 ? 0 : 4));
+  uint32_t byte;
+  const uint32_t word = mx_encode8(x, byte);
   reinterpret_cast<uint32_t*>(packed)[id] = word;
   if ((threadIdx.x & 3) == 0) {
     const int64_t k = c0 / kMxStep;
@@ -75,10 +61,10 @@ __global__ __launch_bounds__(kMxThreads) void mx_dequantize_kernel(const uint8_t
                                                                    const uint8_t* __restrict__ scales, int64_t rows,
                                                                    int64_t cols, int64_t steps,
                                                                    const T* __restrict__ W, O* __restrict__ out) {
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kMxThreads + threadIdx.x;
-  const int64_t per_row = (cols + 7) / 8;
-  if (id >= rows * per_row) return;
-  const int64_t row = id / per_row, c0 = (id - row * per_row) * 8;
+  const uint32_t id = blockIdx.x * kMxThreads + threadIdx.x;   // below 2^32
+  const uint32_t per_row = static_cast<uint32_t>((cols + 7) / 8);
+  const int64_t row = id / per_row, c0 = static_cast<int64_t>(id % per_row) * 8;
+  if (row >= rows) return;
   const uint32_t word = *reinterpret_cast<const uint32_t*>(packed + row * steps * (kMxStep / 2) + c0 / 2);
   const float sc = mx_scale(scales[(c0 / kMxStep * rows + row) * 8 + (c0 % kMxStep) / kMxBlock]);
   float v[8];
