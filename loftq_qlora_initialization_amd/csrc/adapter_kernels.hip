@@ -213,7 +213,7 @@ __device__ __forceinline__ u32x4 drop8(u32x4 v, uint64_t key, uint64_t e, uint32
 // tokens zeroed.  The waves' sums meet in LDS.
 template <int NT>
 __global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n) {
-  constexpr int U = 2;
+  constexpr int U = NT <= 2 ? 4 : 2;
   __shared__ float part[3][2 * NT * 4 * 64];
   const DownJob& jb = jobs.job[blockIdx.x < jobs.job[0].wgs ? 0 : 1];
   const uint32_t wg = blockIdx.x < jobs.job[0].wgs ? blockIdx.x : blockIdx.x - jobs.job[0].wgs;
@@ -280,8 +280,8 @@ __global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n
 // The sum of the partials in split order, as three bf16 pieces x = h0 + h1 + h2 (each the
 // rounding of what the ones before leave: the three hold 24 bits, so the products they
 // enter lose nothing against fp32; an infinity or NaN is all in the first).  Ranks past r
-// and tokens past n are zeros.  A workgroup takes 32 tokens; the rank-major form is turned
-// round in LDS.
+// and tokens past n are zeros.  A workgroup takes 32 tokens and 16 ranks; the rank-major
+// form is turned round in LDS.
 __device__ __forceinline__ void split3(float x, __bf16 (&h)[3]) {
 #pragma unroll
   for (int q = 0; q < 3; ++q) {
@@ -291,12 +291,14 @@ __device__ __forceinline__ void split3(float x, __bf16 (&h)[3]) {
 }
 __global__ __launch_bounds__(kThreads) void down_sum_kernel(DownSumJobs jobs, int64_t n, int r, int rp, int ld,
                                                             int64_t n_pad) {
-  __shared__ __bf16 turned[3 * 64][32 + 2];
+  __shared__ __align__(4) __bf16 turned[3 * 16][32 + 2];
   const DownSumJob& jb = jobs.job[blockIdx.x < jobs.job[0].wgs ? 0 : 1];
   const uint32_t wg = blockIdx.x < jobs.job[0].wgs ? blockIdx.x : blockIdx.x - jobs.job[0].wgs;
-  const int64_t m0 = static_cast<int64_t>(wg) * 32;
-  for (int i = threadIdx.x; i < 32 * rp; i += kThreads) {
-    const int tok = i / rp, p = i - tok * rp;
+  const int parts = rp / 16, p0 = static_cast<int>(wg % parts) * 16;
+  const int64_t m0 = static_cast<int64_t>(wg / parts) * 32;
+#pragma unroll
+  for (int i = threadIdx.x; i < 32 * 16; i += kThreads) {
+    const int tok = i / 16, p = p0 + i % 16;
     const int64_t m = m0 + tok;
     float x = 0.f;
     if (m < n && p < r) {
@@ -318,14 +320,15 @@ __global__ __launch_bounds__(kThreads) void down_sum_kernel(DownSumJobs jobs, in
     if (jb.St != nullptr) {
       split3(x, h);
 #pragma unroll
-      for (int q = 0; q < 3; ++q) turned[q * rp + p][tok] = h[q];
+      for (int q = 0; q < 3; ++q) turned[q * 16 + i % 16][tok] = h[q];
     }
   }
   if (jb.St == nullptr) return;
   __syncthreads();
-  for (int i = threadIdx.x; i < 3 * rp * 16; i += kThreads) {   // two tokens a store
-    const int p = i / 16, t = (i % 16) * 2;
-    *reinterpret_cast<uint32_t*>(jb.St + p * n_pad + m0 + t) = *reinterpret_cast<const uint32_t*>(&turned[p][t]);
+  for (int i = threadIdx.x; i < 3 * 16 * 16; i += kThreads) {   // two tokens a store
+    const int row = i / 16, t = (i % 16) * 2;
+    *reinterpret_cast<uint32_t*>(jb.St + (row / 16 * rp + p0 + row % 16) * n_pad + m0 + t) =
+        *reinterpret_cast<const uint32_t*>(&turned[row][t]);
   }
 }
 
@@ -333,14 +336,17 @@ __global__ __launch_bounds__(kThreads) void down_sum_kernel(DownSumJobs jobs, in
 // out[i][p] = sum_t keep(L)[t][i] S[t][p].  The matrix cores want each operand's K (tokens) in
 // one lane, and L's tokens are rows: lane L loads 8 tokens x 8 features (16 bytes of 8
 // rows) and turns the 8 x 8 block round in its registers, which gives the operands of 8
-// products, the j-th for features 8 (L%16) + j.  A workgroup takes 128 features; its four
-// waves share a token range 32 tokens at a time, the next step's loads in flight while one
-// is multiplied, and their sums meet in LDS.  kRankMajor (dA): S is the first operand, so a
+// products, the j-th for features 8 (L%16) + j.  A workgroup takes 128 features and a token
+// range, which its four waves share 32 tokens at a time, the next step's loads in flight
+// while one is multiplied; past 32 ranks two waves share a step, half of the ranks each (the
+// sums of all of them leave a wave no registers for its loads).  The sums meet in LDS.  kRankMajor (dA): S is the first operand, so a
 // lane holds 8 consecutive features of a rank; else (dB) a lane's rank is L%16.
-template <int NT, bool kRankMajor>
+template <int NR, bool kRankMajor>
 __device__ __forceinline__ void grad_job(const GradJob& jb, uint32_t wg, int64_t n, int64_t n_pad, int r,
-                                         float (*part)[8 * NT * 4 * 64]) {
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
+                                         float (*part)[8 * (NR > 2 ? 2 : NR) * 4 * 64]) {
+  constexpr int kParts = NR > 2 ? 2 : 1, NT = NR > 2 ? 2 : NR, kWaves = 4 / kParts;   // waves per step's ranks, of a rank half
+  const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
+  const int half = (threadIdx.x >> 6) % kParts, w = (threadIdx.x >> 6) / kParts, tile0 = half * NT;
   const int64_t group = wg / jb.ts, F = jb.F;
   const int q = wg % jb.ts;
   const int64_t f0 = group * 128 + 8 * li, f = f0 < F ? f0 : F - 8;   // F % 8 == 0
@@ -353,27 +359,22 @@ __device__ __forceinline__ void grad_job(const GradJob& jb, uint32_t wg, int64_t
   for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  // S's operands are loaded ahead too where the registers allow it
-  constexpr int kSets = NT <= 2 ? 2 : 1;
-  u32x4 x[2][8], b[kSets][3][NT];
-  auto load_s = [&](int set, int s) __attribute__((always_inline)) {
-    const int64_t t0 = static_cast<int64_t>(s < end ? s : end - 1) * 32 + 8 * lg;
-#pragma unroll
-    for (int h = 0; h < 3; ++h)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-        b[set % kSets][h][t] = *reinterpret_cast<const u32x4*>(jb.St + (h * 16 * NT + t * 16 + li) * n_pad + t0);
-  };
+  u32x4 x[2][8], b[2][3][NT];
   auto load = [&](int set, int s) __attribute__((always_inline)) {
     const int64_t t0 = static_cast<int64_t>(s < end ? s : end - 1) * 32 + 8 * lg;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
       x[set][i] = *reinterpret_cast<const u32x4*>(jb.L + (t0 + i < n ? t0 + i : n - 1) * F + f);
-    if (kSets == 2) load_s(set, s);
+#pragma unroll
+    for (int h = 0; h < 3; ++h)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {   // of an odd number of rank tiles the last half's second repeats the first
+        const int tile = tile0 + t < NR ? tile0 + t : tile0;
+        b[set][h][t] = *reinterpret_cast<const u32x4*>(jb.St + (h * 16 * NR + tile * 16 + li) * n_pad + t0);
+      }
   };
   auto multiply = [&](int set, int s) __attribute__((always_inline)) {
     const int64_t t0 = static_cast<int64_t>(s) * 32 + 8 * lg;
-    if (kSets == 1) load_s(set, s);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if (t0 + i >= n) x[set][i] = u32x4{0u, 0u, 0u, 0u};
@@ -391,72 +392,73 @@ __device__ __forceinline__ void grad_job(const GradJob& jb, uint32_t wg, int64_t
       for (int h = 0; h < 3; ++h)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          acc[2 * c][t] = kRankMajor ? mfma16(b[set % kSets][h][t], lo, acc[2 * c][t])
-                                     : mfma16(lo, b[set % kSets][h][t], acc[2 * c][t]);
+          acc[2 * c][t] = kRankMajor ? mfma16(b[set][h][t], lo, acc[2 * c][t])
+                                     : mfma16(lo, b[set][h][t], acc[2 * c][t]);
           acc[2 * c + 1][t] =
-              kRankMajor ? mfma16(b[set % kSets][h][t], hi, acc[2 * c + 1][t])
-                         : mfma16(hi, b[set % kSets][h][t], acc[2 * c + 1][t]);
+              kRankMajor ? mfma16(b[set][h][t], hi, acc[2 * c + 1][t])
+                         : mfma16(hi, b[set][h][t], acc[2 * c + 1][t]);
         }
     }
   };
   if (begin + w < end) {
     load(0, begin + w);
-    for (int s = begin + w; s < end; s += 8) {
-      load(1, s + 4);
+    for (int s = begin + w; s < end; s += 2 * kWaves) {
+      load(1, s + kWaves);
       multiply(0, s);
-      if (s + 4 >= end) break;
-      load(0, s + 8);
-      multiply(1, s + 4);
+      if (s + kWaves >= end) break;
+      load(0, s + 2 * kWaves);
+      multiply(1, s + kWaves);
     }
   }
-  // waves 2 and 3 park their sums, 0 and 1 add them; then 1 parks and 0 adds
+  // of four waves 2 and 3 park their sums, 0 and 1 add them; then 1 parks and 0 adds
   auto at = [&](int j, int t, int v) { return ((j * NT + t) * 4 + v) * 64 + lane; };
-  if (w >= 2)
+  auto park = [&](float* to) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) part[w - 2][at(j, t, v)] = acc[j][t][v];
-  __syncthreads();
-  if (w < 2)
+        for (int v = 0; v < 4; ++v) to[at(j, t, v)] = acc[j][t][v];
+  };
+  auto add = [&](const float* from) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
 #pragma unroll
       for (int t = 0; t < NT; ++t)
 #pragma unroll
-        for (int v = 0; v < 4; ++v) acc[j][t][v] += part[w][at(j, t, v)];
-  __syncthreads();
-  if (w == 1)
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-#pragma unroll
-      for (int t = 0; t < NT; ++t)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) part[0][at(j, t, v)] = acc[j][t][v];
+        for (int v = 0; v < 4; ++v) acc[j][t][v] += from[at(j, t, v)];
+  };
+  if constexpr (kWaves == 4) {
+    if (w >= 2) park(part[w - 2]);
+    __syncthreads();
+    if (w < 2) add(part[w]);
+    __syncthreads();
+  }
+  if (w == 1) park(part[half]);
   __syncthreads();
   if (w != 0) return;
+  add(part[half]);
   // one range: the gradient itself; more: a partial sum with whole padded ranks and features
   const bool whole = jb.ts == 1;
   const int64_t nf = whole ? jb.nf : F;
-  const int nr = whole ? r : 16 * NT;
+  const int nr = whole ? r : 16 * NR;
   const float coef = whole ? jb.coef : 1.f;
-  float* o = whole ? jb.out : jb.partials + static_cast<int64_t>(q) * F * (16 * NT);
+  float* o = whole ? jb.out : jb.partials + static_cast<int64_t>(q) * F * (16 * NR);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int v = 0; v < 4; ++v) {
       float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = coef * (acc[j][t][v] + part[0][at(j, t, v)]);
+      for (int j = 0; j < 8; ++j) y[j] = coef * acc[j][t][v];
       if constexpr (kRankMajor) {
-        const int p = t * 16 + 4 * lg + v;   // features f0 .. f0 + 7
+        const int p = (tile0 + t) * 16 + 4 * lg + v;   // features f0 .. f0 + 7
         if (p < nr && f0 < F)                // nf == F here, and 8 | F
 #pragma unroll
           for (int h = 0; h < 2; ++h)
             *reinterpret_cast<f32x4*>(o + p * nf + f0 + 4 * h) = f32x4{y[4 * h], y[4 * h + 1], y[4 * h + 2], y[4 * h + 3]};
       } else {
-        const int p = t * 16 + li;
+        const int p = (tile0 + t) * 16 + li;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const int64_t i = group * 128 + 8 * (4 * lg + v) + j;
@@ -469,7 +471,7 @@ __device__ __forceinline__ void grad_job(const GradJob& jb, uint32_t wg, int64_t
 // job 0: dB over dY; job 1: dA over X
 template <int NT>
 __global__ __launch_bounds__(kThreads) void grad_kernel(GradJobs jobs, int64_t n, int64_t n_pad, int r) {
-  __shared__ float part[2][8 * NT * 4 * 64];
+  __shared__ float part[2][8 * (NT > 2 ? 2 : NT) * 4 * 64];
   if (blockIdx.x < jobs.job[0].wgs)
     grad_job<NT, false>(jobs.job[0], blockIdx.x, n, n_pad, r, part);
   else
@@ -538,9 +540,9 @@ hipError_t launch_prepare(PrepareArgs p, const Base4& b, PrepareBase kind, hipSt
   }
 
 int down_splits(int64_t n, int64_t K) {
-  // about two workgroups per CU, each with at least 8 steps (two per wave)
+  // about four workgroups per CU, each with at least 8 steps (two per wave)
   const int64_t groups = n > 32 ? (n + 31) / 32 : 1;
-  int64_t ks = 512 / groups;
+  int64_t ks = 1024 / groups;
   if (ks > K / 32 / 8) ks = K / 32 / 8;
   return static_cast<int>(ks < 1 ? 1 : (ks > 32 ? 32 : ks));
 }
@@ -555,14 +557,14 @@ hipError_t launch_down(DownJobs jobs, int64_t n, int rp, hipStream_t s) {
 }
 
 hipError_t launch_down_sum(DownSumJobs jobs, int64_t n, int r, int rp, hipStream_t s) {
-  for (DownSumJob& j : jobs.job) j.wgs = j.partials != nullptr ? static_cast<unsigned>((n + 31) / 32) : 0;
+  for (DownSumJob& j : jobs.job) j.wgs = j.partials != nullptr ? static_cast<unsigned>((n + 31) / 32 * (rp / 16)) : 0;
   LQ_LAUNCH("adapter_down_sum", down_sum_kernel, dim3(jobs.job[0].wgs + jobs.job[1].wgs), dim3(kThreads), 0, s, jobs, n, r,
             rp, adapter_ld(rp), (n + 31) / 32 * 32);
   return hipGetLastError();
 }
 
 int grad_splits(int64_t n, int64_t rows_pad, int64_t cols) {
-  // about two workgroups per CU for the two gradients, each with at least 128 tokens (a step per wave)
+  // about two workgroups per CU for the two gradients, each with at least 128 tokens
   const int64_t groups = (rows_pad + 127) / 128 + (cols + 127) / 128;
   int64_t ts = groups > 0 ? 512 / groups : 1;
   const int64_t most = (n + 127) / 128;
