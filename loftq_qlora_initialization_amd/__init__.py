@@ -23,5 +23,6 @@ _BINDING_NAMES = {
 
 def __getattr__(name):
     if name in _BINDING_NAMES:
-        return getattr(importlib.import_module(".binding", __name__), name)
+        value = globals()[name] = getattr(importlib.import_module(".binding", __name__), name)
+        return value
     raise AttributeError(name)

@@ -336,142 +336,154 @@ def loftq_qlora_forward_noalloc(X: torch.Tensor, packed: torch.Tensor, shape, ab
 
 # ---- training and serving an adapted layer ----
 
-def _dropout(p, seed, offset, step, X):
-    if step is not None:
-        _expect(step, "step", X, torch.int64, (1,))
-    return LoftqDropout(float(p), int(seed) & (2 ** 64 - 1), int(offset) & (2 ** 64 - 1),
-                        None if step is None else step.data_ptr())
+_M64 = 2 ** 64 - 1
+_FLOATS = (torch.float32, torch.bfloat16)
 
 
-def _expect(t, what, like, dtype, shape=None, least=None):
-    """A contiguous tensor of the given type on `like`'s device, of a shape or of at least so many elements."""
-    _contig(t, what)
-    if t.device != like.device:
-        raise ValueError(f"{what} must be on {like.device}")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise TypeError(f"{what} must be {dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+def _first(t, what):
+    """The tensor that says where a call runs: its device's number."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous device tensor")
+    return t.get_device()
+
+
+def _expect(t, what, dev, dtype, shape=None, least=0):
+    """A contiguous tensor on device `dev` of the given type (None: fp32 or bf16) and of a shape or of at least so
+    many elements; its address."""
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous device tensor")
+    if t.get_device() != dev:
+        raise ValueError(f"{what} must be on device {dev}")
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in _FLOATS):
+        raise TypeError(f"{what} must be {dtype or 'float32 or bfloat16'}")
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{what} must have the shape {tuple(shape)}")
-    if least is not None and t.numel() < least:
+    if t.numel() < least:
         raise ValueError(f"{what} must hold {least} elements")
-    return t
+    return t.data_ptr()
 
 
-def _on(X, stream):
-    """The tensor's device for a call and its stream there (the device's current one by default)."""
-    return torch.cuda.device(X.device), _stream(torch.cuda.current_stream(X.device) if stream is None else stream)
+def _call(name, c_fn, dev, stream, *args):
+    """c_fn on device `dev`, on `stream` or the device's current one."""
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        s = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        st = c_fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = c_fn(*args, s)
+    if st != 0:
+        raise LoftqError(name, st)
+
+
+def _dropout(p, seed, offset, step, dev):
+    at = None if step is None else _expect(step, "step", dev, torch.int64, (1,))
+    if p == 0:
+        return None
+    return ctypes.byref(LoftqDropout(p, seed & _M64, offset & _M64, at))
 
 
 def _out_dtype(t, dtype):
     dtype = t.dtype if t is not None else dtype
-    if dtype not in (torch.float32, torch.bfloat16):
+    if dtype not in _FLOATS:
         raise TypeError("outputs are float32 or bfloat16")
     return dtype
 
 
-def _nf_args(X, packed, rows, cols, absmax, qabsmax, dq_scale, bits):
+def _nf_args(dev, packed, rows, cols, absmax, qabsmax, dq_scale, bits):
     nb = (rows * cols + 63) // 64
-    _expect(packed, "packed", X, torch.uint8, least=(rows * cols + 1) // 2)
+    at = _expect(packed, "packed", dev, torch.uint8, least=(rows * cols + 1) // 2)
     if qabsmax is not None or dq_scale is not None:
         if qabsmax is None or dq_scale is None:
             raise ValueError("qabsmax and dq_scale are given together")
-        _expect(qabsmax, "qabsmax", X, torch.int8, least=nb)
-        _expect(dq_scale, "dq_scale", X, torch.float32, least=(nb + 255) // 256)
-    elif absmax is None:
+        return (at, None, _expect(qabsmax, "qabsmax", dev, torch.int8, least=nb),
+                _expect(dq_scale, "dq_scale", dev, torch.float32, least=(nb + 255) // 256), bits)
+    if absmax is None:
         raise ValueError("absmax, or qabsmax and dq_scale, must be given")
-    else:
-        _expect(absmax, "absmax", X, torch.float32, least=nb)
-    return [_ptr(packed), _ptr(absmax), _ptr(qabsmax), _ptr(dq_scale), int(bits)]
+    return at, _expect(absmax, "absmax", dev, torch.float32, least=nb), None, None, bits
 
 
-def _mx_args(X, packed, scales, rows, cols):
-    _expect(packed, "packed", X, torch.uint8, least=_c_mx_packed(rows, cols))
-    _expect(scales, "scales", X, torch.uint8, least=_c_mx_scales(rows, cols))
-    return [_ptr(packed), _ptr(scales)]
+def _mx_args(dev, packed, scales, rows, cols):
+    steps = (cols + 255) // 256
+    return (_expect(packed, "packed", dev, torch.uint8, least=rows * steps * 128),
+            _expect(scales, "scales", dev, torch.uint8, least=rows * steps * 8))
 
 
-def _adapter_args(X, B, A, rows, cols, alpha, drop):
-    if (B is None) != (A is None):
+def _adapter_args(dev, B, A, rows, cols):
+    """(B, A, r) of a call."""
+    if B is None and A is None:
+        return None, None, 0
+    if B is None or A is None:
         raise ValueError("B and A are given together")
-    r = 0
-    if B is not None:
-        r = B.shape[1] if B.dim() == 2 else -1
-        _expect(B, "B", X, torch.float32, (rows, r))
-        _expect(A, "A", X, torch.float32, (r, cols))
-    return r, [_ptr(B), _ptr(A), r, float(alpha), ctypes.byref(drop)]
+    r = B.shape[1] if B.dim() == 2 else -1
+    return _expect(B, "B", dev, torch.float32, (rows, r)), _expect(A, "A", dev, torch.float32, (r, cols)), r
 
 
-def _workspace(ws, need, X):
+def _workspace(ws, query, sizes, like):
+    """(tensor, its address, its bytes); a new one of the size that `query` names where none is given."""
     if ws is None:
-        ws = torch.empty(max(need, 16), dtype=torch.uint8, device=X.device)
-    _contig(ws, "ws")
-    if ws.device != X.device:
-        raise ValueError(f"ws must be on {X.device}")
-    return ws, ws.numel() * ws.element_size()
+        ws = torch.empty(max(int(query(*sizes)), 16), dtype=torch.uint8, device=like.device)
+    if not ws.is_cuda or not ws.is_contiguous() or ws.get_device() != like.get_device():
+        raise ValueError(f"ws must be a contiguous tensor on {like.device}")
+    return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
 
-def _layer_forward(name, c_fn, c_ws, X, base, rows, cols, B, A, alpha, drop, out, out_dtype, ws, stream):
+def _layer_forward(name, c_fn, query, X, dev, base, rows, cols, B, A, alpha, drop, out, out_dtype, ws, stream):
     n = X.shape[0]
     out_dtype = _out_dtype(out, out_dtype)
-    r, adapter = _adapter_args(X, B, A, rows, cols, alpha, drop)
+    b, a, r = _adapter_args(dev, B, A, rows, cols)
     if out is None:
         out = torch.empty((n, rows), dtype=out_dtype, device=X.device)
-    _expect(out, "out", X, out_dtype, (n, rows))
-    ws, ws_bytes = _workspace(ws, int(c_ws(n, rows, cols, r)), X)
-    device, st = _on(X, stream)
-    with device:
-        _check(name, c_fn(_ptr(X), n, rows, cols, *base, *adapter, _ptr(out), _wdtype(out), _ptr(ws), ws_bytes, st))
+    y = _expect(out, "out", dev, out_dtype, (n, rows))
+    ws, w, ws_bytes = _workspace(ws, query, (n, rows, cols, r), X)
+    _call(name, c_fn, dev, stream, X.data_ptr(), n, rows, cols, *base, b, a, r, alpha, drop, y,
+          LOFTQ_BF16 if out_dtype is torch.bfloat16 else LOFTQ_F32, w, ws_bytes)
     return out
 
 
-def _layer_backward(name, c_fn, c_ws, dY, X, base, rows, cols, B, A, alpha, drop, need_dx, out, dx_dtype, ws, stream):
+def _layer_backward(name, c_fn, query, dY, X, dev, base, rows, cols, B, A, alpha, drop, need_dx, out, dx_dtype, ws,
+                    stream):
     n = dY.shape[0]
-    r, adapter = _adapter_args(dY, B, A, rows, cols, alpha, drop)
-    dX, dB, dA = out if out is not None else (None, None, None)
-    if out is None:
-        if need_dx:
-            dX = torch.empty((n, cols), dtype=_out_dtype(None, dx_dtype), device=dY.device)
-        if B is not None:
-            dB, dA = torch.empty_like(B), torch.empty_like(A)
+    b, a, r = _adapter_args(dev, B, A, rows, cols)
+    if out is not None:
+        dX, dB, dA = out
+    else:
+        dX = torch.empty((n, cols), dtype=_out_dtype(None, dx_dtype), device=dY.device) if need_dx else None
+        dB, dA = (torch.empty_like(B), torch.empty_like(A)) if r else (None, None)
     if X is None and dB is not None:
         raise ValueError("X must be given for dB and dA")
-    if X is not None:
-        _expect(X, "X", dY, torch.bfloat16, (n, cols))
-    if dX is not None:
-        _expect(dX, "dX", dY, (torch.float32, torch.bfloat16), (n, cols))
-    if dB is not None:
-        _expect(dB, "dB", dY, torch.float32, (rows, r))
-    if dA is not None:
-        _expect(dA, "dA", dY, torch.float32, (r, cols))
-    ws, ws_bytes = _workspace(ws, int(c_ws(n, rows, cols, r)), dY)
-    device, st = _on(dY, stream)
-    with device:
-        _check(name, c_fn(_ptr(dY), _ptr(X), n, rows, cols, *base, *adapter, _ptr(dX),
-                          _wdtype(dX) if dX is not None else LOFTQ_BF16, _ptr(dB), _ptr(dA), _ptr(ws), ws_bytes, st))
+    x = None if X is None else _expect(X, "X", dev, torch.bfloat16, (n, cols))
+    gx = None if dX is None else _expect(dX, "dX", dev, None, (n, cols))
+    gb = None if dB is None else _expect(dB, "dB", dev, torch.float32, (rows, r))
+    ga = None if dA is None else _expect(dA, "dA", dev, torch.float32, (r, cols))
+    ws, w, ws_bytes = _workspace(ws, query, (n, rows, cols, r), dY)
+    _call(name, c_fn, dev, stream, dY.data_ptr(), x, n, rows, cols, *base, b, a, r, alpha, drop, gx,
+          LOFTQ_F32 if dX is not None and dX.dtype is torch.float32 else LOFTQ_BF16, gb, ga, w, ws_bytes)
     return dX, dB, dA
 
 
 def _tokens(X, what, width):
-    _contig(X, what)
-    if X.dtype != torch.bfloat16:
+    dev = _first(X, what)
+    if X.dtype is not torch.bfloat16:
         raise TypeError(f"{what} must be bfloat16")
     if X.dim() != 2 or X.shape[1] != width:
         raise ValueError(f"{what} must have {width} columns")
-    return X
+    return dev
 
 
 def loftq_dropout(X: torch.Tensor, p: float, seed: int, offset: int = 0, step: Optional[torch.Tensor] = None,
                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """X / (1 - p) where the mask of (p, seed, offset + step) keeps, else 0; the gradient is the same call
     on dY.  `step` is a one-element int64 device tensor that is read when the kernel runs.  `out` may be X."""
-    _contig(X, "X")
+    dev, dtype = _first(X, "X"), _wdtype(X)
     if out is None:
         out = torch.empty_like(X)
-    _expect(out, "out", X, X.dtype, X.shape)
-    drop = _dropout(p, seed, offset, step, X)
-    device, st = _on(X, stream)
-    with device:
-        _check("loftq_dropout", _c_dropout(_ptr(X), _wdtype(X), X.numel(), ctypes.byref(drop), _ptr(out), st))
+    y = _expect(out, "out", dev, X.dtype, X.shape)
+    at = None if step is None else _expect(step, "step", dev, torch.int64, (1,))
+    drop = LoftqDropout(p, seed & _M64, offset & _M64, at)
+    _call("loftq_dropout", _c_dropout, dev, stream, X.data_ptr(), dtype, X.numel(), ctypes.byref(drop), y)
     return out
 
 
@@ -500,10 +512,10 @@ def loftq_qlora_forward_dropout(X: torch.Tensor, packed: torch.Tensor, shape, ab
                                 ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Y = X bf16(deq(Q))^T + alpha / (1 - p) (keep(X) bf16(A)^T) bf16(B)^T for bf16 X (n_tok x cols)."""
     rows, cols = shape
-    _tokens(X, "X", cols)
-    return _layer_forward("loftq_qlora_forward_dropout", _c_fwd_drop, _c_fwd_drop_ws, X,
-                          _nf_args(X, packed, rows, cols, absmax, qabsmax, dq_scale, bits), rows, cols, B, A, alpha,
-                          _dropout(p, seed, offset, step, X), out, out_dtype, ws, stream)
+    dev = _tokens(X, "X", cols)
+    return _layer_forward("loftq_qlora_forward_dropout", _c_fwd_drop, _c_fwd_drop_ws, X, dev,
+                          _nf_args(dev, packed, rows, cols, absmax, qabsmax, dq_scale, bits), rows, cols, B, A, alpha,
+                          _dropout(p, seed, offset, step, dev), out, out_dtype, ws, stream)
 
 
 def loftq_qlora_backward(dY: torch.Tensor, X: Optional[torch.Tensor], packed: torch.Tensor, shape,
@@ -515,29 +527,27 @@ def loftq_qlora_backward(dY: torch.Tensor, X: Optional[torch.Tensor], packed: to
     """(dX, dB, dA) of loftq_qlora_forward_dropout for bf16 dY (n_tok x rows) and the forward's X and mask.
     `out`: the three tensors to fill, None for one that is not wanted (dB and dA both or neither)."""
     rows, cols = shape
-    _tokens(dY, "dY", rows)
-    return _layer_backward("loftq_qlora_backward", _c_bwd, _c_bwd_ws, dY, X,
-                           _nf_args(dY, packed, rows, cols, absmax, qabsmax, dq_scale, bits), rows, cols, B, A, alpha,
-                           _dropout(p, seed, offset, step, dY), need_dx, out, dx_dtype, ws, stream)
+    dev = _tokens(dY, "dY", rows)
+    return _layer_backward("loftq_qlora_backward", _c_bwd, _c_bwd_ws, dY, X, dev,
+                           _nf_args(dev, packed, rows, cols, absmax, qabsmax, dq_scale, bits), rows, cols, B, A, alpha,
+                           _dropout(p, seed, offset, step, dev), need_dx, out, dx_dtype, ws, stream)
 
 
 def loftq_mxfp4_quantize(W: torch.Tensor, B: Optional[torch.Tensor] = None, A: Optional[torch.Tensor] = None,
                          packed: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None):
     """W - B A (or W) in MXFP4: codes (rows x 128-byte steps of 256 columns) and scales (steps x rows x 8)."""
-    _contig(W, "W")
+    dev, dtype = _first(W, "W"), _wdtype(W)
     if W.dim() != 2:
         raise ValueError("W must be a matrix")
     rows, cols = W.shape
     steps = (cols + 255) // 256
-    r, adapter = _adapter_args(W, B, A, rows, cols, 1.0, LoftqDropout())
+    b, a, r = _adapter_args(dev, B, A, rows, cols)
     if packed is None:
         packed = torch.empty((rows, steps * 128), dtype=torch.uint8, device=W.device)
     if scales is None:
         scales = torch.empty((steps, rows, 8), dtype=torch.uint8, device=W.device)
-    base = _mx_args(W, packed, scales, rows, cols)
-    device, st = _on(W, stream)
-    with device:
-        _check("loftq_mxfp4_quantize", _c_mx_quant(_ptr(W), _wdtype(W), rows, cols, *adapter[:3], *base, st))
+    _call("loftq_mxfp4_quantize", _c_mx_quant, dev, stream, W.data_ptr(), dtype, rows, cols, b, a, r,
+          *_mx_args(dev, packed, scales, rows, cols))
     return packed, scales
 
 
@@ -545,17 +555,16 @@ def loftq_mxfp4_dequantize(packed: torch.Tensor, scales: torch.Tensor, shape, W:
                            out: Optional[torch.Tensor] = None, out_dtype=torch.float32, stream=None) -> torch.Tensor:
     """deq(Q), or W - deq(Q) when W is given; formed in fp32 and rounded to out_dtype."""
     rows, cols = shape
-    base = _mx_args(packed, packed, scales, rows, cols)
-    if W is not None:
-        _expect(W, "W", packed, (torch.float32, torch.bfloat16), (rows, cols))
+    dev = _first(packed, "packed")
+    base = _mx_args(dev, packed, scales, rows, cols)
+    w = None if W is None else _expect(W, "W", dev, None, (rows, cols))
     out_dtype = _out_dtype(out, out_dtype)
     if out is None:
         out = torch.empty((rows, cols), dtype=out_dtype, device=packed.device)
-    _expect(out, "out", packed, out_dtype, (rows, cols))
-    device, st = _on(packed, stream)
-    with device:
-        _check("loftq_mxfp4_dequantize", _c_mx_deq(*base, rows, cols, _ptr(W), _wdtype(W) if W is not None else
-                                                   LOFTQ_F32, _ptr(out), _wdtype(out), st))
+    _call("loftq_mxfp4_dequantize", _c_mx_deq, dev, stream, *base, rows, cols, w,
+          LOFTQ_BF16 if W is not None and W.dtype is torch.bfloat16 else LOFTQ_F32,
+          _expect(out, "out", dev, out_dtype, (rows, cols)),
+          LOFTQ_BF16 if out_dtype is torch.bfloat16 else LOFTQ_F32)
     return out
 
 
@@ -566,9 +575,10 @@ def loftq_mxfp4_forward(X: torch.Tensor, packed: torch.Tensor, scales: torch.Ten
                         ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Y = MX(X) deq(Q)^T + alpha / (1 - p) (keep(X) bf16(A)^T) bf16(B)^T for bf16 X (n_tok x cols)."""
     rows, cols = shape
-    _tokens(X, "X", cols)
-    return _layer_forward("loftq_mxfp4_forward", _c_mx_fwd, _c_mx_fwd_ws, X, _mx_args(X, packed, scales, rows, cols),
-                          rows, cols, B, A, alpha, _dropout(p, seed, offset, step, X), out, out_dtype, ws, stream)
+    dev = _tokens(X, "X", cols)
+    return _layer_forward("loftq_mxfp4_forward", _c_mx_fwd, _c_mx_fwd_ws, X, dev,
+                          _mx_args(dev, packed, scales, rows, cols), rows, cols, B, A, alpha,
+                          _dropout(p, seed, offset, step, dev), out, out_dtype, ws, stream)
 
 
 def loftq_mxfp4_backward(dY: torch.Tensor, X: Optional[torch.Tensor], packed: torch.Tensor, scales: torch.Tensor,
@@ -579,10 +589,10 @@ def loftq_mxfp4_backward(dY: torch.Tensor, X: Optional[torch.Tensor], packed: to
     """(dX, dB, dA) of loftq_mxfp4_forward, the rounding of X passing the gradient as it is; `out` as in
     loftq_qlora_backward."""
     rows, cols = shape
-    _tokens(dY, "dY", rows)
-    return _layer_backward("loftq_mxfp4_backward", _c_mx_bwd, _c_mx_bwd_ws, dY, X,
-                           _mx_args(dY, packed, scales, rows, cols), rows, cols, B, A, alpha,
-                           _dropout(p, seed, offset, step, dY), need_dx, out, dx_dtype, ws, stream)
+    dev = _tokens(dY, "dY", rows)
+    return _layer_backward("loftq_mxfp4_backward", _c_mx_bwd, _c_mx_bwd_ws, dY, X, dev,
+                           _mx_args(dev, packed, scales, rows, cols), rows, cols, B, A, alpha,
+                           _dropout(p, seed, offset, step, dev), need_dx, out, dx_dtype, ws, stream)
 
 
 def lowrank_workspace_bytes(rows: int, cols: int, r: int, oversample: int, exact: bool) -> int:

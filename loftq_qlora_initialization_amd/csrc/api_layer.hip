@@ -31,6 +31,7 @@ struct ForwardSpace {
   uint8_t* xs;
   __bf16 *Ab, *Bb, *S;
   float* partials;   // of X A^T
+  float* T;          // of X A^T for the few-token product
   float* joins;      // of the product's K ranges
   int ks;
   size_t bytes;
@@ -39,6 +40,7 @@ struct ForwardSpace {
 ForwardSpace forward_space(void* ws, i64 n, i64 rows, i64 cols, int r, bool mx) {
   Arena a{static_cast<char*>(ws)};
   ForwardSpace f{};
+  if (mx && r > 0 && token_product_pays(n, rows, cols)) f.T = a.take<float>(lora_down_splits(n, cols, r) * n * r);
   if (mx) {
     f.xq = a.take<uint8_t>(n * mx_steps(cols) * (kMxStep / 2));
     f.xs = a.take<uint8_t>(n * mx_steps(cols) * 8);
@@ -102,7 +104,7 @@ bool layer_shape_ok(i64 n, i64 rows, i64 cols, int r) {
   if (!tile_product_shape_ok(n, rows, cols) || !tile_product_shape_ok(n, cols, rows_pad)) return false;
   const i64 base = rows_pad * (cols / 8 + 16), codes = n * mx_steps(cols) * 32, pad = n * (rows_pad / 8);
   const i64 operands = (rp + adapter_ld(static_cast<int>(rp))) * (cols + rows_pad);
-  return (base > codes ? base : codes) + pad + operands < limit && pad_to(n, 64) * 64 < limit;
+  return (base > codes ? base : codes) + pad + operands < limit && pad_to(n, 64) * 64 < limit && rows < limit / 64;
 }
 
 bool drop_ok(const loftq_dropout_t* d) {
@@ -171,6 +173,11 @@ loftq_status_t layer_forward(const void* X, i64 n, i64 rows, i64 cols, const Bas
   if (ws_bytes < f.bytes) return LOFTQ_ERR_WORKSPACE;
   const __bf16* Xb = static_cast<const __bf16*>(X);
   const DropArg d = drop_arg(drop);
+  if (mx && (r == 0 || d.thr == 0) && token_product_pays(n, rows, cols)) {   // dropout is the tiled path's
+    if (r > 0) LQ_TRY(launch_lora_down(Xb, n, cols, A, r, f.T, s));
+    return from_hip(launch_token_product(TokenProduct{Xb, base.packed, base.mx, f.T, B, n, rows, cols,
+                                                      r > 0 ? lora_down_splits(n, cols, r) : 0, r, alpha, Y, ydt}, s));
+  }
   const int rp = rank_pad(r);
   PrepareArgs p{};
   p.a = AdapterOperands{A, B, r, rp, rows, cols, rows, f.Ab, nullptr, f.Bb, nullptr, adapter_ld(rp)};

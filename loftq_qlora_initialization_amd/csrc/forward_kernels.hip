@@ -541,6 +541,47 @@ bool qlora_forward_shape_ok(int64_t n_tok, int64_t rows, int64_t cols, int r) {
   return p.grid_down * 1024 < limit && p.grid_gemm * p.block_gemm < limit;
 }
 
+int lora_down_splits(int64_t n_tok, int64_t cols, int r) { return plan_forward(n_tok, 16, cols, r).ks; }
+
+hipError_t launch_lora_down(const void* X, int64_t n_tok, int64_t cols, const float* A, int r, float* Tws,
+                            hipStream_t s) {
+  const __bf16* Xb = static_cast<const __bf16*>(X);
+  const ForwardPlan pl = plan_forward(n_tok, 16, cols, r);
+  const int ks = pl.ks;
+  const dim3 grid(static_cast<unsigned>(pl.grid_down));
+  // steps per wave in one K range, rounded up to a power of two, capped by registers
+  // (1024-thread workgroups: at most 128 VGPRs)
+  const int64_t per = ((cols / 32) + ks - 1) / ks;
+  const int64_t spw = (per + 15) / 16;
+  const int nt = (r + 15) / 16;
+  const int umax = pl.tt == 4 ? 2 : (nt == 1 ? 8 : (nt == 2 ? 4 : 2));
+  int u = spw <= 1 ? 1 : spw <= 2 ? 2 : spw <= 4 ? 4 : 8;
+  if (u > umax) u = umax;
+#define LQ_DOWN(NT, U, TT)                                                                                 \
+LQ_LAUNCH("lora_down", (lora_down_kernel<NT, U, TT>), grid, dim3(1024), 0, s, Xb, n_tok, cols, A, r, ks, \
+          Tws)
+  if (pl.tt == 4) {
+    if (u == 1) LQ_DOWN(1, 1, 4);
+    else LQ_DOWN(1, 2, 4);
+  } else {
+    switch (nt * 16 + u) {
+      case 16 + 1: LQ_DOWN(1, 1, 1); break;
+      case 16 + 2: LQ_DOWN(1, 2, 1); break;
+      case 16 + 4: LQ_DOWN(1, 4, 1); break;
+      case 16 + 8: LQ_DOWN(1, 8, 1); break;
+      case 32 + 1: LQ_DOWN(2, 1, 1); break;
+      case 32 + 2: LQ_DOWN(2, 2, 1); break;
+      case 32 + 4: LQ_DOWN(2, 4, 1); break;
+      case 48 + 1: LQ_DOWN(3, 1, 1); break;
+      case 48 + 2: LQ_DOWN(3, 2, 1); break;
+      case 64 + 1: LQ_DOWN(4, 1, 1); break;
+      default: LQ_DOWN(4, 2, 1); break;
+    }
+  }
+#undef LQ_DOWN
+  return hipGetLastError();
+}
+
 hipError_t launch_qlora_forward(const void* X, int64_t n_tok, int64_t rows, int64_t cols, const uint8_t* packed,
                                 const float* absmax, const int8_t* qa, const float* dqs, int bits, const float* B,
                                 const float* A, int r, float alpha, float* Y, float* Tws, hipStream_t s) {
@@ -550,37 +591,8 @@ hipError_t launch_qlora_forward(const void* X, int64_t n_tok, int64_t rows, int6
   const ForwardPlan pl = plan_forward(n_tok, rows, cols, r);
   const int ks = pl.ks;
   if (B != nullptr) {
-    const dim3 grid(static_cast<unsigned>(pl.grid_down));
-    // steps per wave in one K range, rounded up to a power of two, capped by registers
-    // (1024-thread workgroups: at most 128 VGPRs)
-    const int64_t per = ((cols / 32) + ks - 1) / ks;
-    const int64_t spw = (per + 15) / 16;
-    const int nt = (r + 15) / 16;
-    const int umax = pl.tt == 4 ? 2 : (nt == 1 ? 8 : (nt == 2 ? 4 : 2));
-    int u = spw <= 1 ? 1 : spw <= 2 ? 2 : spw <= 4 ? 4 : 8;
-    if (u > umax) u = umax;
-#define LQ_DOWN(NT, U, TT)                                                                                 \
-  LQ_LAUNCH("lora_down", (lora_down_kernel<NT, U, TT>), grid, dim3(1024), 0, s, Xb, n_tok, cols, A, r, ks, \
-            Tws)
-    if (pl.tt == 4) {
-      if (u == 1) LQ_DOWN(1, 1, 4);
-      else LQ_DOWN(1, 2, 4);
-    } else {
-      switch (nt * 16 + u) {
-        case 16 + 1: LQ_DOWN(1, 1, 1); break;
-        case 16 + 2: LQ_DOWN(1, 2, 1); break;
-        case 16 + 4: LQ_DOWN(1, 4, 1); break;
-        case 16 + 8: LQ_DOWN(1, 8, 1); break;
-        case 32 + 1: LQ_DOWN(2, 1, 1); break;
-        case 32 + 2: LQ_DOWN(2, 2, 1); break;
-        case 32 + 4: LQ_DOWN(2, 4, 1); break;
-        case 48 + 1: LQ_DOWN(3, 1, 1); break;
-        case 48 + 2: LQ_DOWN(3, 2, 1); break;
-        case 64 + 1: LQ_DOWN(4, 1, 1); break;
-        default: LQ_DOWN(4, 2, 1); break;
-      }
-    }
-#undef LQ_DOWN
+    const hipError_t e = launch_lora_down(X, n_tok, cols, A, r, Tws, s);
+    if (e != hipSuccess) return e;
   }
   const Nf4Tables& tab = nf_tables(bits);
   const float* T = B != nullptr ? Tws : nullptr;

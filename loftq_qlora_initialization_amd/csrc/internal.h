@@ -83,6 +83,10 @@ bool qlora_forward_shape_ok(int64_t n_tok, int64_t rows, int64_t cols, int r);
 hipError_t launch_qlora_forward(const void* X, int64_t n_tok, int64_t rows, int64_t cols, const uint8_t* packed,
                                 const float* absmax, const int8_t* qa, const float* dqs, int bits, const float* B,
                                 const float* A, int r, float alpha, float* Y, float* Tws, hipStream_t s);
+// Its first half: the partials of X bf16(A)^T over lora_down_splits(...) K ranges (cols % 32 == 0).
+int lora_down_splits(int64_t n_tok, int64_t cols, int r);
+hipError_t launch_lora_down(const void* X, int64_t n_tok, int64_t cols, const float* A, int r, float* Tws,
+                            hipStream_t s);
 // Q' = NF4(deq(Q) + alpha B A); input scales absmax or (q, dqscale); output
 // absmax_out and, with q_out / dqs_out, its double quant (dq_blocksize 256).
 hipError_t launch_nf4_merge(const uint8_t* packed, const float* absmax, const int8_t* q, const float* dqscale,

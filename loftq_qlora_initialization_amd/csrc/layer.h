@@ -46,6 +46,23 @@ TilePlan plan_tile_product(int64_t M, int64_t N, int steps, int adapter_steps, b
 hipError_t launch_tile_product(TileProduct t, bool mx, float* partials, hipStream_t s);
 bool tile_product_shape_ok(int64_t M, int64_t N, int64_t K);
 
+// The MXFP4 product for M <= 16 tokens, from X itself (token_product.hip), and whether it is
+// faster than the tiled one.
+bool token_product_pays(int64_t M, int64_t N, int64_t K);
+struct TokenProduct {
+  const __bf16* X;            // M x K, K % 32 == 0
+  const uint8_t* W;
+  const uint8_t* wscale;
+  const float* T;             // [ks][M][r] partials of X A^T
+  const float* B;             // N x r
+  int64_t M, N, K;
+  int ks, r;                  // r = 0: no adapter
+  float alpha;
+  void* out;
+  loftq_dtype_t odt;
+};
+hipError_t launch_token_product(const TokenProduct& t, hipStream_t s);
+
 // ---- adapter and base operands (adapter_kernels.hip) ----
 struct AdapterOperands {
   const float* A;   // r x cols

@@ -38,11 +38,21 @@ __device__ __forceinline__ float mx_scale(uint32_t byte) {
                                                                    : __uint_as_float(byte << 23));
 }
 
+// Eight scaled values into a word of codes.  The conversion instruction rounds to the nearest
+// e2m1 value, ties to the even code, and takes larger magnitudes to 6; the scale is applied
+// before it, exactly, since the instruction's own scale does not reach 2^-127.
+__device__ __forceinline__ uint32_t mx_codes8(const float (&v)[8]) {
+  uint32_t word = 0;   // the instruction puts its first value into the low nibble
+  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, v[1], v[0], 1.f, 0);
+  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, v[3], v[2], 1.f, 1);
+  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, v[5], v[4], 1.f, 2);
+  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, v[7], v[6], 1.f, 3);
+  return word;
+}
+
 // Eight consecutive values of a row (columns c0 .. c0 + 7 of the padded matrix) into a word of
 // codes; the four lanes of a quad hold one block and exchange its largest magnitude by two quad
-// permutes.  The conversion instruction rounds to the nearest e2m1 value, ties to the even code,
-// and takes larger magnitudes to 6; the scale is applied before it, exactly, since the
-// instruction's own scale does not reach 2^-127.
+// permutes.
 __device__ __forceinline__ uint32_t mx_encode8(const float (&x)[8], uint32_t& byte) {
   uint32_t amax = 0;
 #pragma unroll
@@ -56,12 +66,10 @@ __device__ __forceinline__ uint32_t mx_encode8(const float (&x)[8], uint32_t& by
   amax = o2 > amax ? o2 : amax;
   byte = mx_scale_byte(amax);
   const float inv = mx_inverse_scale(byte);
-  uint32_t word = 0;   // the instruction puts its first value into the low nibble
-  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, x[1] * inv, x[0] * inv, 1.f, 0);
-  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, x[3] * inv, x[2] * inv, 1.f, 1);
-  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, x[5] * inv, x[4] * inv, 1.f, 2);
-  word = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(word, x[7] * inv, x[6] * inv, 1.f, 3);
-  return word;
+  float v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = x[j] * inv;
+  return mx_codes8(v);
 }
 __device__ __forceinline__ float fp4_value(uint32_t code) {
   // magnitude code 0: 0, 1: 0.5, else (1 + m / 2) 2^(e - 1) with e = code >> 1 & 3, m = code & 1

@@ -1,0 +1,170 @@
+// The adapted layer over an MXFP4 base for a few tokens (serving): bound by reading the weight,
+// and by the launches before it, so the tokens' codes are formed where they are multiplied.
+//
+// v_mfma_scale_f32_16x16x128_f8f6f4 on FP4: lane L supplies row L%16, k = 32 (L/16) .. + 31,
+// one MXFP4 block with its scale byte, for either operand; tokens are the first, so lane L
+// receives token 4 (L/16) + v, feature L%16 in element v.
+//
+// A workgroup owns 16 NF features and up to 16 tokens; its waves take steps of 256 columns in
+// turn (whole lines of the weight's codes).  A lane holds a whole block of a token: it finds
+// the scale and the codes by itself, as mx_quantize_kernel does, so a token's result is that of
+// the tiled product up to the order of its sums.  That repeats the tokens' rounding in every
+// workgroup, and reads four times a feature tile's bytes for it: NF tiles share it where the
+// features suffice.  The partial sums meet in LDS in wave order, then the adapter's term is
+// added in fp32.
+//
+// Measured with its adapter's launch, in a graph, one token: 4096 x 4096 9.2 us (the tiled
+// product and its launches 21.3), 11008 x 4096 16.4 us (20.2), 28672 x 8192 34.7 us (34.8);
+// 16 tokens 12.5 us (22.4), 23.1 us (21.6), 50 us (36).
+#include "layer.h"
+
+namespace loftq {
+namespace {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kWaves = 16, kChunk = 128;
+
+__device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+// A block of 32 values into its codes and scale byte.
+__device__ __forceinline__ i32x4 encode_block(const bf16x8 (&x)[4], uint32_t& byte) {
+  uint32_t amax = 0;
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const uint32_t b = __float_as_uint(static_cast<float>(x[q][j])) & 0x7FFFFFFFu;
+      amax = b > amax ? b : amax;
+    }
+  byte = mx_scale_byte(amax);
+  const float inv = mx_inverse_scale(byte);
+  i32x4 out;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = static_cast<float>(x[q][j]) * inv;
+    out[q] = static_cast<int>(mx_codes8(v));
+  }
+  return out;
+}
+
+template <int NF, typename O>
+__global__ __launch_bounds__(kWaves * 64) void token_product_kernel(TokenProduct t) {
+  __shared__ float part[kWaves / 2][NF * 256];
+  __shared__ float Ts[16 * 64];         // the tokens' rows of X A^T, r <= 64
+  __shared__ float Bs[NF * 16 * 64];    // bf16(B) of the workgroup's features
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, li = lane & 15, lg = lane >> 4;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * (16 * NF), M = t.M, N = t.N, K = t.K;
+  const int r = t.r;
+  // the epilogue's operands first, their loads beside the main loop's
+  if (r > 0) {
+    for (int i = tid; i < M * r; i += kWaves * 64) {
+      float x = 0.f;
+      for (int q = 0; q < t.ks; ++q) x += t.T[q * M * r + i];
+      Ts[i] = x;
+    }
+    for (int i = tid; i < NF * 16 * r; i += kWaves * 64) {
+      const int64_t n = n0 + i / r < N ? n0 + i / r : N - 1;
+      Bs[i] = static_cast<float>(static_cast<__bf16>(t.B[n * r + i % r]));
+    }
+  }
+  const int64_t steps = (K + kMxStep - 1) / kMxStep;
+  int64_t n[NF];   // rows past the last repeat it (never stored)
+#pragma unroll
+  for (int f = 0; f < NF; ++f) n[f] = n0 + f * 16 + li < N ? n0 + f * 16 + li : N - 1;
+  const int64_t m = li < M ? li : M - 1;
+  f32x4 acc[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f) acc[f] = f32x4{0.f, 0.f, 0.f, 0.f};
+  // the two chunks of a step at a time: whole lines of the codes; blocks past K (K % 32 == 0)
+  // load a valid address and count as zeros
+  for (int64_t k0 = static_cast<int64_t>(w) * kMxStep; k0 < K; k0 += kWaves * kMxStep) {
+    i32x4 wc[2][NF];
+    uint32_t ws[2][NF];
+    bf16x8 x[2][4];
+    bool live[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const int64_t k = k0 + u * kChunk + 32 * lg;
+      live[u] = k < K;
+      const int64_t kk = live[u] ? k : 0;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        wc[u][f] = *reinterpret_cast<const i32x4*>(t.W + n[f] * steps * (kMxStep / 2) + kk / 2);
+        ws[u][f] = t.wscale[(kk / kMxStep * N + n[f]) * 8 + kk % kMxStep / kMxBlock];
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) x[u][q] = *reinterpret_cast<const bf16x8*>(t.X + m * K + kk + 8 * q);
+    }
+    __builtin_amdgcn_sched_barrier(0);   // every load of the step is in flight before the first wait
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+      const i32x4 zero = {0, 0, 0, 0};
+      uint32_t byte;
+      i32x4 xv = encode_block(x[u], byte);
+      xv = live[u] ? xv : zero;
+      byte = live[u] ? byte : 0u;
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+        acc[f] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(xv), widen(live[u] ? wc[u][f] : zero), acc[f], 4, 4,
+                                                                  0, static_cast<int>(byte), 0,
+                                                                  static_cast<int>(live[u] ? ws[u][f] : 0u));
+    }
+  }
+  auto at = [&](int f, int v) { return (f * 4 + v) * 64 + lane; };
+  if (w >= kWaves / 2)
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) part[w - kWaves / 2][at(f, v)] = acc[f][v];
+  __syncthreads();
+  if (w < kWaves / 2)
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int v = 0; v < 4; ++v) part[w][at(f, v)] += acc[f][v];
+  __syncthreads();
+  for (int e = tid; e < NF * 256; e += kWaves * 64) {
+    const int ln = e & 63, v = (e >> 6) & 3, f = e >> 8;
+    const int64_t mm = 4 * (ln >> 4) + v, nn = n0 + f * 16 + (ln & 15);
+    if (mm >= M || nn >= N) continue;
+    float y = 0.f;
+#pragma unroll
+    for (int q = 0; q < kWaves / 2; ++q) y += part[q][e];
+    float lora = 0.f;
+    for (int p = 0; p < r; ++p) lora = fmaf(Ts[mm * r + p], Bs[(f * 16 + (ln & 15)) * r + p], lora);
+    if (r > 0) y = fmaf(t.alpha, lora, y);
+    static_cast<O*>(t.out)[mm * N + nn] = static_cast<O>(y);
+  }
+}
+
+}  // namespace
+
+bool token_product_pays(int64_t M, int64_t N, int64_t K) {
+  return M <= 8 || (M <= 16 && N * K <= (int64_t(1) << 25));
+}
+
+hipError_t launch_token_product(const TokenProduct& t, hipStream_t s) {
+  // as many features a workgroup as leave each CU one
+  const int nf = t.N >= 16384 ? 4 : (t.N >= 8192 ? 2 : 1);
+  const dim3 grid(static_cast<unsigned>((t.N + 16 * nf - 1) / (16 * nf))), block(kWaves * 64);
+#define LQ_TOKEN(NF, O) LQ_LAUNCH("mx_token_product", (token_product_kernel<NF, O>), grid, block, 0, s, t)
+#define LQ_TOKEN_O(O)                \
+  do {                               \
+    if (nf == 4) LQ_TOKEN(4, O);     \
+    else if (nf == 2) LQ_TOKEN(2, O); \
+    else LQ_TOKEN(1, O);             \
+  } while (0)
+  if (t.odt == LOFTQ_BF16) LQ_TOKEN_O(__bf16);
+  else LQ_TOKEN_O(float);
+#undef LQ_TOKEN_O
+#undef LQ_TOKEN
+  return hipGetLastError();
+}
+
+}  // namespace loftq

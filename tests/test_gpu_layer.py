@@ -259,7 +259,8 @@ SHAPES = [  # n, rows, cols, r, base, dq, bits
     (130, 384, 1024, 33, "nf", False, 4), (257, 260, 128, 48, "nf", True, 4),
     (1, 1, 32, 1, "mx", False, 4), (1, 48, 256, 16, "mx", False, 4), (3, 33, 96, 9, "mx", False, 4),
     (64, 130, 288, 64, "mx", False, 4), (70, 255, 544, 0, "mx", False, 4), (129, 512, 1056, 20, "mx", False, 4),
-    (300, 333, 512, 64, "mx", False, 4),
+    (300, 333, 512, 64, "mx", False, 4), (16, 70, 416, 3, "mx", False, 4), (17, 129, 2080, 64, "mx", False, 4),
+    (32, 48, 4128, 16, "mx", False, 4), (33, 48, 4128, 16, "mx", False, 4),
 ]
 
 
@@ -358,6 +359,26 @@ def test_outputs_are_overwritten_and_nothing_else(lib):
         for o, b, t in zip(out, bufs, want):
             assert torch.equal(o, t) and torch.isnan(b[t.numel():]).all()
         assert (ws[need:] == fill).all()
+
+
+@pytest.mark.parametrize("n", [7, 300])
+def test_mx_forward_of_what_is_not_finite(lib, n):
+    """A NaN or an infinity makes its block of 32 columns NaN, and with it its token's results, and no other's."""
+    layer = Layer(n, 96, 288, 8, "mx", seed=15)
+    clean = layer.forward(lib)
+    for bad in (float("nan"), float("inf")):
+        X = layer.Xd
+        layer.Xd = X.clone()
+        layer.Xd[2, 287] = bad
+        Y = layer.forward(lib)
+        layer.Xd = X
+        others = torch.arange(n, device="cuda") != 2
+        assert torch.isnan(Y[2]).all() and torch.equal(Y[others], clean[others])
+    layer.kw["scales"] = layer.kw["scales"].clone()
+    layer.kw["scales"][1, 5, 0] = 255   # a NaN block of the weight's row 5
+    Y = layer.forward(lib)
+    rows = torch.arange(96, device="cuda") != 5
+    assert torch.isnan(Y[:, 5]).all() and torch.equal(Y[:, rows], clean[:, rows])
 
 
 @pytest.mark.parametrize("base", ["nf", "mx"])
