@@ -80,36 +80,36 @@ __device__ __forceinline__ void adapter_operand(const AdapterOperands& a, uint32
   }
 }
 
-// Eight elements of the base from e8 on (row-major, 8 | e8) as bf16(fp32 value).
+// A word of eight codes (the first in the high nibble of the low byte) and its scale as
+// bf16(fp32 value).
+__device__ __forceinline__ u32x4 decode8(const float* lvl, uint32_t word, float sc) {
+  bf16x8 o;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = static_cast<__bf16>(lvl[word >> (8 * (j >> 1) + (j & 1 ? 0 : 4)) & 15u] * sc);
+  return __builtin_bit_cast(u32x4, o);
+}
+// The codes and the scale of eight elements of a row from column c on (8 | c).
 struct NfSource {
   const uint8_t* packed;
   const float* absmax;
   const int8_t* qabsmax;
   const float* dq_scale;
-  __device__ __forceinline__ u32x4 load8(const float* lvl, int64_t row, int64_t c, int64_t rows, int64_t cols) const {
-    return at(lvl, row * cols + c);
-  }
-  __device__ __forceinline__ u32x4 at(const float* lvl, int64_t e) const {
+  __device__ __forceinline__ void fetch(int64_t e, uint32_t& word, float& sc) const {
     const int64_t b = e >> 6;
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(packed + (e >> 1));
-    const float sc = qabsmax != nullptr ? static_cast<float>(qabsmax[b]) * dq_scale[b >> 8] : absmax[b];
-    bf16x8 o;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = static_cast<__bf16>(lvl[word >> (8 * (j >> 1) + (j & 1 ? 0 : 4)) & 15u] * sc);
-    return __builtin_bit_cast(u32x4, o);
+    word = *reinterpret_cast<const uint32_t*>(packed + (e >> 1));
+    sc = qabsmax != nullptr ? static_cast<float>(qabsmax[b]) * dq_scale[b >> 8] : absmax[b];
+  }
+  __device__ __forceinline__ void fetch(int64_t row, int64_t c, int64_t rows, int64_t cols, uint32_t& word, float& sc) const {
+    fetch(row * cols + c, word, sc);
   }
 };
 struct MxSource {
   const uint8_t* packed;
   const uint8_t* scales;
-  __device__ __forceinline__ u32x4 load8(const float* lvl, int64_t row, int64_t c, int64_t rows, int64_t cols) const {
+  __device__ __forceinline__ void fetch(int64_t row, int64_t c, int64_t rows, int64_t cols, uint32_t& word, float& sc) const {
     const int64_t steps = (cols + kMxStep - 1) / kMxStep;
-    const uint32_t word = *reinterpret_cast<const uint32_t*>(packed + row * steps * (kMxStep / 2) + c / 2);
-    const float sc = mx_scale(scales[(c / kMxStep * rows + row) * 8 + (c % kMxStep) / kMxBlock]);
-    bf16x8 o;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = static_cast<__bf16>(lvl[word >> (8 * (j >> 1) + (j & 1 ? 0 : 4)) & 15u] * sc);
-    return __builtin_bit_cast(u32x4, o);
+    word = *reinterpret_cast<const uint32_t*>(packed + row * steps * (kMxStep / 2) + c / 2);
+    sc = mx_scale(scales[(c / kMxStep * rows + row) * 8 + (c % kMxStep) / kMxBlock]);
   }
 };
 struct Levels {
@@ -127,11 +127,21 @@ __device__ __forceinline__ void turn_base(const Src& src, const float* lvl, uint
   const int tid = threadIdx.x, pair = tid / 8, c16 = (tid % 8) * 16;
   const int64_t row = tr * kTurnRows + 2 * pair;
   const u32x4 zero = {0u, 0u, 0u, 0u};
+  uint32_t word[2][2];
+  float sc[2][2];
+  bool live[2][2];
+#pragma unroll
+  for (int q = 0; q < 2; ++q)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {   // every load in flight before the first is decoded
+      const int64_t c = tc * kTurnCols + c16 + q * 8;
+      live[q][h] = row + h < rows && c < cols;
+      src.fetch(live[q][h] ? row + h : 0, live[q][h] ? c : 0, rows, cols, word[q][h], sc[q][h]);
+    }
 #pragma unroll
   for (int q = 0; q < 2; ++q) {
-    const int64_t c = tc * kTurnCols + c16 + q * 8;
-    const u32x4 lo = row < rows && c < cols ? src.load8(lvl, row, c, rows, cols) : zero;
-    const u32x4 hi = row + 1 < rows && c < cols ? src.load8(lvl, row + 1, c, rows, cols) : zero;
+    const u32x4 lo = live[q][0] ? decode8(lvl, word[q][0], sc[q][0]) : zero;
+    const u32x4 hi = live[q][1] ? decode8(lvl, word[q][1], sc[q][1]) : zero;
 #pragma unroll
     for (int j = 0; j < 8; ++j)
       tile[c16 + q * 8 + j][pair] = __builtin_amdgcn_perm(hi[j >> 1], lo[j >> 1], j & 1 ? 0x07060302u : 0x05040100u);
@@ -175,8 +185,20 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Src src, Levels lv, P
         const uint32_t ntr = static_cast<uint32_t>(p.a.rows_pad / kTurnRows);
         turn_base(src, lvl, tile, wg % ntr, wg / ntr, p.a.rows, p.a.cols, p.a.rows_pad, p.base);
       } else {
-        const int64_t e = (static_cast<int64_t>(wg) * kThreads + tid) * 8;
-        if (e < p.a.rows * p.a.cols) *reinterpret_cast<u32x4*>(p.base + e) = src.at(lvl, e);
+        // four groups of eight a thread, every load in flight before the first is decoded
+        const int64_t n = p.a.rows * p.a.cols, e0 = (static_cast<int64_t>(wg) * (4 * kThreads) + tid) * 8;
+        uint32_t word[4];
+        float sc[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t e = e0 + q * (kThreads * 8);
+          src.fetch(e < n ? e : 0, word[q], sc[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int64_t e = e0 + q * (kThreads * 8);
+          if (e < n) *reinterpret_cast<u32x4*>(p.base + e) = decode8(lvl, word[q], sc[q]);
+        }
       }
     }
     return;
@@ -213,31 +235,31 @@ __device__ __forceinline__ u32x4 drop8(u32x4 v, uint64_t key, uint64_t e, uint32
 // tokens zeroed.  The waves' sums meet in LDS.
 template <int NT>
 __global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n) {
-  constexpr int U = NT <= 2 ? 4 : 2;
-  __shared__ float part[3][2 * NT * 4 * 64];
+  constexpr int TT = 2, U = NT <= 2 ? 4 : 2;
+  __shared__ float part[3][TT * NT * 4 * 64];
   const DownJob& jb = jobs.job[blockIdx.x < jobs.job[0].wgs ? 0 : 1];
   const uint32_t wg = blockIdx.x < jobs.job[0].wgs ? blockIdx.x : blockIdx.x - jobs.job[0].wgs;
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
-  const int64_t K = jb.K, m0 = static_cast<int64_t>(wg / jb.ks) * 32;
+  const int64_t K = jb.K, m0 = static_cast<int64_t>(wg / jb.ks) * (16 * TT);
   const int q = wg % jb.ks, steps = static_cast<int>(K / 32), per = (steps + jb.ks - 1) / jb.ks;
   const int begin = q * per, end = begin + per < steps ? begin + per : steps;
   const uint32_t thr = jb.drop.thr;
   const uint64_t key = thr != 0 ? drop_key(jb.drop) : 0;
-  int64_t m[2];
+  int64_t m[TT];
 #pragma unroll
-  for (int t = 0; t < 2; ++t) m[t] = m0 + 16 * t + li < n ? m0 + 16 * t + li : n - 1;
-  f32x4 acc[2][NT];
+  for (int t = 0; t < TT; ++t) m[t] = m0 + 16 * t + li < n ? m0 + 16 * t + li : n - 1;
+  f32x4 acc[TT][NT];
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int t = 0; t < TT; ++t)
 #pragma unroll
     for (int p = 0; p < NT; ++p) acc[t][p] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int s0 = begin + w * U; s0 < end; s0 += 4 * U) {
-    u32x4 x[U][2], b[U][NT];
+    u32x4 x[U][TT], b[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t k = (s0 + u < end ? s0 + u : end - 1) * 32 + 8 * lg;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) x[u][t] = *reinterpret_cast<const u32x4*>(jb.X + m[t] * K + k);
+      for (int t = 0; t < TT; ++t) x[u][t] = *reinterpret_cast<const u32x4*>(jb.X + m[t] * K + k);
 #pragma unroll
       for (int p = 0; p < NT; ++p) b[u][p] = *reinterpret_cast<const u32x4*>(jb.M + (p * 16 + li) * K + k);
     }
@@ -246,7 +268,7 @@ __global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n
     for (int u = 0; u < U; ++u) {
       const int64_t k = (s0 + u < end ? s0 + u : end - 1) * 32 + 8 * lg;
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
+      for (int t = 0; t < TT; ++t) {
         u32x4 v = s0 + u < end ? x[u][t] : u32x4{0u, 0u, 0u, 0u};
         if (thr != 0) v = drop8(v, key, static_cast<uint64_t>(m[t] * K + k), thr);
 #pragma unroll
@@ -256,7 +278,7 @@ __global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n
   }
   if (w > 0)
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
       for (int p = 0; p < NT; ++p)
 #pragma unroll
@@ -265,7 +287,7 @@ __global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n
   if (w > 0) return;
   float* o = jb.out + static_cast<int64_t>(q) * n * (16 * NT);
 #pragma unroll
-  for (int t = 0; t < 2; ++t)
+  for (int t = 0; t < TT; ++t)
 #pragma unroll
     for (int p = 0; p < NT; ++p)
 #pragma unroll
@@ -513,7 +535,7 @@ hipError_t launch_prepare(PrepareArgs p, const Base4& b, PrepareBase kind, hipSt
   p.base_wgs = kind == kBaseNone         ? 0
                : kind == kBaseTransposed ? static_cast<unsigned>((a.rows_pad / kTurnRows) * ((a.cols + kTurnCols - 1) / kTurnCols))
                : kind == kBaseCodesOfX   ? blocks_for(p.n * p.steps * (kMxStep / 8))
-                                         : blocks_for(a.rows * a.cols / 8);
+                                         : blocks_for((a.rows * a.cols + 31) / 32);
   const unsigned pad_wgs = p.padded != nullptr ? blocks_for(p.n * (a.rows_pad / 8)) : 0;
   const dim3 grid(p.base_wgs + p.operand_wgs + pad_wgs);
   if (grid.x == 0) return hipSuccess;
