@@ -244,8 +244,9 @@ loftq_status_t loftq_dropout(const void* X, loftq_dtype_t dt, int64_t n, const l
  *   Y      [device] n_tok x rows of dtype ydt out
  *   ws     [device] loftq_qlora_forward_dropout_workspace_bytes(n_tok, rows, cols, r) bytes
  *          (it holds bf16(deq(Q)) during the call)
- * Without B and A there is no adapter term and drop has no effect.
- * UNSUPPORTED: cols % 64 != 0, r > 64, or a launch of 2^32 work-items. */
+ * Without B and A there is no adapter term and drop has no effect.  alpha s must be finite.
+ * UNSUPPORTED: cols % 64 != 0, r > 64, cols >= 2^22, or a launch of 2^32 work-items (2^26
+ * tokens, 2^35 weights). */
 loftq_status_t loftq_qlora_forward_dropout(const void* X, int64_t n_tok, int64_t rows, int64_t cols,
                                            const uint8_t* packed, const float* absmax, const int8_t* qabsmax,
                                            const float* dq_scale, int32_t bits, const float* B, const float* A,
@@ -264,7 +265,7 @@ size_t loftq_qlora_forward_dropout_workspace_bytes(int64_t n_tok, int64_t rows, 
  *   dX      [device] n_tok x cols of dtype xdt out, or NULL
  *   dB, dA  [device] fp32 rows x r and r x cols out, or both NULL (always without B and A)
  *   ws      [device] loftq_qlora_backward_workspace_bytes(n_tok, rows, cols, r) bytes
- * n_tok = 0 writes zeros to dB and dA.  UNSUPPORTED as the forward, and rows = 0. */
+ * n_tok = 0 writes zeros to dB and dA.  UNSUPPORTED as the forward, rows = 0 and rows >= 2^22. */
 loftq_status_t loftq_qlora_backward(const void* dY, const void* X, int64_t n_tok, int64_t rows, int64_t cols,
                                     const uint8_t* packed, const float* absmax, const int8_t* qabsmax,
                                     const float* dq_scale, int32_t bits, const float* B, const float* A, int32_t r,
@@ -305,7 +306,7 @@ loftq_status_t loftq_mxfp4_dequantize(const uint8_t* packed, const uint8_t* scal
  * Products accumulate in fp32.  drop, Y, ydt as loftq_qlora_forward_dropout (serving: NULL).
  *   X       [device] n_tok x cols bf16
  *   ws      [device] loftq_mxfp4_forward_workspace_bytes(n_tok, rows, cols, r) bytes
- * UNSUPPORTED: cols % 32 != 0, r > 64, or a launch of 2^32 work-items. */
+ * UNSUPPORTED: cols % 32 != 0, else as loftq_qlora_forward_dropout. */
 loftq_status_t loftq_mxfp4_forward(const void* X, int64_t n_tok, int64_t rows, int64_t cols, const uint8_t* packed,
                                    const uint8_t* scales, const float* B, const float* A, int32_t r, float alpha,
                                    const loftq_dropout_t* drop, void* Y, loftq_dtype_t ydt, void* ws, size_t ws_bytes,
@@ -313,7 +314,7 @@ loftq_status_t loftq_mxfp4_forward(const void* X, int64_t n_tok, int64_t rows, i
 size_t loftq_mxfp4_forward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t r);
 
 /* Its gradient: loftq_qlora_backward over the MXFP4 weight's bf16 values (the rounding of X
- * passes the gradient as it is).  UNSUPPORTED as the forward, and rows = 0. */
+ * passes the gradient as it is).  UNSUPPORTED as the forward, rows = 0 and rows >= 2^22. */
 loftq_status_t loftq_mxfp4_backward(const void* dY, const void* X, int64_t n_tok, int64_t rows, int64_t cols,
                                     const uint8_t* packed, const uint8_t* scales, const float* B, const float* A,
                                     int32_t r, float alpha, const loftq_dropout_t* drop, void* dX, loftq_dtype_t xdt,

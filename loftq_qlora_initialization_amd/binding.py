@@ -382,7 +382,7 @@ def _dropout(p, seed, offset, step, dev):
     at = None if step is None else _expect(step, "step", dev, torch.int64, (1,))
     if p == 0:
         return None
-    return ctypes.byref(LoftqDropout(p, seed & _M64, offset & _M64, at))
+    return ctypes.byref(LoftqDropout(p, int(seed) & _M64, int(offset) & _M64, at))
 
 
 def _out_dtype(t, dtype):
@@ -482,7 +482,7 @@ def loftq_dropout(X: torch.Tensor, p: float, seed: int, offset: int = 0, step: O
         out = torch.empty_like(X)
     y = _expect(out, "out", dev, X.dtype, X.shape)
     at = None if step is None else _expect(step, "step", dev, torch.int64, (1,))
-    drop = LoftqDropout(p, seed & _M64, offset & _M64, at)
+    drop = LoftqDropout(p, int(seed) & _M64, int(offset) & _M64, at)
     _call("loftq_dropout", _c_dropout, dev, stream, X.data_ptr(), dtype, X.numel(), ctypes.byref(drop), y)
     return out
 

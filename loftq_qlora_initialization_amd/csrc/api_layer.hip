@@ -101,7 +101,7 @@ BackwardSpace backward_space(void* ws, i64 n, i64 rows, i64 cols, int r) {
 // their 32-bit thread numbers run over.
 bool layer_shape_ok(i64 n, i64 rows, i64 cols, int r) {
   const i64 limit = (i64(1) << 32) - 4096, rp = rank_pad(r), rows_pad = pad_to(rows, 64);
-  if (!tile_product_shape_ok(n, rows, cols) || !tile_product_shape_ok(n, cols, rows_pad)) return false;
+  if (!tile_product_shape_ok(n, rows, cols) || !tile_product_shape_ok(n, cols, 0)) return false;
   const i64 base = rows_pad * (cols / 8 + 16), codes = n * mx_steps(cols) * 32, pad = n * (rows_pad / 8);
   const i64 operands = (rp + adapter_ld(static_cast<int>(rp))) * (cols + rows_pad);
   return (base > codes ? base : codes) + pad + operands < limit && pad_to(n, 64) * 64 < limit && rows < limit / 64;
@@ -132,7 +132,7 @@ loftq_status_t check_layer(i64 n, i64 rows, i64 cols, const Base4& b, bool mx, c
   }
   if ((B == nullptr) != (A == nullptr)) return LOFTQ_ERR_INVALID_ARG;
   if (B != nullptr && r < 1) return LOFTQ_ERR_INVALID_ARG;
-  if (!std::isfinite(alpha) || !drop_ok(drop)) return LOFTQ_ERR_INVALID_ARG;
+  if (!std::isfinite(alpha) || !drop_ok(drop) || !std::isfinite(alpha * drop_arg(drop).scale)) return LOFTQ_ERR_INVALID_ARG;
   return LOFTQ_OK;
 }
 
@@ -227,7 +227,7 @@ loftq_status_t layer_backward(const void* dY, const void* X, i64 n, i64 rows, i6
   if (dX && !dtype_ok(xdt)) return LOFTQ_ERR_INVALID_ARG;
   if ((dB == nullptr) != (dA == nullptr) || (dB && !B)) return LOFTQ_ERR_INVALID_ARG;
   if (!dX && !dB) return LOFTQ_ERR_INVALID_ARG;
-  if (rows == 0) return LOFTQ_ERR_UNSUPPORTED;
+  if (rows == 0 || rows >= i64(1) << 22) return LOFTQ_ERR_UNSUPPORTED;   // rows are the product's K
   st = check_layer_buffers(n, rows, cols, base, mx, B, A, r);
   if (st != LOFTQ_OK) return st;
   if ((dX && !aligned16(dX)) || (dB && (!aligned16(dB) || !aligned16(dA)))) return LOFTQ_ERR_INVALID_ARG;

@@ -426,6 +426,55 @@ def test_same_results_again_and_on_a_stream(lib, base):
     assert torch.equal(layer.forward(lib, p=0.1, seed=1, step=two), Y)
 
 
+def test_two_streams_at_once(lib):
+    """Calls with workspaces of their own may overlap on two streams."""
+    a, b = Layer(300, 512, 1024, 16, "nf", seed=16), Layer(280, 448, 992, 32, "mx", seed=17)
+    rng = dict(p=0.2, seed=5, offset=1)
+    want = [(x.forward(lib, **rng), *x.backward(lib, **rng)) for x in (a, b)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for st in streams:
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(5):
+        for i, x in enumerate((a, b)):
+            with torch.cuda.stream(streams[i]):
+                got[i].append((x.forward(lib, **rng), *x.backward(lib, **rng)))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for once in got[i]:
+            assert all(torch.equal(x, y) for x, y in zip(once, want[i]))
+
+
+def test_captured_serving(lib):
+    """The few-token and the tiled product over MXFP4 in one graph, sharing a workspace, replayed on new inputs."""
+    layer = Layer(40, 192, 288, 16, "mx", seed=18)
+    ws = torch.empty(lib.mxfp4_forward_workspace_bytes(40, 192, 288, 16), dtype=torch.uint8, device="cuda")
+    X = layer.Xd.clone()
+    one, many = torch.empty(1, 192, device="cuda"), torch.empty(40, 192, device="cuda")
+    kw = dict(shape=layer.shape, B=layer.Bd, A=layer.Ad, alpha=0.5, ws=ws, **layer.kw)
+
+    def serve():
+        lib.loftq_mxfp4_forward(X, out=many, **kw)
+        lib.loftq_mxfp4_forward(X[:1], out=one, **kw)
+
+    serve()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        serve()
+    for k in range(4):
+        X.copy_(torch.randn(40, 288, device="cuda"))
+        graph.replay()
+        got = one.clone(), many.clone()
+        serve()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], one) and torch.equal(got[1], many)
+        layer.X, layer.Xd = X.double().cpu().numpy(), X
+        layer.check_forward(many, alpha=0.5)
+        layer.X = layer.X[:1]
+        layer.check_forward(one, alpha=0.5)
+
+
 def test_captured_training_step(lib):
     """Forward and gradient in one graph that counts its own step: each replay draws that step's mask."""
     layer = Layer(96, 192, 256, 16, dq=True, seed=10)

@@ -55,9 +55,10 @@ def test_layer_refusals(b, call, mx):
     for kw in (dict(n=-1), dict(n=1 << 31), dict(rows=-1), dict(rows=1 << 31), dict(packed=None), dict(packed=FAKE + 8),
                dict(scale=None), dict(scale=FAKE + 8), dict(B=None), dict(A=None), dict(B=FAKE + 4), dict(r=0),
                dict(alpha=float("nan")), dict(alpha=float("inf")), dict(X=None), dict(X=FAKE + 2), dict(ws=None),
-               dict(ws=FAKE + 8), dict(drop=drop(b, 2.0)), dict(drop=drop(b, step=FAKE + 4))):
+               dict(ws=FAKE + 8), dict(alpha=3e38, drop=drop(b, 0.9)), dict(drop=drop(b, 2.0)), dict(drop=drop(b, step=FAKE + 4))):
         assert bad(**kw) == INVALID, kw
-    for kw in (dict(r=65), dict(cols=0), dict(cols=100), dict(cols=16), dict(n=(1 << 31) - 1, rows=1 << 20)):
+    for kw in (dict(r=65), dict(cols=0), dict(cols=100), dict(cols=16), dict(n=(1 << 31) - 1, rows=1 << 20),
+               dict(cols=1 << 22)):
         assert bad(**kw) == UNSUPPORTED, kw
     assert bad(ws_bytes=255) == WORKSPACE
     if not mx:
@@ -75,7 +76,7 @@ def test_forward_and_backward_outputs(b, mx):
     assert bwd(b, mx, dX=FAKE + 4) == INVALID and bwd(b, mx, xdt=3) == INVALID
     assert bwd(b, mx, dX=None, dB=None, dA=None) == INVALID         # nothing asked for
     assert bwd(b, mx, B=None, A=None) == INVALID                    # gradients of no adapter
-    assert bwd(b, mx, rows=0) == UNSUPPORTED
+    assert bwd(b, mx, rows=0) == UNSUPPORTED and bwd(b, mx, rows=1 << 22) == UNSUPPORTED
     assert bwd(b, mx, n=0, dB=None, dA=None) == OK
 
 
