@@ -3,6 +3,13 @@
 // gradients (features x r) as products over the tokens.  A gradient needs two of each,
 // over dY and over X: one launch takes both, as two jobs of one grid.
 //
+// All of it is bound by loads: the arithmetic of the thin products is a hundredth of the
+// layer's.  Gradient of 2048 tokens x (11008 x 4096), r = 64: base and operands 36 us (25 MB
+// of codes in, 90 MB of bf16 out), dY B and X A^T 33 us, their sums 8 us, dB and dA 38 us (62
+// MB of dY and X, at one wave per SIMD: the sums of 128 features fill the registers), their
+// sums 6 us.  8192 tokens x (4096 x 11008), r = 16: 38, 79, 5, 60 and 5 us, X's mask being
+// drawn twice.
+//
 // v_mfma_f32_16x16x32_bf16: lane L supplies A[L%16][8(L/16) + j] and
 // B[8(L/16) + j][L%16] (j = 0..7) and receives D[4(L/16) + v][L%16] in element v.
 #include "layer.h"

