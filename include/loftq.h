@@ -245,7 +245,7 @@ loftq_status_t loftq_dropout(const void* X, loftq_dtype_t dt, int64_t n, const l
  *   ws     [device] loftq_qlora_forward_dropout_workspace_bytes(n_tok, rows, cols, r) bytes
  *          (it holds bf16(deq(Q)) during the call)
  * Without B and A there is no adapter term and drop has no effect.  alpha s must be finite.
- * UNSUPPORTED: cols % 64 != 0, r > 64, cols >= 2^22, or a launch of 2^32 work-items (2^26
+ * UNSUPPORTED: cols % 64 != 0, r > 64, cols >= 2^22, or a launch of 2^32 work-items (2^25
  * tokens, 2^35 weights). */
 loftq_status_t loftq_qlora_forward_dropout(const void* X, int64_t n_tok, int64_t rows, int64_t cols,
                                            const uint8_t* packed, const float* absmax, const int8_t* qabsmax,

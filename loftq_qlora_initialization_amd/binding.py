@@ -477,7 +477,10 @@ def loftq_dropout(X: torch.Tensor, p: float, seed: int, offset: int = 0, step: O
                   out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """X / (1 - p) where the mask of (p, seed, offset + step) keeps, else 0; the gradient is the same call
     on dY.  `step` is a one-element int64 device tensor that is read when the kernel runs.  `out` may be X."""
-    dev, dtype = _first(X, "X"), _wdtype(X)
+    dev = _first(X, "X")
+    if X.dtype not in _FLOATS:
+        raise TypeError("X must be float32 or bfloat16")
+    dtype = LOFTQ_BF16 if X.dtype is torch.bfloat16 else LOFTQ_F32
     if out is None:
         out = torch.empty_like(X)
     y = _expect(out, "out", dev, X.dtype, X.shape)

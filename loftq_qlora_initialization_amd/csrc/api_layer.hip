@@ -104,7 +104,7 @@ bool layer_shape_ok(i64 n, i64 rows, i64 cols, int r) {
   if (!tile_product_shape_ok(n, rows, cols) || !tile_product_shape_ok(n, cols, 0)) return false;
   const i64 base = rows_pad * (cols / 8 + 16), codes = n * mx_steps(cols) * 32, pad = n * (rows_pad / 8);
   const i64 operands = (rp + adapter_ld(static_cast<int>(rp))) * (cols + rows_pad);
-  return (base > codes ? base : codes) + pad + operands < limit && pad_to(n, 64) * 64 < limit && rows < limit / 64;
+  return (base > codes ? base : codes) + pad + operands < limit && pad_to(n, 64) * 128 < limit && rows < limit / 64;
 }
 
 bool drop_ok(const loftq_dropout_t* d) {
