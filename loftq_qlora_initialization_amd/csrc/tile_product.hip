@@ -32,7 +32,6 @@ namespace loftq {
 namespace {
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -414,7 +413,7 @@ constexpr TileShape kShapes[] = {
     {256, 256, 1, 1.54f, 1.87f, 9.f},
     {192, 256, 1, 1.20f, 1.45f, 9.f},
     {128, 256, 1, 0.80f, 1.06f, 8.f},
-    {64, 128, 2, 0.50f, 0.60f, 6.f},
+    {64, 128, 2, 0.50f, 0.69f, 8.f},
 };
 
 }  // namespace
