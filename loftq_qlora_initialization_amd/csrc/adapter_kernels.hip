@@ -5,13 +5,14 @@
 //
 // All of it is bound by loads: the arithmetic of the thin products is a hundredth of the
 // layer's.  Gradient of 2048 tokens x (11008 x 4096), r = 64: base and operands 36 us (25 MB
-// of codes in, 90 MB of bf16 out), dY B and X A^T 33 us, their sums 8 us, dB and dA 38 us (62
-// MB of dY and X, at one wave per SIMD: the sums of 128 features fill the registers), their
-// sums 6 us.  8192 tokens x (4096 x 11008), r = 16: 38, 79, 5, 60 and 5 us, X's mask being
-// drawn twice.
+// of codes in, 90 MB of bf16 out), dY B and X A^T 33 us (their second operand, from L2,
+// is as many bytes as four 16-token tiles of dY), their sums 8 us, dB and dA 27 us (62 MB of dY
+// and X), their sums 6 us.  8192 tokens x (4096 x 11008), r = 16: 38, 80, 5, 53 and 5 us, X's
+// mask being drawn twice.
 //
 // v_mfma_f32_16x16x32_bf16: lane L supplies A[L%16][8(L/16) + j] and
 // B[8(L/16) + j][L%16] (j = 0..7) and receives D[4(L/16) + v][L%16] in element v.
+#include "buffer.h"
 #include "layer.h"
 
 namespace loftq {
@@ -238,46 +239,52 @@ __device__ __forceinline__ u32x4 drop8(u32x4 v, uint64_t key, uint64_t e, uint32
 // ---- thin product over the features: partial q of keep(X) M^T over the q-th K range ----
 // A workgroup takes 32 tokens and one range, which its four waves share U steps of 32 at a
 // time; M (rank-major, K along its rows) serves both 16-token tiles.  All loads of U steps
-// are issued before the first product; steps past the range repeat its last one with the
-// tokens zeroed.  The waves' sums meet in LDS.
+// are issued before the first product.  The waves' sums meet in LDS.
 template <int NT>
 __global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n) {
-  constexpr int TT = 2, U = NT <= 2 ? 4 : 2;
-  __shared__ float part[3][TT * NT * 4 * 64];
+  constexpr int U = NT <= 2 ? 4 : 2;
+  __shared__ float part[3][2 * NT * 4 * 64];
   const DownJob& jb = jobs.job[blockIdx.x < jobs.job[0].wgs ? 0 : 1];
   const uint32_t wg = blockIdx.x < jobs.job[0].wgs ? blockIdx.x : blockIdx.x - jobs.job[0].wgs;
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6, li = lane & 15, lg = lane >> 4;
-  const int64_t K = jb.K, m0 = static_cast<int64_t>(wg / jb.ks) * (16 * TT);
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), li = lane & 15, lg = lane >> 4;
+  const int64_t K = jb.K, m0 = static_cast<int64_t>(wg / jb.ks) * 32;
   const int q = wg % jb.ks, steps = static_cast<int>(K / 32), per = (steps + jb.ks - 1) / jb.ks;
-  const int begin = q * per, end = begin + per < steps ? begin + per : steps;
+  const int begin = __builtin_amdgcn_readfirstlane(q * per), end = begin + per < steps ? begin + per : steps;
   const uint32_t thr = jb.drop.thr;
   const uint64_t key = thr != 0 ? drop_key(jb.drop) : 0;
-  int64_t m[TT];
+  // this lane's offsets from a step's first bytes; tokens past the last and steps past the
+  // range are zeros
+  uint32_t xat[2], bat[NT];
 #pragma unroll
-  for (int t = 0; t < TT; ++t) m[t] = m0 + 16 * t + li < n ? m0 + 16 * t + li : n - 1;
-  f32x4 acc[TT][NT];
+  for (int t = 0; t < 2; ++t) xat[t] = static_cast<uint32_t>(((t * 16 + li) * K + 8 * lg) * 2);
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
+  for (int p = 0; p < NT; ++p) bat[p] = static_cast<uint32_t>(((p * 16 + li) * K + 8 * lg) * 2);
+  f32x4 acc[2][NT];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int p = 0; p < NT; ++p) acc[t][p] = f32x4{0.f, 0.f, 0.f, 0.f};
   for (int s0 = begin + w * U; s0 < end; s0 += 4 * U) {
-    u32x4 x[U][TT], b[U][NT];
+    u32x4 x[U][2], b[U][NT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t k = (s0 + u < end ? s0 + u : end - 1) * 32 + 8 * lg;
+      const int64_t k = static_cast<int64_t>(s0 + u) * 32;
+      const bool any = s0 + u < end;
+      const __amdgpu_buffer_rsrc_t xb = buffer_of(jb.X + m0 * K + k, any ? ((n - m0) * K - k) * 2 : 0);
+      const __amdgpu_buffer_rsrc_t bb = buffer_at(jb.M + k, any);
 #pragma unroll
-      for (int t = 0; t < TT; ++t) x[u][t] = *reinterpret_cast<const u32x4*>(jb.X + m[t] * K + k);
+      for (int t = 0; t < 2; ++t) x[u][t] = __builtin_amdgcn_raw_buffer_load_b128(xb, xat[t], 0, 0);
 #pragma unroll
-      for (int p = 0; p < NT; ++p) b[u][p] = *reinterpret_cast<const u32x4*>(jb.M + (p * 16 + li) * K + k);
+      for (int p = 0; p < NT; ++p) b[u][p] = __builtin_amdgcn_raw_buffer_load_b128(bb, bat[p], 0, 0);
     }
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t k = (s0 + u < end ? s0 + u : end - 1) * 32 + 8 * lg;
 #pragma unroll
-      for (int t = 0; t < TT; ++t) {
-        u32x4 v = s0 + u < end ? x[u][t] : u32x4{0u, 0u, 0u, 0u};
-        if (thr != 0) v = drop8(v, key, static_cast<uint64_t>(m[t] * K + k), thr);
+      for (int t = 0; t < 2; ++t) {
+        u32x4 v = x[u][t];
+        if (thr != 0)
+          v = drop8(v, key, static_cast<uint64_t>((m0 + 16 * t + li) * K + static_cast<int64_t>(s0 + u) * 32 + 8 * lg), thr);
 #pragma unroll
         for (int p = 0; p < NT; ++p) acc[t][p] = mfma16(v, b[u][p], acc[t][p]);
       }
@@ -285,7 +292,7 @@ __global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n
   }
   if (w > 0)
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
+    for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int p = 0; p < NT; ++p)
 #pragma unroll
@@ -294,7 +301,7 @@ __global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n
   if (w > 0) return;
   float* o = jb.out + static_cast<int64_t>(q) * n * (16 * NT);
 #pragma unroll
-  for (int t = 0; t < TT; ++t)
+  for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int p = 0; p < NT; ++p)
 #pragma unroll
@@ -366,16 +373,19 @@ __global__ __launch_bounds__(kThreads) void down_sum_kernel(DownSumJobs jobs, in
 // one lane, and L's tokens are rows: lane L loads 8 tokens x 8 features (16 bytes of 8
 // rows) and turns the 8 x 8 block round in its registers, which gives the operands of 8
 // products, the j-th for features 8 (L%16) + j.  A workgroup takes 128 features and a token
-// range, which its four waves share 32 tokens at a time, the next step's loads in flight
+// range, which its four waves share 32 tokens at a time, the next step's rows of L in flight
 // while one is multiplied; past 32 ranks two waves share a step, half of the ranks each (the
-// sums of all of them leave a wave no registers for its loads).  The sums meet in LDS.  kRankMajor (dA): S is the first operand, so a
+// sums of all of them leave a wave no registers for its loads).  S's operands are loaded when
+// their step begins: ahead of it they cost the second wave per SIMD (38 against 27 us at 2048
+// tokens of 11008 and 4096 features, r = 64).  The sums meet in LDS.  kRankMajor (dA): S is the first operand, so a
 // lane holds 8 consecutive features of a rank; else (dB) a lane's rank is L%16.
 template <int NR, bool kRankMajor>
 __device__ __forceinline__ void grad_job(const GradJob& jb, uint32_t wg, int64_t n, int64_t n_pad, int r,
                                          float (*part)[8 * (NR > 2 ? 2 : NR) * 4 * 64]) {
   constexpr int kParts = NR > 2 ? 2 : 1, NT = NR > 2 ? 2 : NR, kWaves = 4 / kParts;   // waves per step's ranks, of a rank half
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
-  const int half = (threadIdx.x >> 6) % kParts, w = (threadIdx.x >> 6) / kParts, tile0 = half * NT;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int half = wave % kParts, w = wave / kParts, tile0 = half * NT;
   const int64_t group = wg / jb.ts, F = jb.F;
   const int q = wg % jb.ts;
   const int64_t f0 = group * 128 + 8 * li, f = f0 < F ? f0 : F - 8;   // F % 8 == 0
@@ -388,27 +398,34 @@ __device__ __forceinline__ void grad_job(const GradJob& jb, uint32_t wg, int64_t
   for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  u32x4 x[2][8], b[2][3][NT];
-  auto load = [&](int set, int s) __attribute__((always_inline)) {
-    const int64_t t0 = static_cast<int64_t>(s < end ? s : end - 1) * 32 + 8 * lg;
+  // this lane's offsets from a step's first bytes; tokens past the last are zeros
+  uint32_t xat[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      x[set][i] = *reinterpret_cast<const u32x4*>(jb.L + (t0 + i < n ? t0 + i : n - 1) * F + f);
+  for (int i = 0; i < 8; ++i) xat[i] = static_cast<uint32_t>(((8 * lg + i) * F + f) * 2);
+  const uint32_t bat = static_cast<uint32_t>((li * n_pad + 8 * lg) * 2);
+  u32x4 x[2][8], b[3][NT];
+  auto load = [&](int set, int s) __attribute__((always_inline)) {
+    const int64_t t0 = static_cast<int64_t>(s) * 32;
+    const __amdgpu_buffer_rsrc_t xb = buffer_of(jb.L + t0 * F, s < end ? (n - t0) * F * 2 : 0);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[set][i] = __builtin_amdgcn_raw_buffer_load_b128(xb, xat[i], 0, 0);
+  };
+  auto load_s = [&](int s) __attribute__((always_inline)) {
+    const int64_t t0 = static_cast<int64_t>(s) * 32;
 #pragma unroll
     for (int h = 0; h < 3; ++h)
 #pragma unroll
       for (int t = 0; t < NT; ++t) {   // of an odd number of rank tiles the last half's second repeats the first
         const int tile = tile0 + t < NR ? tile0 + t : tile0;
-        b[set][h][t] = *reinterpret_cast<const u32x4*>(jb.St + (h * 16 * NR + tile * 16 + li) * n_pad + t0);
+        b[h][t] = __builtin_amdgcn_raw_buffer_load_b128(
+            buffer_at(jb.St + static_cast<int64_t>(h * 16 * NR + tile * 16) * n_pad + t0, s < end), bat, 0, 0);
       }
   };
   auto multiply = [&](int set, int s) __attribute__((always_inline)) {
-    const int64_t t0 = static_cast<int64_t>(s) * 32 + 8 * lg;
+    if (thr != 0)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (t0 + i >= n) x[set][i] = u32x4{0u, 0u, 0u, 0u};
-      if (thr != 0) x[set][i] = drop8(x[set][i], key, static_cast<uint64_t>((t0 + i) * F + f), thr);
-    }
+      for (int i = 0; i < 8; ++i)
+        x[set][i] = drop8(x[set][i], key, static_cast<uint64_t>((static_cast<int64_t>(s) * 32 + 8 * lg + i) * F + f), thr);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       u32x4 lo, hi;   // features 2 c and 2 c + 1: tokens 0 .. 7
@@ -421,20 +438,22 @@ __device__ __forceinline__ void grad_job(const GradJob& jb, uint32_t wg, int64_t
       for (int h = 0; h < 3; ++h)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          acc[2 * c][t] = kRankMajor ? mfma16(b[set][h][t], lo, acc[2 * c][t])
-                                     : mfma16(lo, b[set][h][t], acc[2 * c][t]);
+          acc[2 * c][t] = kRankMajor ? mfma16(b[h][t], lo, acc[2 * c][t])
+                                     : mfma16(lo, b[h][t], acc[2 * c][t]);
           acc[2 * c + 1][t] =
-              kRankMajor ? mfma16(b[set][h][t], hi, acc[2 * c + 1][t])
-                         : mfma16(hi, b[set][h][t], acc[2 * c + 1][t]);
+              kRankMajor ? mfma16(b[h][t], hi, acc[2 * c + 1][t])
+                         : mfma16(hi, b[h][t], acc[2 * c + 1][t]);
         }
     }
   };
   if (begin + w < end) {
     load(0, begin + w);
     for (int s = begin + w; s < end; s += 2 * kWaves) {
+      load_s(s);
       load(1, s + kWaves);
       multiply(0, s);
       if (s + kWaves >= end) break;
+      load_s(s + kWaves);
       load(0, s + 2 * kWaves);
       multiply(1, s + kWaves);
     }
@@ -499,7 +518,7 @@ __device__ __forceinline__ void grad_job(const GradJob& jb, uint32_t wg, int64_t
 
 // job 0: dB over dY; job 1: dA over X
 template <int NT>
-__global__ __launch_bounds__(kThreads) void grad_kernel(GradJobs jobs, int64_t n, int64_t n_pad, int r) {
+__global__ __launch_bounds__(kThreads, 2) void grad_kernel(GradJobs jobs, int64_t n, int64_t n_pad, int r) {
   __shared__ float part[2][8 * (NT > 2 ? 2 : NT) * 4 * 64];
   if (blockIdx.x < jobs.job[0].wgs)
     grad_job<NT, false>(jobs.job[0], blockIdx.x, n, n_pad, r, part);

@@ -24,6 +24,7 @@
 // line is fetched twice), the reads of a quarter step before its products (all waves read,
 // then all multiply), 16 x 16 instructions in FP4 (the scales of twice the rows: 77 against 67
 // us at 2048 x 11008, K = 4096).
+#include "buffer.h"
 #include "layer.h"
 
 #include <type_traits>
@@ -46,13 +47,6 @@ __device__ __forceinline__ void static_for(F&& f) {
     static_for<N - 1>(f);
     f(std::integral_constant<int, N - 1>{});
   }
-}
-
-// A buffer resource over `p`, for loads with a scalar base and 32-bit lane offsets that are
-// bounded before.  Where nothing is left to load it holds no records: such loads touch no
-// memory and give zeros, so that a loop can issue them to its end without a branch.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_at(const char* p, bool any) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<char*>(p), 0, __builtin_amdgcn_readfirstlane(any ? -1 : 0), 0x00027000);
 }
 
 // the largest divisor of n that is at most `most` (0: none)

@@ -361,6 +361,26 @@ def test_outputs_are_overwritten_and_nothing_else(lib):
         assert (ws[need:] == fill).all()
 
 
+@pytest.mark.parametrize("base,n,rows,cols", [("nf", 45, 100, 192), ("nf", 70, 128, 320), ("mx", 13, 96, 96), ("mx", 77, 130, 288)])
+def test_nothing_behind_the_inputs_is_used(lib, base, n, rows, cols):
+    """Inputs that end where NaN begins (every byte 255 behind each) give what they give by themselves."""
+    layer = Layer(n, rows, cols, 20, base, seed=19)
+    rng = dict(p=0.3, seed=9, offset=1)
+    want = (layer.forward(lib, **rng), layer.forward(lib), *layer.backward(lib, **rng))
+
+    def fenced(t):
+        raw = t.contiguous().view(torch.uint8).reshape(-1)
+        big = torch.full((raw.numel() + (1 << 16),), 255, dtype=torch.uint8, device="cuda")
+        big[: raw.numel()] = raw
+        return big[: raw.numel()].view(t.dtype).view(t.shape)
+
+    for name in ("Xd", "Gd", "Ad", "Bd"):
+        setattr(layer, name, fenced(getattr(layer, name)))
+    layer.kw = {k: fenced(v) if torch.is_tensor(v) else v for k, v in layer.kw.items()}
+    got = (layer.forward(lib, **rng), layer.forward(lib), *layer.backward(lib, **rng))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 @pytest.mark.parametrize("n", [7, 300])
 def test_mx_forward_of_what_is_not_finite(lib, n):
     """A NaN or an infinity makes its block of 32 columns NaN, and with it its token's results, and no other's."""
