@@ -86,9 +86,12 @@ struct Tile {
   static constexpr int kRows = TM + TN;              // LDS rows: features, then tokens
   static constexpr int kBuf = kRows * kStepBytes;
   static constexpr int kLoadsW = TN * 8 / kThreads, kLoadsX = TM * 8 / kThreads, kLoads = kLoadsW + kLoadsX;
-  static constexpr int kEvery = kPhases * NT * MT >= 2 * kLoads ? 2 : 1;   // products from one load to the next
+  // products from one load to the next: close together where a step's loads have one step's
+  // time, further apart in a deeper ring (2048 x 4096, K = 11008: 169 -> 163 us)
+  static constexpr int kProducts = kPhases * NT * MT;
+  static constexpr int kEvery = R > 2 && kProducts >= 4 * kLoads ? 4 : (kProducts >= 2 * kLoads ? 2 : 1);
   static_assert(TN * 8 % kThreads == 0 && TM * 8 % kThreads == 0, "whole 16-byte pieces of either operand per thread");
-  static_assert(kPhases * NT * MT >= kLoads * kEvery, "a step's products take its loads between them");
+  static_assert(kProducts >= kLoads * kEvery, "a step's products take its loads between them");
   typedef frag_acc Acc[NT][MT];
 
   char* lds;
