@@ -13,10 +13,26 @@ namespace {
 
 constexpr int kMxThreads = 256;
 
-// One thread per 8 consecutive columns of the padded matrix.  kVec: cols % 8 == 0, so eight
-// elements are 16-byte loads; otherwise they are loaded one by one.
+// Eight elements of a row whose address is a multiple of their size only: rows of any length
+// are read and written in whole vectors (the memory system takes them at any address).
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  T v[8];
+  __builtin_memcpy(v, p, sizeof v);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(v[j]);
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  T v[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = static_cast<T>(x[j]);
+  __builtin_memcpy(p, v, sizeof v);
+}
+
+// One thread per 8 consecutive columns of the padded matrix.
 // R = W - B A is formed in fp32, the r products added in the order of p.
-template <typename T, bool kVec>
+template <typename T>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __restrict__ W, int64_t rows, int64_t cols,
                                                                  int64_t steps, const float* __restrict__ B,
                                                                  const float* __restrict__ A, int r,
@@ -27,16 +43,8 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __rest
   const int64_t row = id / per_row, c0 = static_cast<int64_t>(id % per_row) * 8;
   if (row >= rows) return;   // whole quads: per_row % 32 == 0
   float x[8];
-  if (kVec) {
-    if (c0 < cols) {
-      typedef T vec __attribute__((ext_vector_type(8)));
-      const vec w = *reinterpret_cast<const vec*>(W + row * cols + c0);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = static_cast<float>(w[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = 0.f;
-    }
+  if (c0 + 8 <= cols) {
+    load8(W + row * cols + c0, x);
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) x[j] = c0 + j < cols ? static_cast<float>(W[row * cols + c0 + j]) : 0.f;
@@ -62,7 +70,7 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __rest
 }
 
 // out = deq or W - deq, in fp32 or bf16; one thread per 8 columns.
-template <typename T, typename O, bool kHasW, bool kVec>
+template <typename T, typename O, bool kHasW>
 __global__ __launch_bounds__(kMxThreads) void mx_dequantize_kernel(const uint8_t* __restrict__ packed,
                                                                    const uint8_t* __restrict__ scales, int64_t rows,
                                                                    int64_t cols, int64_t steps,
@@ -76,25 +84,21 @@ __global__ __launch_bounds__(kMxThreads) void mx_dequantize_kernel(const uint8_t
   float v[8];
 #pragma unroll
   for (int j = 0; j < 8; ++j) v[j] = fp4_value(word >> (8 * (j >> 1) + (j & 1 ? 0 : 4)) & 15u) * sc;
-  if (kVec) {
-    typedef T tvec __attribute__((ext_vector_type(8)));
-    typedef O ovec __attribute__((ext_vector_type(8)));
-    ovec o;
+  const int64_t at = row * cols + c0;
+  if (c0 + 8 <= cols) {
     if (kHasW) {
-      const tvec w = *reinterpret_cast<const tvec*>(W + row * cols + c0);
+      float w[8];
+      load8(W + at, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = static_cast<float>(w[j]) - v[j];
+      for (int j = 0; j < 8; ++j) v[j] = w[j] - v[j];
     }
+    store8(out + at, v);
+    return;
+  }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = static_cast<O>(v[j]);
-    *reinterpret_cast<ovec*>(out + row * cols + c0) = o;
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (c0 + j >= cols) break;
-      const float w = kHasW ? static_cast<float>(W[row * cols + c0 + j]) : 0.f;
-      out[row * cols + c0 + j] = static_cast<O>(kHasW ? w - v[j] : v[j]);
-    }
+  for (int j = 0; j < 8; ++j) {
+    if (c0 + j >= cols) break;
+    out[at + j] = static_cast<O>(kHasW ? static_cast<float>(W[at + j]) - v[j] : v[j]);
   }
 }
 
@@ -111,17 +115,11 @@ hipError_t launch_mx_quantize(const void* W, loftq_dtype_t wdt, int64_t rows, in
                               const float* A, int r, uint8_t* packed, uint8_t* scales, hipStream_t s) {
   const int64_t steps = mx_steps(cols);
   const dim3 grid(blocks_for(rows * steps * (kMxStep / 8)));
-#define LQ_MXQ(T, VEC)                                                                                            \
-  LQ_LAUNCH("mx_quantize", (mx_quantize_kernel<T, VEC>), grid, dim3(kMxThreads), 0, s, static_cast<const T*>(W), rows, \
-            cols, steps, B, A, r, packed, scales)
-  const bool vec = cols % 8 == 0;
-  if (wdt == LOFTQ_BF16) {
-    if (vec) LQ_MXQ(__bf16, true);
-    else LQ_MXQ(__bf16, false);
-  } else {
-    if (vec) LQ_MXQ(float, true);
-    else LQ_MXQ(float, false);
-  }
+#define LQ_MXQ(T)                                                                                                     \
+  LQ_LAUNCH("mx_quantize", (mx_quantize_kernel<T>), grid, dim3(kMxThreads), 0, s, static_cast<const T*>(W), rows, cols, \
+            steps, B, A, r, packed, scales)
+  if (wdt == LOFTQ_BF16) LQ_MXQ(__bf16);
+  else LQ_MXQ(float);
 #undef LQ_MXQ
   return hipGetLastError();
 }
@@ -130,21 +128,14 @@ hipError_t launch_mx_dequantize(const uint8_t* packed, const uint8_t* scales, in
                                 const void* W, loftq_dtype_t wdt, void* out, loftq_dtype_t odt, hipStream_t s) {
   const int64_t steps = mx_steps(cols);
   const dim3 grid(blocks_for(rows * ((cols + 7) / 8)));
-#define LQ_MXD(T, O, HASW, VEC)                                                                                       \
-  LQ_LAUNCH("mx_dequantize", (mx_dequantize_kernel<T, O, HASW, VEC>), grid, dim3(kMxThreads), 0, s, packed, scales, rows, \
-            cols, steps, static_cast<const T*>(W), static_cast<O*>(out))
-#define LQ_MXD_O(O)                                                  \
-  do {                                                               \
-    if (W == nullptr) {                                              \
-      if (cols % 8 == 0) LQ_MXD(float, O, false, true);              \
-      else LQ_MXD(float, O, false, false);                           \
-    } else if (wdt == LOFTQ_BF16) {                                  \
-      if (cols % 8 == 0) LQ_MXD(__bf16, O, true, true);              \
-      else LQ_MXD(__bf16, O, true, false);                           \
-    } else {                                                         \
-      if (cols % 8 == 0) LQ_MXD(float, O, true, true);               \
-      else LQ_MXD(float, O, true, false);                            \
-    }                                                                \
+#define LQ_MXD(T, O, HASW)                                                                                              \
+  LQ_LAUNCH("mx_dequantize", (mx_dequantize_kernel<T, O, HASW>), grid, dim3(kMxThreads), 0, s, packed, scales, rows, cols, \
+            steps, static_cast<const T*>(W), static_cast<O*>(out))
+#define LQ_MXD_O(O)                                            \
+  do {                                                         \
+    if (W == nullptr) LQ_MXD(float, O, false);                 \
+    else if (wdt == LOFTQ_BF16) LQ_MXD(__bf16, O, true);       \
+    else LQ_MXD(float, O, true);                               \
   } while (0)
   if (odt == LOFTQ_BF16) LQ_MXD_O(__bf16);
   else LQ_MXD_O(float);
