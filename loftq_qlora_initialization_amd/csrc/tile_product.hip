@@ -19,7 +19,7 @@
 // in the loop the clock stands at 1.75 to 1.85 GHz with the matrix cores busy 51 to 59 % of
 // the cycles; what a step waits for is its loads (without them a 256 x 256 step of FP4 takes
 // 1.4 instead of 1.9 us).  8192 x 11008 outputs, K = 4096: 655 to 670 us, 1.1 PFLOP/s; 2048 x
-// 4096, K = 11008: 147 to 165 us, 1.1 to 1.26; FP4 8192 x 28672, K = 8192: 1.06 ms, 3.6
+// 4096, K = 11008: 145 to 165 us, 1.1 to 1.27; FP4 8192 x 28672, K = 8192: 1.06 ms, 3.6
 // PFLOP/s.  Tried and slower: half steps in a ring of four (64-byte pieces of lines: every
 // line is fetched twice), the reads of a quarter step before its products (all waves read,
 // then all multiply), 16 x 16 instructions in FP4 (the scales of twice the rows: 77 against 67
