@@ -3,8 +3,8 @@
 // Without an adapter both are bound by memory: 11008 x 4096 fp32 to codes 42 us (204 MB, 4.9
 // TB/s), codes and W to the fp32 residual 61 us (385 MB, 6.3 TB/s).  Neighbouring threads take
 // neighbouring 16 or 32 bytes of a row; the codes of a thread are one word, so no LDS is needed.
-// A residual's r products run on the vector units (2 r operations an element: past r = 8 or so
-// they, not memory, set the time).
+// A residual's r products run on the vector units and the rows of A come from the caches; they,
+// not memory, set its time (11008 x 4096 bf16: 58 us at r = 16, 175 us at r = 64).
 #include "internal.h"
 #include "mxfp4.h"
 
@@ -30,9 +30,11 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
   __builtin_memcpy(p, v, sizeof v);
 }
 
-// One thread per 8 consecutive columns of the padded matrix.
-// R = W - B A is formed in fp32, the r products added in the order of p.
-template <typename T>
+// One thread per 8 consecutive columns of kRows rows of the padded matrix: one row of W, or
+// four of a residual R = W - B A, which share each load of A: 11008 x 4096 bf16 with 1, 2, 4 and
+// 8 rows takes 117, 71, 58 and 66 us at r = 16, and 419, 258, 175 and 172 us at r = 64 (8192 x
+// 28672: 2227, 1321, 864 and 963 us).  R is formed in fp32, the r products added in the order of p.
+template <typename T, int kRows>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __restrict__ W, int64_t rows, int64_t cols,
                                                                  int64_t steps, const float* __restrict__ B,
                                                                  const float* __restrict__ A, int r,
@@ -40,32 +42,52 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __rest
                                                                  uint8_t* __restrict__ scales) {
   const uint32_t id = blockIdx.x * kMxThreads + threadIdx.x;   // below 2^32
   const uint32_t per_row = static_cast<uint32_t>(steps * (kMxStep / 8));
-  const int64_t row = id / per_row, c0 = static_cast<int64_t>(id % per_row) * 8;
-  if (row >= rows) return;   // whole quads: per_row % 32 == 0
-  float x[8];
-  if (c0 + 8 <= cols) {
-    load8(W + row * cols + c0, x);
-  } else {
+  const int64_t row0 = static_cast<int64_t>(id / per_row) * kRows, c0 = static_cast<int64_t>(id % per_row) * 8;
+  if (row0 >= rows) return;   // whole quads: per_row % 32 == 0
+  const bool whole = c0 + 8 <= cols;
+  float x[kRows][8];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = c0 + j < cols ? static_cast<float>(W[row * cols + c0 + j]) : 0.f;
+  for (int i = 0; i < kRows; ++i) {   // rows past the last repeat it and are not stored
+    const T* src = W + (row0 + i < rows ? row0 + i : rows - 1) * cols + c0;
+    if (whole) {
+      load8(src, x[i]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = c0 + j < cols ? static_cast<float>(src[j]) : 0.f;
+    }
   }
-  if (r > 0) {
-    float ba[8] = {};
+  if constexpr (kRows > 1) {
+    float ba[kRows][8] = {};
     for (int p = 0; p < r; ++p) {
-      const float b = B[row * r + p];
+      float a[8];
+      const float* src = A + static_cast<int64_t>(p) * cols + c0;
+      if (whole) {
+        load8(src, a);
+      } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (c0 + j < cols) ba[j] = fmaf(b, A[static_cast<int64_t>(p) * cols + c0 + j], ba[j]);
+        for (int j = 0; j < 8; ++j) a[j] = c0 + j < cols ? src[j] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) {
+        const float b = B[(row0 + i < rows ? row0 + i : rows - 1) * r + p];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ba[i][j] = fmaf(b, a[j], ba[i][j]);
+      }
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] -= ba[j];
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)   // the padding stays zero, also where B is not finite
+        if (whole || c0 + j < cols) x[i][j] -= ba[i][j];
   }
-  uint32_t byte;
-  const uint32_t word = mx_encode8(x, byte);
-  reinterpret_cast<uint32_t*>(packed)[id] = word;
-  if ((threadIdx.x & 3) == 0) {
-    const int64_t k = c0 / kMxStep;
-    scales[(k * rows + row) * 8 + (c0 % kMxStep) / kMxBlock] = static_cast<uint8_t>(byte);
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    uint32_t byte;
+    const uint32_t word = mx_encode8(x[i], byte);
+    const int64_t row = row0 + i;
+    if (row >= rows) break;
+    *reinterpret_cast<uint32_t*>(packed + row * steps * (kMxStep / 2) + c0 / 2) = word;
+    if ((threadIdx.x & 3) == 0) scales[(c0 / kMxStep * rows + row) * 8 + (c0 % kMxStep) / kMxBlock] = static_cast<uint8_t>(byte);
   }
 }
 
@@ -114,12 +136,18 @@ bool mx_shape_ok(int64_t rows, int64_t cols) {
 hipError_t launch_mx_quantize(const void* W, loftq_dtype_t wdt, int64_t rows, int64_t cols, const float* B,
                               const float* A, int r, uint8_t* packed, uint8_t* scales, hipStream_t s) {
   const int64_t steps = mx_steps(cols);
-  const dim3 grid(blocks_for(rows * steps * (kMxStep / 8)));
-#define LQ_MXQ(T)                                                                                                     \
-  LQ_LAUNCH("mx_quantize", (mx_quantize_kernel<T>), grid, dim3(kMxThreads), 0, s, static_cast<const T*>(W), rows, cols, \
-            steps, B, A, r, packed, scales)
-  if (wdt == LOFTQ_BF16) LQ_MXQ(__bf16);
-  else LQ_MXQ(float);
+  const int64_t groups = B != nullptr ? (rows + 3) / 4 : rows;
+  const dim3 grid(blocks_for(groups * steps * (kMxStep / 8)));
+#define LQ_MXQ(T, ROWS)                                                                                        \
+  LQ_LAUNCH("mx_quantize", (mx_quantize_kernel<T, ROWS>), grid, dim3(kMxThreads), 0, s, static_cast<const T*>(W), \
+            rows, cols, steps, B, A, r, packed, scales)
+  if (wdt == LOFTQ_BF16) {
+    if (B != nullptr) LQ_MXQ(__bf16, 4);
+    else LQ_MXQ(__bf16, 1);
+  } else {
+    if (B != nullptr) LQ_MXQ(float, 4);
+    else LQ_MXQ(float, 1);
+  }
 #undef LQ_MXQ
   return hipGetLastError();
 }

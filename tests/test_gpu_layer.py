@@ -251,6 +251,29 @@ def test_mx_quantize_residual(lib, r):
     assert same.mean() > 0.999
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("rows,cols,r", [(1, 1, 1), (2, 31, 3), (3, 256, 2), (4, 257, 5), (5, 40, 17), (6, 1000, 64),
+                                         (7, 33, 4), (9, 300, 16)])
+def test_mx_quantize_residual_exact(lib, rows, cols, r, dtype):
+    """Small integers make R exact: every byte is the oracle's, with any number of rows, and the padding is zero also
+    where B holds an infinity."""
+    g = np.random.default_rng(rows * 1000 + cols)
+    W = g.integers(-64, 65, (rows, cols)).astype(np.float32)
+    B = g.integers(-3, 4, (rows, r)).astype(np.float32)
+    A = g.integers(-3, 4, (r, cols)).astype(np.float32)
+    for last in (2.0, np.inf):
+        B[rows - 1, r - 1] = last
+        with np.errstate(invalid="ignore"):
+            codes, byte = oracle.mx_quantize((W - B @ A).astype(np.float32))
+        want_packed, want_scales = oracle.mx_pack(codes, byte)
+        packed, scales = lib.loftq_mxfp4_quantize(dev(W, dtype), dev(B), dev(A))
+        assert np.array_equal(scales.cpu().numpy(), want_scales)
+        packed = packed.cpu().numpy()
+        finite = rows if last == 2.0 else rows - 1   # the codes beside a scale of 255 are free
+        assert np.array_equal(packed[:finite], want_packed[:finite])
+        assert not packed[:, (cols + 31) // 32 * 16:].any()
+
+
 # ---- the layer's forward and gradient ----
 
 SHAPES = [  # n, rows, cols, r, base, dq, bits
