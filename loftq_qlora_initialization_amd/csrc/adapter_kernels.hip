@@ -126,8 +126,8 @@ struct Levels {
 
 // One 64 x 128 tile of the base turned round in LDS: thread t decodes rows 2 (t / 8) and the
 // next, columns 16 (t % 8) .. + 15, and keeps the two rows' values of a column in one word
-// (row stride 33 words: a wave's 64 words fall into 64 banks); then it writes half a column's
-// 64 rows, 64 bytes.
+// (row stride 33 words: a wave's 64 words fall into 64 banks); then the 8 lanes of a column
+// write its 64 rows, a line.
 constexpr int kTurnRows = 64, kTurnCols = 128;
 template <typename Src>
 __device__ __forceinline__ void turn_base(const Src& src, const float* lvl, uint32_t (*tile)[33], int64_t tr, int64_t tc,

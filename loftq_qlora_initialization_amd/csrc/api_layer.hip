@@ -207,8 +207,6 @@ loftq_status_t layer_forward(const void* X, i64 n, i64 rows, i64 cols, const Bas
   if (r > 0) {
     LQ_TRY(launch_down(DownJobs{{{Xb, f.Ab, f.partials, cols, f.ks, 0, d}, {}}}, n, rp, s));
     LQ_TRY(launch_down_sum(DownSumJobs{{{f.partials, f.ks, alpha * d.scale, f.S, nullptr, 0}, {}}}, n, r, rp, s));
-  }
-  if (r > 0) {
     t.V = f.Bb;
     t.S = f.S;
     t.adapter_steps = adapter_ld(rp) / 64;

@@ -1,4 +1,4 @@
-// The tiled product of the adapted layer on the matrix cores: C = X W^T + gain keep S V^T
+// The tiled product of the adapted layer on the matrix cores: C = X W^T + keep(S V^T)
 // for operands whose K runs along their rows, in bf16 or in MXFP4.
 //
 // A K step is 128 bytes of a row in either format (64 bf16 or 256 FP4 values) and a lane's
