@@ -12,9 +12,13 @@ The functions carry the C entry points' names (see include/loftq.h):
     loftq_mxfp4_quantize, loftq_mxfp4_dequantize, loftq_mxfp4_forward, loftq_mxfp4_backward
 and return freshly allocated torch tensors on the input's device (or fill the
 caller's ``out`` / ``buffers`` where those are given).
+With ``stream`` a call runs there instead of on the current stream, and so do the
+allocations of what it returns: inputs have to be ready on that stream, and a reader
+on another stream waits for it.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -149,6 +153,30 @@ def _stream(stream=None):
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _on(stream):
+    """Where a call on `stream` allocates: the memory comes from that stream's pool.  A block of the current stream's
+    pool may still be in use there, and one dropped on return would go to the current stream's next tensor while the
+    call's kernels use it."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A new output of a call on `stream`.  The caller may read and drop it on the current stream, so its memory
+    waits for that stream too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with _on(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _scratch(nbytes, device, stream) -> torch.Tensor:
+    """A new workspace of a call on `stream`, dropped when the call returns."""
+    with _on(stream):
+        return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=device)
+
+
 def _wdtype(W: torch.Tensor) -> int:
     if W.dtype == torch.float32:
         return LOFTQ_F32
@@ -202,9 +230,9 @@ def loftq_nf4_quantize(W: torch.Tensor, B: Optional[torch.Tensor] = None, A: Opt
         _contig(B, "B"), _contig(A, "A")
         r = B.shape[1]
     if packed is None:
-        packed = torch.empty((n + 1) // 2, dtype=torch.uint8, device=W.device)
+        packed = _empty((n + 1) // 2, torch.uint8, W.device, stream)
     if absmax is None:
-        absmax = torch.empty((n + 63) // 64, dtype=torch.float32, device=W.device)
+        absmax = _empty((n + 63) // 64, torch.float32, W.device, stream)
     _check("loftq_nf4_quantize", _c_quant(_ptr(W), _wdtype(W), rows, cols, _ptr(B), _ptr(A), r, 64, _ptr(packed),
                                           _ptr(absmax), _stream(stream)))
     return packed, absmax
@@ -213,8 +241,8 @@ def loftq_nf4_quantize(W: torch.Tensor, B: Optional[torch.Tensor] = None, A: Opt
 def loftq_double_quant(absmax: torch.Tensor, stream=None):
     _contig(absmax, "absmax")
     nb = absmax.numel()
-    q = torch.empty(nb, dtype=torch.int8, device=absmax.device)
-    s = torch.empty((nb + 255) // 256, dtype=torch.float32, device=absmax.device)
+    q = _empty(nb, torch.int8, absmax.device, stream)
+    s = _empty((nb + 255) // 256, torch.float32, absmax.device, stream)
     _check("loftq_double_quant", _c_dq(_ptr(absmax), nb, 256, _ptr(q), _ptr(s), _stream(stream)))
     return q, s
 
@@ -224,8 +252,8 @@ def loftq_nf4_dequantize(packed: torch.Tensor, shape, absmax: Optional[torch.Ten
                          W: Optional[torch.Tensor] = None, with_sumsq: bool = False, stream=None):
     """deq(Q), or W - deq(Q) when W is given; optionally also sum of squares (fp64)."""
     rows, cols = shape
-    out = torch.empty((rows, cols), dtype=torch.float32, device=packed.device)
-    ss = torch.empty(1, dtype=torch.float64, device=packed.device) if with_sumsq else None
+    out = _empty((rows, cols), torch.float32, packed.device, stream)
+    ss = _empty(1, torch.float64, packed.device, stream) if with_sumsq else None
     wdt = _wdtype(W) if W is not None else LOFTQ_F32
     _check("loftq_nf4_dequantize",
            _c_deq(_ptr(packed), _ptr(absmax), _ptr(qabsmax), _ptr(dq_scale), rows, cols, 64, 256, _ptr(W), wdt,
@@ -242,11 +270,11 @@ def _merge_call(fn, c_fn, packed, shape, absmax, qabsmax, dq_scale, B, A, alpha,
         r = B.shape[1]
     dev = packed.device
     if out is None:
-        out = {"packed": torch.empty((n + 1) // 2, dtype=torch.uint8, device=dev),
-               "absmax": torch.empty((n + 63) // 64, dtype=torch.float32, device=dev)}
+        out = {"packed": _empty((n + 1) // 2, torch.uint8, dev, stream),
+               "absmax": _empty((n + 63) // 64, torch.float32, dev, stream)}
         if double_quant:
-            out["qabsmax"] = torch.empty((n + 63) // 64, dtype=torch.int8, device=dev)
-            out["dq_scale"] = torch.empty(((n + 63) // 64 + 255) // 256, dtype=torch.float32, device=dev)
+            out["qabsmax"] = _empty((n + 63) // 64, torch.int8, dev, stream)
+            out["dq_scale"] = _empty(((n + 63) // 64 + 255) // 256, torch.float32, dev, stream)
     _check(fn, c_fn(_ptr(packed), _ptr(absmax), _ptr(qabsmax), _ptr(dq_scale), rows, cols, 64, 256, _ptr(B), _ptr(A),
                     r, float(alpha), _ptr(out["packed"]), _ptr(out["absmax"]), _ptr(out.get("qabsmax")),
                     _ptr(out.get("dq_scale")), _stream(stream)))
@@ -292,12 +320,12 @@ def loftq_qlora_forward(X: torch.Tensor, packed: torch.Tensor, shape, absmax: Op
         _contig(B, "B"), _contig(A, "A")
         r = B.shape[1]
     if out is None:
-        out = torch.empty((n_tok, rows), dtype=torch.float32, device=X.device)
+        out = _empty((n_tok, rows), torch.float32, X.device, stream)
     ws_bytes = 0
     if B is not None:
         ws_bytes = qlora_forward_workspace_bytes(n_tok, r)
         if ws is None:
-            ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=X.device)
+            ws = _scratch(ws_bytes, X.device, stream)
         else:
             ws_bytes = ws.numel() * ws.element_size()
     _check("loftq_qlora_forward",
@@ -327,7 +355,7 @@ def loftq_qlora_forward_noalloc(X: torch.Tensor, packed: torch.Tensor, shape, ab
         _contig(B, "B"), _contig(A, "A")
         r = B.shape[1]
     if out is None:
-        out = torch.empty((n_tok, rows), dtype=torch.float32, device=X.device)
+        out = _empty((n_tok, rows), torch.float32, X.device, stream)
     _check("loftq_qlora_forward_noalloc",
            _c_fwd_na(_ptr(X), n_tok, rows, cols, _ptr(packed), _ptr(absmax), _ptr(qabsmax), _ptr(dq_scale),
                      int(bits), _ptr(B), _ptr(A), r, float(alpha), _ptr(out), _stream(stream)))
@@ -421,11 +449,11 @@ def _adapter_args(dev, B, A, rows, cols):
     return _expect(B, "B", dev, torch.float32, (rows, r)), _expect(A, "A", dev, torch.float32, (r, cols)), r
 
 
-def _workspace(ws, query, sizes, like):
+def _workspace(ws, query, sizes, like, stream):
     """(tensor, its address, its bytes); a new one of the size that `query` names where none is given."""
     if ws is None:
-        ws = torch.empty(max(int(query(*sizes)), 16), dtype=torch.uint8, device=like.device)
-    if not ws.is_cuda or not ws.is_contiguous() or ws.get_device() != like.get_device():
+        ws = _scratch(query(*sizes), like.device, stream)
+    elif not ws.is_cuda or not ws.is_contiguous() or ws.get_device() != like.get_device():
         raise ValueError(f"ws must be a contiguous tensor on {like.device}")
     return ws, ws.data_ptr(), ws.numel() * ws.element_size()
 
@@ -435,9 +463,9 @@ def _layer_forward(name, c_fn, query, X, dev, base, rows, cols, B, A, alpha, dro
     out_dtype = _out_dtype(out, out_dtype)
     b, a, r = _adapter_args(dev, B, A, rows, cols)
     if out is None:
-        out = torch.empty((n, rows), dtype=out_dtype, device=X.device)
+        out = _empty((n, rows), out_dtype, X.device, stream)
     y = _expect(out, "out", dev, out_dtype, (n, rows))
-    ws, w, ws_bytes = _workspace(ws, query, (n, rows, cols, r), X)
+    ws, w, ws_bytes = _workspace(ws, query, (n, rows, cols, r), X, stream)
     _call(name, c_fn, dev, stream, X.data_ptr(), n, rows, cols, *base, b, a, r, alpha, drop, y,
           LOFTQ_BF16 if out_dtype is torch.bfloat16 else LOFTQ_F32, w, ws_bytes)
     return out
@@ -450,15 +478,15 @@ def _layer_backward(name, c_fn, query, dY, X, dev, base, rows, cols, B, A, alpha
     if out is not None:
         dX, dB, dA = out
     else:
-        dX = torch.empty((n, cols), dtype=_out_dtype(None, dx_dtype), device=dY.device) if need_dx else None
-        dB, dA = (torch.empty_like(B), torch.empty_like(A)) if r else (None, None)
+        dX = _empty((n, cols), _out_dtype(None, dx_dtype), dY.device, stream) if need_dx else None
+        dB, dA = (_empty(t.shape, t.dtype, dY.device, stream) if r else None for t in (B, A))
     if X is None and dB is not None:
         raise ValueError("X must be given for dB and dA")
     x = None if X is None else _expect(X, "X", dev, torch.bfloat16, (n, cols))
     gx = None if dX is None else _expect(dX, "dX", dev, None, (n, cols))
     gb = None if dB is None else _expect(dB, "dB", dev, torch.float32, (rows, r))
     ga = None if dA is None else _expect(dA, "dA", dev, torch.float32, (r, cols))
-    ws, w, ws_bytes = _workspace(ws, query, (n, rows, cols, r), dY)
+    ws, w, ws_bytes = _workspace(ws, query, (n, rows, cols, r), dY, stream)
     _call(name, c_fn, dev, stream, dY.data_ptr(), x, n, rows, cols, *base, b, a, r, alpha, drop, gx,
           LOFTQ_F32 if dX is not None and dX.dtype is torch.float32 else LOFTQ_BF16, gb, ga, w, ws_bytes)
     return dX, dB, dA
@@ -482,7 +510,7 @@ def loftq_dropout(X: torch.Tensor, p: float, seed: int, offset: int = 0, step: O
         raise TypeError("X must be float32 or bfloat16")
     dtype = LOFTQ_BF16 if X.dtype is torch.bfloat16 else LOFTQ_F32
     if out is None:
-        out = torch.empty_like(X)
+        out = _empty(X.shape, X.dtype, X.device, stream)
     y = _expect(out, "out", dev, X.dtype, X.shape)
     at = None if step is None else _expect(step, "step", dev, torch.int64, (1,))
     drop = LoftqDropout(p, int(seed) & _M64, int(offset) & _M64, at)
@@ -546,9 +574,9 @@ def loftq_mxfp4_quantize(W: torch.Tensor, B: Optional[torch.Tensor] = None, A: O
     steps = (cols + 255) // 256
     b, a, r = _adapter_args(dev, B, A, rows, cols)
     if packed is None:
-        packed = torch.empty((rows, steps * 128), dtype=torch.uint8, device=W.device)
+        packed = _empty((rows, steps * 128), torch.uint8, W.device, stream)
     if scales is None:
-        scales = torch.empty((steps, rows, 8), dtype=torch.uint8, device=W.device)
+        scales = _empty((steps, rows, 8), torch.uint8, W.device, stream)
     _call("loftq_mxfp4_quantize", _c_mx_quant, dev, stream, W.data_ptr(), dtype, rows, cols, b, a, r,
           *_mx_args(dev, packed, scales, rows, cols))
     return packed, scales
@@ -563,7 +591,7 @@ def loftq_mxfp4_dequantize(packed: torch.Tensor, scales: torch.Tensor, shape, W:
     w = None if W is None else _expect(W, "W", dev, None, (rows, cols))
     out_dtype = _out_dtype(out, out_dtype)
     if out is None:
-        out = torch.empty((rows, cols), dtype=out_dtype, device=packed.device)
+        out = _empty((rows, cols), out_dtype, packed.device, stream)
     _call("loftq_mxfp4_dequantize", _c_mx_deq, dev, stream, *base, rows, cols, w,
           LOFTQ_BF16 if W is not None and W.dtype is torch.bfloat16 else LOFTQ_F32,
           _expect(out, "out", dev, out_dtype, (rows, cols)),
@@ -608,10 +636,10 @@ def loftq_lowrank_svd(E: torch.Tensor, r: int, oversample: int = 8, power_iters:
     _contig(E, "E")
     rows, cols = E.shape
     ws_bytes = lowrank_workspace_bytes(rows, cols, r, oversample, exact)
-    ws = torch.empty(max(ws_bytes, 16), dtype=torch.uint8, device=E.device)
-    B = torch.empty((rows, r), dtype=torch.float32, device=E.device)
-    A = torch.empty((r, cols), dtype=torch.float32, device=E.device)
-    sigma = torch.empty(r, dtype=torch.float32, device=E.device)
+    ws = _scratch(ws_bytes, E.device, stream)
+    B = _empty((rows, r), torch.float32, E.device, stream)
+    A = _empty((r, cols), torch.float32, E.device, stream)
+    sigma = _empty(r, torch.float32, E.device, stream)
     _check("loftq_lowrank_svd",
            _c_svd(_ptr(E), rows, cols, r, oversample, power_iters, int(bool(exact)), _ptr(omega), seed, t, _ptr(B),
                   _ptr(A), _ptr(sigma), _ptr(ws), ws_bytes, _stream(stream)))
@@ -623,22 +651,23 @@ def workspace_bytes(rows: int, cols: int, cfg: LoftqConfig) -> int:
 
 
 class InitBuffers:
-    """Caller-owned outputs and workspace for repeated loftq_init calls on one shape."""
+    """Caller-owned outputs and workspace for repeated loftq_init calls on one shape, on `stream` where the calls
+    run on another than the current one."""
 
-    def __init__(self, rows: int, cols: int, cfg: LoftqConfig, device="cuda", workspace: bool = True):
+    def __init__(self, rows: int, cols: int, cfg: LoftqConfig, device="cuda", workspace: bool = True, stream=None):
         n = rows * cols
         nb = (n + 63) // 64
         self.cfg = cfg
-        self.packed = torch.empty((n + 1) // 2, dtype=torch.uint8, device=device)
-        self.absmax = torch.empty(nb, dtype=torch.float32, device=device)
-        self.qabsmax = torch.empty(max(nb, 1), dtype=torch.int8, device=device)
-        self.dq_scale = torch.empty(max((nb + 255) // 256, 1), dtype=torch.float32, device=device)
-        self.B = torch.empty((rows, cfg.rank), dtype=torch.float32, device=device)
-        self.A = torch.empty((cfg.rank, cols), dtype=torch.float32, device=device)
-        self.sigma = torch.empty(cfg.rank, dtype=torch.float32, device=device)
-        self.objective = torch.empty(cfg.iterative_steps + 1, dtype=torch.float64, device=device)
+        self.packed = _empty((n + 1) // 2, torch.uint8, device, stream)
+        self.absmax = _empty(nb, torch.float32, device, stream)
+        self.qabsmax = _empty(max(nb, 1), torch.int8, device, stream)
+        self.dq_scale = _empty(max((nb + 255) // 256, 1), torch.float32, device, stream)
+        self.B = _empty((rows, cfg.rank), torch.float32, device, stream)
+        self.A = _empty((cfg.rank, cols), torch.float32, device, stream)
+        self.sigma = _empty(cfg.rank, torch.float32, device, stream)
+        self.objective = _empty(cfg.iterative_steps + 1, torch.float64, device, stream)
         self.ws_bytes = workspace_bytes(rows, cols, cfg) if workspace else 0
-        self.ws = torch.empty(max(self.ws_bytes, 16), dtype=torch.uint8, device=device) if workspace else None
+        self.ws = _scratch(self.ws_bytes, device, stream) if workspace else None
 
     def matrix(self, W: torch.Tensor) -> LoftqMatrix:
         """This buffer set as one loftq_matrix_t of a batch, for weight W."""
@@ -656,7 +685,7 @@ def loftq_init(W: torch.Tensor, cfg: Optional[LoftqConfig] = None, buffers: Opti
     if cfg is None:
         cfg = default_config(**overrides)
     rows, cols = W.shape
-    bufs = buffers if buffers is not None else InitBuffers(rows, cols, cfg, W.device)
+    bufs = buffers if buffers is not None else InitBuffers(rows, cols, cfg, W.device, stream=stream)
     _check("loftq_init",
            _c_init(_ptr(W), _wdtype(W), rows, cols, ctypes.byref(cfg), _ptr(bufs.packed), _ptr(bufs.absmax),
                    _ptr(bufs.qabsmax), _ptr(bufs.dq_scale), _ptr(bufs.B), _ptr(bufs.A), _ptr(bufs.objective),
