@@ -541,7 +541,9 @@ bool qlora_forward_shape_ok(int64_t n_tok, int64_t rows, int64_t cols, int r) {
   return p.grid_down * 1024 < limit && p.grid_gemm * p.block_gemm < limit;
 }
 
-int lora_down_splits(int64_t n_tok, int64_t cols, int r) { return plan_forward(n_tok, 16, cols, r).ks; }
+int lora_down_splits(int64_t n_tok, int64_t cols, int r) {
+  return n_tok > 0 ? plan_forward(n_tok, 16, cols, r).ks : 1;   // a plan divides the tokens' tiles
+}
 
 hipError_t launch_lora_down(const void* X, int64_t n_tok, int64_t cols, const float* A, int r, float* Tws,
                             hipStream_t s) {
