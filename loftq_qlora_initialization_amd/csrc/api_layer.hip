@@ -119,6 +119,11 @@ DropArg drop_arg(const loftq_dropout_t* d) {
   return DropArg{d->seed, d->offset, d->step, thr, scale};
 }
 
+// Both factors or none; one of no elements may have no address.
+bool factors_ok(const float* B, const float* A, i64 rows, i64 cols) {
+  return rows == 0 || cols == 0 || (B == nullptr) == (A == nullptr);
+}
+
 bool dtype_ok(loftq_dtype_t t) { return t == LOFTQ_F32 || t == LOFTQ_BF16; }
 
 // What the training calls share: sizes, the base, the adapter, the dropout.
@@ -130,7 +135,7 @@ loftq_status_t check_layer(i64 n, i64 rows, i64 cols, const Base4& b, bool mx, c
     if (!nf_tables(b.bits).valid) return LOFTQ_ERR_UNSUPPORTED;
     if ((b.qabsmax == nullptr) != (b.dq_scale == nullptr)) return LOFTQ_ERR_INVALID_ARG;
   }
-  if ((B == nullptr) != (A == nullptr)) return LOFTQ_ERR_INVALID_ARG;
+  if (!factors_ok(B, A, rows, cols)) return LOFTQ_ERR_INVALID_ARG;
   if (B != nullptr && r < 1) return LOFTQ_ERR_INVALID_ARG;
   if (!std::isfinite(alpha) || !drop_ok(drop) || !std::isfinite(alpha * drop_arg(drop).scale)) return LOFTQ_ERR_INVALID_ARG;
   return LOFTQ_OK;
@@ -224,7 +229,7 @@ loftq_status_t layer_backward(const void* dY, const void* X, i64 n, i64 rows, i6
   if (st != LOFTQ_OK) return st;
   if (dX && !dtype_ok(xdt)) return LOFTQ_ERR_INVALID_ARG;
   if ((dB == nullptr) != (dA == nullptr) || (dB && !B)) return LOFTQ_ERR_INVALID_ARG;
-  if (!dX && !dB) return LOFTQ_ERR_INVALID_ARG;
+  if (!dX && !dB && n > 0) return LOFTQ_ERR_INVALID_ARG;   // without tokens dX has no elements and may have no address
   if (rows == 0 || rows >= i64(1) << 22) return LOFTQ_ERR_UNSUPPORTED;   // rows are the product's K
   st = check_layer_buffers(n, rows, cols, base, mx, B, A, r);
   if (st != LOFTQ_OK) return st;
@@ -334,7 +339,7 @@ size_t loftq_mxfp4_scale_bytes(int64_t rows, int64_t cols) {
 loftq_status_t loftq_mxfp4_quantize(const void* W, loftq_dtype_t wdt, int64_t rows, int64_t cols, const float* B,
                                     const float* A, int32_t r, uint8_t* packed, uint8_t* scales, void* stream) {
   if (!shape_ok(rows, cols) || !dtype_ok(wdt)) return LOFTQ_ERR_INVALID_ARG;
-  if ((B == nullptr) != (A == nullptr)) return LOFTQ_ERR_INVALID_ARG;
+  if (!factors_ok(B, A, rows, cols)) return LOFTQ_ERR_INVALID_ARG;
   if (B != nullptr && (r < 1 || r > 4096)) return LOFTQ_ERR_INVALID_ARG;
   if (rows == 0 || cols == 0) return LOFTQ_OK;
   if (!mx_shape_ok(rows, cols)) return LOFTQ_ERR_UNSUPPORTED;

@@ -16,6 +16,50 @@ def test_workspace_of_no_tokens(query):
     assert len(run.stdout.split(",")) == 9
 
 
+@pytest.mark.parametrize("mx", [False, True])
+def test_tensors_without_elements_have_no_address(mx):
+    """torch's empty tensors have the address 0, which otherwise says that an argument is not given."""
+    from loftq_qlora_initialization_amd import binding as b
+    at, OK, INVALID = 0x10000, 0, 1   # aligned, never dereferenced
+    base = (at, at) if mx else (at, at, None, None, 4)
+    fwd, bwd = (b._c_mx_fwd, b._c_mx_bwd) if mx else (b._c_fwd_drop, b._c_bwd)
+    # the gradient of no tokens to X alone, with an adapter and without
+    assert bwd(None, None, 0, 64, 128, *base, at, at, 8, 1.0, None, None, 1, None, None, at, 1 << 30, None) == OK
+    assert bwd(None, None, 0, 64, 128, *base, None, None, 0, 1.0, None, None, 1, None, None, at, 1 << 30, None) == OK
+    assert bwd(at, at, 1, 64, 128, *base, at, at, 8, 1.0, None, None, 1, None, None, at, 1 << 30, None) == INVALID
+    # a layer of no rows: B has no elements
+    assert fwd(at, 4, 0, 128, *base, None, at, 8, 1.0, None, None, 0, at, 1 << 30, None) == OK
+    assert fwd(at, 4, 64, 128, *base, None, at, 8, 1.0, None, at, 0, at, 1 << 30, None) == INVALID
+    # a residual of no rows or no columns
+    assert b._c_mx_quant(None, 0, 0, 64, None, at, 8, None, None, None) == OK
+    assert b._c_mx_quant(None, 0, 64, 0, at, None, 8, None, None, None) == OK
+    assert b._c_mx_quant(at, 0, 64, 64, at, None, 8, at, at, None) == INVALID
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("mx", [False, True])
+def test_empty_tensors(lib, mx):
+    def zeros(*shape, dtype=torch.float32):
+        return torch.zeros(*shape, dtype=dtype, device="cuda")
+
+    B, A, W = zeros(64, 8), zeros(8, 128), torch.randn(64, 128, device="cuda")
+    if mx:
+        base, fwd, bwd = dict(zip(("packed", "scales"), lib.loftq_mxfp4_quantize(W))), lib.loftq_mxfp4_forward, lib.loftq_mxfp4_backward
+        none = dict(zip(("packed", "scales"), lib.loftq_mxfp4_quantize(W[:0], B[:0], A)))
+        assert lib.loftq_mxfp4_quantize(zeros(64, 0), B, zeros(8, 0))[0].shape == (64, 0)
+    else:
+        base, fwd, bwd = dict(zip(("packed", "absmax"), lib.loftq_nf4_quantize(W))), lib.loftq_qlora_forward_dropout, lib.loftq_qlora_backward
+        none = {k: v[:0] for k, v in base.items()}
+    G, X = zeros(0, 64, dtype=torch.bfloat16), zeros(0, 128, dtype=torch.bfloat16)
+    dX, dB, dA = bwd(G, None, shape=(64, 128), **base)
+    assert dX.shape == (0, 128) and dB is None and dA is None
+    out = zeros(0, 128, dtype=torch.bfloat16)
+    assert bwd(G, X, shape=(64, 128), B=B, A=A, out=(out, None, None), **base)[0] is out
+    dX, dB, dA = bwd(G, X, shape=(64, 128), B=B, A=A, out=(out, torch.ones_like(B), torch.ones_like(A)), **base)
+    assert not dB.any() and not dA.any()
+    assert fwd(zeros(4, 128, dtype=torch.bfloat16), shape=(0, 128), B=B[:0], A=A, **none).shape == (4, 0)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("r", [0, 8])
 def test_serving_no_tokens(lib, r):
