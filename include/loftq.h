@@ -211,7 +211,10 @@ size_t loftq_qlora_forward_noalloc_max_bytes(void);
  * 4-bit model into the adapter), and MXFP4, the 4-bit format that the matrix cores
  * multiply without decoding.  The conventions above hold, but for one: an infinity or a
  * NaN in X or dY reaches the outputs that it takes part in, and none that it does not;
- * what the dropout drops takes part in nothing. */
+ * what the dropout drops takes part in nothing.
+ *
+ * A workspace query grows with n_tok and with r: the bytes for the most tokens and the
+ * largest rank of a layer serve every call over it. */
 
 /* A dropout mask is a function of (p, seed, offset, element index) and is never stored:
  * a backward call with the same values uses its forward's mask.  thr = round(2^16 p)

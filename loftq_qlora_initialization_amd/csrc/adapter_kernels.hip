@@ -595,6 +595,16 @@ int down_splits(int64_t n, int64_t K) {
   return static_cast<int>(ks < 1 ? 1 : (ks > 32 ? 32 : ks));
 }
 
+// Fewer tokens may be divided into more ranges: k ranges are taken up to 1024 / k groups.
+int64_t down_rows_bound(int64_t n, int64_t K) {
+  int64_t most = n;
+  for (int64_t k = down_splits(0, K); k > 1; --k) {
+    const int64_t tokens = 1024 / k * 32, rows = k * (tokens < n ? tokens : n);
+    if (rows > most) most = rows;
+  }
+  return most;
+}
+
 hipError_t launch_down(DownJobs jobs, int64_t n, int rp, hipStream_t s) {
   for (DownJob& j : jobs.job) j.wgs = j.X != nullptr ? static_cast<unsigned>((n + 31) / 32 * j.ks) : 0;
   const dim3 grid(jobs.job[0].wgs + jobs.job[1].wgs);

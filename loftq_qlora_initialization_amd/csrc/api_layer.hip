@@ -25,6 +25,8 @@ struct Arena {
 int rank_pad(int r) { return (r + 15) / 16 * 16; }
 i64 pad_to(i64 n, i64 m) { return (n + m - 1) / m * m; }
 
+// The pieces of a call's workspace.  Each is as large as any call of up to n tokens and of
+// rank up to r needs it, so that the workspace of a long prompt serves a shorter one.
 struct ForwardSpace {
   __bf16* W;        // NormalFloat base: bf16(deq)
   uint8_t* xq;      // MXFP4 base: the activations' codes and scales
@@ -40,7 +42,10 @@ struct ForwardSpace {
 ForwardSpace forward_space(void* ws, i64 n, i64 rows, i64 cols, int r, bool mx) {
   Arena a{static_cast<char*>(ws)};
   ForwardSpace f{};
-  if (mx && r > 0 && token_product_pays(n, rows, cols)) f.T = a.take<float>(lora_down_splits(n, cols, r) * n * r);
+  if (mx && r > 0) {
+    const i64 few = n < token_product_most(rows, cols) ? n : token_product_most(rows, cols);
+    f.T = a.take<float>(lora_down_splits(few, cols, r) * few * r);   // one number of ranges up to 16 tokens
+  }
   if (mx) {
     f.xq = a.take<uint8_t>(n * mx_steps(cols) * (kMxStep / 2));
     f.xs = a.take<uint8_t>(n * mx_steps(cols) * 8);
@@ -53,10 +58,10 @@ ForwardSpace forward_space(void* ws, i64 n, i64 rows, i64 cols, int r, bool mx) 
     f.Ab = a.take<__bf16>(rp * cols);
     f.Bb = a.take<__bf16>(rows * adapter_ld(rp));
     f.S = a.take<__bf16>(n * adapter_ld(rp));
-    f.partials = a.take<float>(static_cast<i64>(f.ks) * n * rp);
+    f.partials = a.take<float>(down_rows_bound(n, cols) * rp);
   }
   const int steps = static_cast<int>(mx ? mx_steps(cols) : cols / 64);
-  f.joins = a.take<float>(plan_tile_product(n, rows, steps, r > 0 ? adapter_ld(rank_pad(r)) / 64 : 0, mx).partial_bytes / 4);
+  f.joins = a.take<float>(tile_product_partial_bound(n, rows, steps) / 4);
   f.bytes = a.used;
   return f;
 }
@@ -86,13 +91,12 @@ BackwardSpace backward_space(void* ws, i64 n, i64 rows, i64 cols, int r) {
     f.Ht = a.take<__bf16>(3 * rp * n_pad);
     f.Pt = a.take<__bf16>(3 * rp * n_pad);
     f.Ps = a.take<__bf16>(n * adapter_ld(rp));
-    f.down_p = a.take<float>(f.ks_p * n * rp);
-    f.down_h = a.take<float>(f.ks_h * n * rp);
+    f.down_p = a.take<float>(down_rows_bound(n, rows_pad) * rp);
+    f.down_h = a.take<float>(down_rows_bound(n, cols) * rp);
     f.grad_b = a.take<float>(f.ts > 1 ? f.ts * rows_pad * rp : 0);
     f.grad_a = a.take<float>(f.ts > 1 ? f.ts * cols * rp : 0);
   }
-  f.joins = a.take<float>(plan_tile_product(n, cols, static_cast<int>(rows_pad / 64), r > 0 ? adapter_ld(rp) / 64 : 0,
-                                            false).partial_bytes / 4);
+  f.joins = a.take<float>(tile_product_partial_bound(n, cols, static_cast<int>(rows_pad / 64)) / 4);
   f.bytes = a.used;
   return f;
 }
@@ -178,7 +182,7 @@ loftq_status_t layer_forward(const void* X, i64 n, i64 rows, i64 cols, const Bas
   if (ws_bytes < f.bytes) return LOFTQ_ERR_WORKSPACE;
   const __bf16* Xb = static_cast<const __bf16*>(X);
   const DropArg d = drop_arg(drop);
-  if (mx && (r == 0 || d.thr == 0) && token_product_pays(n, rows, cols)) {   // dropout is the tiled path's
+  if (mx && (r == 0 || d.thr == 0) && n <= token_product_most(rows, cols)) {   // dropout is the tiled path's
     if (r > 0) LQ_TRY(launch_lora_down(Xb, n, cols, A, r, f.T, s));
     return from_hip(launch_token_product(TokenProduct{Xb, base.packed, base.mx, f.T, B, n, rows, cols,
                                                       r > 0 ? lora_down_splits(n, cols, r) : 0, r, alpha, Y, ydt}, s));

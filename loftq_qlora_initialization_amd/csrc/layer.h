@@ -37,18 +37,19 @@ struct TileProduct {
   int splits;                 // K ranges, set by the launcher
 };
 
-// How a product is divided: a tile shape, K ranges, and the bytes of their partial outputs.
+// How a product is divided: a tile shape and K ranges.
 struct TilePlan {
   int shape, splits;
-  size_t partial_bytes;
 };
 TilePlan plan_tile_product(int64_t M, int64_t N, int steps, int adapter_steps, bool mx);
+// at least the bytes of the K ranges' partial outputs in every plan for up to M tokens, with an adapter or without
+size_t tile_product_partial_bound(int64_t M, int64_t N, int steps);
 hipError_t launch_tile_product(TileProduct t, bool mx, float* partials, hipStream_t s);
 bool tile_product_shape_ok(int64_t M, int64_t N, int64_t K);
 
-// The MXFP4 product for M <= 16 tokens, from X itself (token_product.hip), and whether it is
-// faster than the tiled one.
-bool token_product_pays(int64_t M, int64_t N, int64_t K);
+// The MXFP4 product for M <= 16 tokens, from X itself (token_product.hip), and up to how many
+// tokens it is faster than the tiled one.
+int64_t token_product_most(int64_t N, int64_t K);
 struct TokenProduct {
   const __bf16* X;            // M x K, K % 32 == 0
   const uint8_t* W;
@@ -119,6 +120,7 @@ struct DownSumJobs {
   DownSumJob job[2];
 };
 int down_splits(int64_t n, int64_t K);
+int64_t down_rows_bound(int64_t n, int64_t K);   // at least down_splits(m, K) m for every m <= n
 hipError_t launch_down(DownJobs jobs, int64_t n, int rp, hipStream_t s);
 hipError_t launch_down_sum(DownSumJobs jobs, int64_t n, int r, int rp, hipStream_t s);
 

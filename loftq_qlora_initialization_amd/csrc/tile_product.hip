@@ -418,7 +418,7 @@ constexpr TileShape kShapes[] = {
 // The shape and the number of K ranges with the least estimated time: rounds of
 // workgroups over the CUs, and for more than one range the pass that joins them.
 TilePlan plan_tile_product(int64_t M, int64_t N, int steps, int adapter_steps, bool mx) {
-  TilePlan best{0, 1, 0};
+  TilePlan best{0, 1};
   float least = 0.f;
   if (steps < 1) return best;
   for (int i = 0; i < 4; ++i) {
@@ -433,11 +433,27 @@ TilePlan plan_tile_product(int64_t M, int64_t N, int steps, int adapter_steps, b
       if (splits > 1) us += 4.f + static_cast<float>(M * N) * 4.f * (splits + 1) / 4e6f;
       if ((i == 0 && want == 1) || us < least) {
         least = us;
-        best = TilePlan{i, splits, splits > 1 ? static_cast<size_t>(splits * M * N) * 4 : 0};
+        best = TilePlan{i, splits};
       }
     }
   }
   return best;
+}
+
+// Fewer tokens may be divided into more K ranges, so the partials do not grow with M: for each
+// shape and number of ranges, the most tokens that it can be chosen for.
+size_t tile_product_partial_bound(int64_t M, int64_t N, int steps) {
+  size_t most = 0;
+  if (steps < 1 || N < 1) return most;
+  for (const TileShape& c : kShapes)
+    for (int want = 2; want <= kMostSplits; ++want) {
+      const int per = (steps + want - 1) / want;
+      if ((steps + per - 1) / per != want) continue;
+      const int64_t tokens = kCUs * c.per_cu / (want * ((N + c.tn - 1) / c.tn)) * c.tm;
+      const size_t bytes = static_cast<size_t>(want * (tokens < M ? tokens : M) * N) * 4;
+      if (bytes > most) most = bytes;
+    }
+  return most;
 }
 
 bool tile_product_shape_ok(int64_t M, int64_t N, int64_t K) {

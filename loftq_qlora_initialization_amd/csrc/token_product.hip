@@ -145,9 +145,7 @@ __global__ __launch_bounds__(kWaves * 64) void token_product_kernel(TokenProduct
 
 }  // namespace
 
-bool token_product_pays(int64_t M, int64_t N, int64_t K) {
-  return M <= 8 || (M <= 16 && N * K <= (int64_t(1) << 25));
-}
+int64_t token_product_most(int64_t N, int64_t K) { return N * K <= (int64_t(1) << 25) ? 16 : 8; }
 
 hipError_t launch_token_product(const TokenProduct& t, hipStream_t s) {
   // as many features a workgroup as leave each CU one
