@@ -210,8 +210,10 @@ size_t loftq_qlora_forward_noalloc_max_bytes(void);
  * frozen 4-bit base ("QLoRA论文概述": gradients are back-propagated through the frozen
  * 4-bit model into the adapter), and MXFP4, the 4-bit format that the matrix cores
  * multiply without decoding.  The conventions above hold, but for one: an infinity or a
- * NaN in X or dY reaches the outputs that it takes part in, and none that it does not;
- * what the dropout drops takes part in nothing.
+ * NaN in X or dY makes those outputs infinite or NaN whose formula it enters, and no
+ * others.  keep() puts a zero in the place of what it drops, whatever that holds; where
+ * that zero is a factor of a sum it is one like any other, so that an infinite or NaN
+ * row of dY B makes all of dA infinite or NaN.
  *
  * A workspace query grows with n_tok and with r: the bytes for the most tokens and the
  * largest rank of a layer serve every call over it. */
