@@ -386,14 +386,21 @@ __global__ __launch_bounds__(256) void join_kernel(const float* __restrict__ par
   }
 }
 
+// The name under which launch timing files a product: its format and its tile.
+template <bool kMx, int TM>
+constexpr const char* product_name() {
+  if constexpr (kMx) return TM == 256 ? "mx_product_256x256" : TM == 192 ? "mx_product_192x256" : TM == 128 ? "mx_product_128x256" : "mx_product_64x128";
+  else return TM == 256 ? "bf16_product_256x256" : TM == 192 ? "bf16_product_192x256" : TM == 128 ? "bf16_product_128x256" : "bf16_product_64x128";
+}
+
 template <bool kMx, int TM, int TN, int WM, int WN, int D, int R>
 hipError_t launch_tile(const TileProduct& t, hipStream_t s) {
   const int64_t wgs = ((t.M + TM - 1) / TM) * ((t.N + TN - 1) / TN) * t.splits;
   const dim3 grid(static_cast<unsigned>(wgs)), block((TM / WM) * (TN / WN) * 64);
   if (t.odt == LOFTQ_BF16)
-    LQ_LAUNCH(kMx ? "mx_product" : "bf16_product", (tile_product_kernel<kMx, TM, TN, WM, WN, D, R, __bf16>), grid, block, 0, s, t);
+    LQ_LAUNCH((product_name<kMx, TM>()), (tile_product_kernel<kMx, TM, TN, WM, WN, D, R, __bf16>), grid, block, 0, s, t);
   else
-    LQ_LAUNCH(kMx ? "mx_product" : "bf16_product", (tile_product_kernel<kMx, TM, TN, WM, WN, D, R, float>), grid, block, 0, s, t);
+    LQ_LAUNCH((product_name<kMx, TM>()), (tile_product_kernel<kMx, TM, TN, WM, WN, D, R, float>), grid, block, 0, s, t);
   return hipGetLastError();
 }
 
