@@ -17,11 +17,11 @@ __device__ __forceinline__ T drop_one(T x, bool keep, float scale) {
   return keep ? static_cast<T>(static_cast<float>(x) * scale) : static_cast<T>(0.f);
 }
 
-// One thread per 16 bytes (8 bf16 or 4 fp32 elements); the last thread takes the
-// elements past the last whole 16 bytes one by one.
+// One thread per 16 bytes (8 bf16 or 4 fp32 elements); the first thread takes the
+// elements past the last whole 16 bytes one by one.  Y may be X: each element is read and
+// written by one thread, in that order.
 template <typename T>
-__global__ __launch_bounds__(kDropThreads) void dropout_kernel(const T* __restrict__ X, int64_t n, DropArg d,
-                                                               T* __restrict__ Y) {
+__global__ __launch_bounds__(kDropThreads) void dropout_kernel(const T* X, int64_t n, DropArg d, T* Y) {
   constexpr int E = 16 / sizeof(T);
   typedef T vec __attribute__((ext_vector_type(E)));
   const uint64_t key = drop_key(d);

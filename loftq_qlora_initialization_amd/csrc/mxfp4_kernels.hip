@@ -91,12 +91,13 @@ __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __rest
   }
 }
 
-// out = deq or W - deq, in fp32 or bf16; one thread per 8 columns.
+// out = deq or W - deq, in fp32 or bf16; one thread per 8 columns.  out may be W: each element is
+// read and written by one thread, in that order.
 template <typename T, typename O, bool kHasW>
 __global__ __launch_bounds__(kMxThreads) void mx_dequantize_kernel(const uint8_t* __restrict__ packed,
                                                                    const uint8_t* __restrict__ scales, int64_t rows,
                                                                    int64_t cols, int64_t steps,
-                                                                   const T* __restrict__ W, O* __restrict__ out) {
+                                                                   const T* W, O* out) {
   const uint32_t id = blockIdx.x * kMxThreads + threadIdx.x;   // below 2^32
   const uint32_t per_row = static_cast<uint32_t>((cols + 7) / 8);
   const int64_t row = id / per_row, c0 = static_cast<int64_t>(id % per_row) * 8;
