@@ -43,7 +43,7 @@ ForwardSpace forward_space(void* ws, i64 n, i64 rows, i64 cols, int r, bool mx) 
   Arena a{static_cast<char*>(ws)};
   ForwardSpace f{};
   if (mx && r > 0) {
-    const i64 few = n < token_product_most(rows, cols) ? n : token_product_most(rows, cols);
+    const i64 few = n < kFewTokens ? n : kFewTokens;
     f.T = a.take<float>(lora_down_splits(few, cols, r) * few * r);   // one number of ranges up to 16 tokens
   }
   if (mx) {
@@ -182,7 +182,7 @@ loftq_status_t layer_forward(const void* X, i64 n, i64 rows, i64 cols, const Bas
   if (ws_bytes < f.bytes) return LOFTQ_ERR_WORKSPACE;
   const __bf16* Xb = static_cast<const __bf16*>(X);
   const DropArg d = drop_arg(drop);
-  if (mx && (r == 0 || d.thr == 0) && n <= token_product_most(rows, cols)) {   // dropout is the tiled path's
+  if (mx && (r == 0 || d.thr == 0) && token_product_pays(n, rows, cols, r)) {   // dropout is the tiled path's
     if (r > 0) LQ_TRY(launch_lora_down(Xb, n, cols, A, r, f.T, s));
     return from_hip(launch_token_product(TokenProduct{Xb, base.packed, base.mx, f.T, B, n, rows, cols,
                                                       r > 0 ? lora_down_splits(n, cols, r) : 0, r, alpha, Y, ydt}, s));

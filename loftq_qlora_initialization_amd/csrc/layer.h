@@ -47,9 +47,10 @@ size_t tile_product_partial_bound(int64_t M, int64_t N, int steps);
 hipError_t launch_tile_product(TileProduct t, bool mx, float* partials, hipStream_t s);
 bool tile_product_shape_ok(int64_t M, int64_t N, int64_t K);
 
-// The MXFP4 product for M <= 16 tokens, from X itself (token_product.hip), and up to how many
-// tokens it is faster than the tiled one.
-int64_t token_product_most(int64_t N, int64_t K);
+// The MXFP4 product for M <= kFewTokens tokens, from X itself (token_product.hip), and whether it
+// is faster than the tiled one.
+constexpr int64_t kFewTokens = 16;
+bool token_product_pays(int64_t M, int64_t N, int64_t K, int r);
 struct TokenProduct {
   const __bf16* X;            // M x K, K % 32 == 0
   const uint8_t* W;

@@ -12,10 +12,6 @@
 // workgroup, and reads four times a feature tile's bytes for it: NF tiles share it where the
 // features suffice.  The partial sums meet in LDS in wave order, then the adapter's term is
 // added in fp32.
-//
-// Measured with its adapter's launch, in a graph, one token: 4096 x 4096 9.2 us (the tiled
-// product and its launches 21.3), 11008 x 4096 16.4 us (20.2), 28672 x 8192 34.7 us (34.8);
-// 16 tokens 12.5 us (22.4), 23.1 us (21.6), 50 us (36).
 #include "layer.h"
 
 namespace loftq {
@@ -143,13 +139,35 @@ __global__ __launch_bounds__(kWaves * 64) void token_product_kernel(TokenProduct
   }
 }
 
+// Feature tiles a workgroup: as many as leave each CU one.
+int feature_tiles(int64_t N) { return N >= 16384 ? 4 : (N >= 8192 ? 2 : 1); }
+
 }  // namespace
 
-int64_t token_product_most(int64_t N, int64_t K) { return N * K <= (int64_t(1) << 25) ? 16 : 8; }
+// Both sides with their launches, in a graph, weights read from memory (us, this against tiled):
+//                  r = 16, 1 token   8 tokens         r = 64, 1 token   8 tokens
+//   4096 x  4096   9.8  against 21.5 11.7        22.3 13.7        26.0  16.9        27.4
+//  11008 x  4096   18.9         23.9 22.0        24.6 24.4        29.0  32.5        29.8
+//   8192 x  8192   19.0         27.8 20.2        27.9 25.5        31.8  30.1        32.9
+//  22016 x  4096   25.2         28.6 29.0        28.9 33.8        36.3  49.8        37.2
+//  16384 x  8192   27.4         34.5 29.6        34.0 36.2        40.2  42.7        41.3
+//  11008 x 11008   35.0         33.0 40.8        33.7 46.4        39.2  56.7        40.3
+//  28672 x  8192   45.1         44.5 51.2        44.7 55.6        55.1  71.8        56.8
+//     64 x 11008   15.8         20.1 19.2        20.0 25.3        23.2  30.0        24.3
+//   1024 x 16384   20.5         21.3 23.8        23.1 32.2        26.3  36.4        28.1
+//    128 x 65536   64.9         31.7 77.1        32.6 107         41.5  121         43.9
+// Up to 2^25 weights one round of workgroups takes them all, and what counts is the length of K
+// that a workgroup goes through, with the adapter's and the tokens' share of a step; past them
+// the weight with its features in whole rounds, and for the adapter's end M r.
+bool token_product_pays(int64_t M, int64_t N, int64_t K, int r) {
+  if (M > kFewTokens) return false;
+  if (N * K <= (int64_t(1) << 25)) return K * (72 + 2 * r + 5 * M) <= (int64_t(1) << 21);
+  const int64_t round = 256 * 16 * feature_tiles(N), size = (N + round - 1) / round * round * K;
+  return M <= 8 && size <= (int64_t(1) << 27) && M * r * size <= (int64_t(1) << 34);
+}
 
 hipError_t launch_token_product(const TokenProduct& t, hipStream_t s) {
-  // as many features a workgroup as leave each CU one
-  const int nf = t.N >= 16384 ? 4 : (t.N >= 8192 ? 2 : 1);
+  const int nf = feature_tiles(t.N);
   const dim3 grid(static_cast<unsigned>((t.N + 16 * nf - 1) / (16 * nf))), block(kWaves * 64);
 #define LQ_TOKEN(NF, O) LQ_LAUNCH("mx_token_product", (token_product_kernel<NF, O>), grid, block, 0, s, t)
 #define LQ_TOKEN_O(O)                \

@@ -84,3 +84,19 @@ def test_few_tokens_with_two_and_four_feature_tiles(lib, ran, rows, n, r, dtype)
     Y, names = ran(lambda: layer.forward(lib, out_dtype=dtype))
     assert "mx_token_product" in names
     layer.check_forward(Y)
+
+
+@pytest.mark.parametrize("rows,cols,r,n,few", [
+    (4096, 4096, 64, 16, True), (8192, 4096, 64, 16, True), (4096, 4096, 16, 17, False), (11008, 4096, 16, 8, True),
+    (11008, 4096, 16, 9, False), (11008, 4096, 64, 8, False), (16384, 8192, 16, 8, True), (16384, 8192, 64, 2, True),
+    (22016, 4096, 64, 8, False), (11008, 11008, 0, 1, False), (11008, 11008, 64, 8, False), (28672, 8192, 16, 2, False),
+    (1024, 11008, 16, 8, True), (64, 11008, 64, 1, False), (1024, 16384, 64, 8, False), (128, 65536, 0, 1, False)])
+def test_which_product_takes_few_tokens(lib, ran, rows, cols, r, n, few):
+    """The faster of the two, as measured at these sizes."""
+    steps = -(-cols // 256)
+    base = dict(packed=torch.zeros(rows, steps * 128, dtype=torch.uint8, device="cuda"),
+                scales=torch.zeros(steps, rows, 8, dtype=torch.uint8, device="cuda"))
+    ad = dict(B=torch.zeros(rows, r, device="cuda"), A=torch.zeros(r, cols, device="cuda")) if r else {}
+    X = torch.ones(n, cols, dtype=torch.bfloat16, device="cuda")
+    Y, names = ran(lambda: lib.loftq_mxfp4_forward(X, shape=(rows, cols), **base, **ad))
+    assert ("mx_token_product" in names) == few and not Y.any()
