@@ -7,7 +7,7 @@
 // layer's.  Gradient of 2048 tokens x (11008 x 4096), r = 64: base and operands 36 us (25 MB
 // of codes in, 90 MB of bf16 out), dY B and X A^T 33 us (their second operand, from L2,
 // is as many bytes as four 16-token tiles of dY), their sums 8 us, dB and dA 27 us (62 MB of dY
-// and X), their sums 6 us.  8192 tokens x (4096 x 11008), r = 16: 38, 80, 5, 53 and 5 us, X's
+// and X), their sums 6 us.  8192 tokens x (4096 x 11008), r = 16: 37, 81, 5, 47 and 5 us, X's
 // mask being drawn twice.
 //
 // v_mfma_f32_16x16x32_bf16: lane L supplies A[L%16][8(L/16) + j] and

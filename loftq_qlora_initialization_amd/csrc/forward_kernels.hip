@@ -560,8 +560,8 @@ hipError_t launch_lora_down(const void* X, int64_t n_tok, int64_t cols, const fl
   int u = spw <= 1 ? 1 : spw <= 2 ? 2 : spw <= 4 ? 4 : 8;
   if (u > umax) u = umax;
 #define LQ_DOWN(NT, U, TT)                                                                                 \
-LQ_LAUNCH("lora_down", (lora_down_kernel<NT, U, TT>), grid, dim3(1024), 0, s, Xb, n_tok, cols, A, r, ks, \
-          Tws)
+  LQ_LAUNCH("lora_down", (lora_down_kernel<NT, U, TT>), grid, dim3(1024), 0, s, Xb, n_tok, cols, A, r, ks, \
+            Tws)
   if (pl.tt == 4) {
     if (u == 1) LQ_DOWN(1, 1, 4);
     else LQ_DOWN(1, 2, 4);

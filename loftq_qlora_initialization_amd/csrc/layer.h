@@ -80,7 +80,6 @@ struct AdapterOperands {
 // elements of a row of the adapter's operands in the tiled product: three times the padded rank, in whole steps
 inline int adapter_ld(int rp) { return (3 * rp + 63) / 64 * 64; }
 
-
 // What a call's products read: the base's bf16 operand (as it lies, or transposed with zeros
 // past `rows`), or over MXFP4 the codes of X; the adapter's operands; dY with padded rows.
 enum PrepareBase { kBaseNone, kBaseAsItLies, kBaseTransposed, kBaseCodesOfX };

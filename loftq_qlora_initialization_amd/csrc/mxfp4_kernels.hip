@@ -4,7 +4,7 @@
 // TB/s), codes and W to the fp32 residual 61 us (385 MB, 6.3 TB/s).  Neighbouring threads take
 // neighbouring 16 or 32 bytes of a row; the codes of a thread are one word, so no LDS is needed.
 // A residual's r products run on the vector units and the rows of A come from the caches; they,
-// not memory, set its time (11008 x 4096 bf16: 58 us at r = 16, 175 us at r = 64).
+// not memory, set its time (11008 x 4096 bf16, traced: 60 us at r = 16, 160 us at r = 64).
 #include "internal.h"
 #include "mxfp4.h"
 
@@ -31,8 +31,8 @@ __device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
 }
 
 // One thread per 8 consecutive columns of kRows rows of the padded matrix: one row of W, or
-// four of a residual R = W - B A, which share each load of A: 11008 x 4096 bf16 with 1, 2, 4 and
-// 8 rows takes 117, 71, 58 and 66 us at r = 16, and 419, 258, 175 and 172 us at r = 64 (8192 x
+// four of a residual R = W - B A, which share each load of A: calls over 11008 x 4096 bf16 with
+// 1, 2, 4 and 8 rows took 117, 71, 58 and 66 us at r = 16, and 419, 258, 175 and 172 us at r = 64 (8192 x
 // 28672: 2227, 1321, 864 and 963 us).  R is formed in fp32, the r products added in the order of p.
 template <typename T, int kRows>
 __global__ __launch_bounds__(kMxThreads) void mx_quantize_kernel(const T* __restrict__ W, int64_t rows, int64_t cols,

@@ -18,9 +18,11 @@
 // 1.8 (32 x 32) and 2.1 PFLOP/s (16 x 16) in bf16 and 8.0 in FP4 before the clock drops, and
 // in the loop the clock stands at 1.75 to 1.85 GHz with the matrix cores busy 51 to 59 % of
 // the cycles; what a step waits for is its loads (without them a 256 x 256 step of FP4 takes
-// 1.4 instead of 1.9 us).  8192 x 11008 outputs, K = 4096: 655 to 670 us, 1.1 PFLOP/s; 2048 x
-// 4096, K = 11008: 145 to 165 us, 1.1 to 1.27; FP4 8192 x 28672, K = 8192: 1.06 ms, 3.6
-// PFLOP/s.  Tried and slower: half steps in a ring of four (64-byte pieces of lines: every
+// 1.4 instead of 1.9 us).  Traced, mean and least of ten launches: 8192 x 11008 outputs, K =
+// 4096: 668 and 665 us, 1.11 PFLOP/s (the library's product of these sizes, in the same trace:
+// 688 and 667); 2048 x 4096, K = 11008: 163 and 156 us, 1.13 (172 and 172); 2048 x 11008, K =
+// 4096, with the three adapter steps of r = 64: 169 and 159 us, 1.09 (161 and 156, without
+// them); FP4 8192 x 28672, K = 8192: 1.08 and 1.05 ms, 3.57 PFLOP/s.  Tried and slower: half steps in a ring of four (64-byte pieces of lines: every
 // line is fetched twice), the reads of a quarter step before its products (all waves read,
 // then all multiply), 16 x 16 instructions in FP4 (the scales of twice the rows: 77 against 67
 // us at 2048 x 11008, K = 4096).
@@ -59,7 +61,9 @@ constexpr int divisor_up_to(int n, int most) {
 __device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 // Workgroups are dealt to the 8 XCDs round-robin by id; each XCD gets a contiguous run of
-// tiles.  Within a run, kBand token tiles by all features in turn, tokens inner, so that
+// tiles where every tile has one workgroup.  (The K ranges of a divided product are neighbours
+// by id, so that its tiles fall to the XCDs otherwise: it has at most two workgroups a CU, and
+// its time is its launch, first loads and join.)  Within a run, kBand token tiles by all features in turn, tokens inner, so that
 // the rows a band shares stay in the XCD's L2.
 constexpr int64_t kBand = 8;
 __device__ __forceinline__ void tile_of(int64_t wg, int64_t ntm, int64_t ntn, int64_t& tm, int64_t& tn) {
@@ -146,7 +150,8 @@ struct Tile {
       wf[i - MT] = *reinterpret_cast<const i32x4*>(t + (wo ^ (ph * (64 / D) << 4)) + (i - MT) * D * kStepBytes);
   }
   // Every wave has read the place that is loaded next, and all but the last `behind` loads
-  // of every wave are done.
+  // of every wave are done.  Over MXFP4 the scales' loads are among the last ones, so that the
+  // ring of three waits for some of the next step's loads as well.
   template <int behind>
   __device__ __forceinline__ void turn() {
     __builtin_amdgcn_sched_barrier(0);
