@@ -12,9 +12,9 @@ The functions carry the C entry points' names (see include/loftq.h):
     loftq_mxfp4_quantize, loftq_mxfp4_dequantize, loftq_mxfp4_forward, loftq_mxfp4_backward
 and return freshly allocated torch tensors on the input's device (or fill the
 caller's ``out`` / ``buffers`` where those are given).
-With ``stream`` a call runs there instead of on the current stream, and so do the
-allocations of what it returns: inputs have to be ready on that stream, and a reader
-on another stream waits for it.
+With ``stream`` a call runs there instead of on the current stream, and what it returns
+is allocated there: the caller has its inputs ready on that stream and keeps them until
+the call is done (or records them on it), and a reader on another stream waits for it.
 """
 from __future__ import annotations
 
