@@ -326,6 +326,142 @@ loftq_status_t loftq_mxfp4_backward(const void* dY, const void* X, int64_t n_tok
                                     float* dB, float* dA, void* ws, size_t ws_bytes, void* stream);
 size_t loftq_mxfp4_backward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t r);
 
+/* ---- Many adapters beside one shared weight ----
+ *
+ * One frozen base serves many adapters ("参数高效微调：LoRA、Adapter 与 QLoRA" §2.2: the adapter
+ * is all that differs between tasks): a batch whose tokens each have an adapter of their own
+ * goes through the base's product once, without B and A, and through the calls below for its
+ * adapters' terms.  The adapters of a layer lie in a pool of slots of one shape; a slot is
+ * filled, replaced or trained without the others.
+ * The conventions of the layer calls above hold, among them those for values that are not
+ * finite and for dropout. */
+typedef struct {
+  const void* B;         /* [device] slots x rows x rank of dtype dt */
+  const void* A;         /* [device] slots x rank x cols of dtype dt */
+  loftq_dtype_t dt;      /* fp32 factors are rounded to bf16 in the products */
+  int32_t slots;         /* 1 .. 1024 */
+  int32_t rank;          /* 1 .. 64 */
+  const int32_t* ranks;  /* [device] slots numbers, or NULL (all `rank`): a slot's own rank, 0 .. rank (numbers
+                            outside count as the nearest); what its factors hold past it is not used */
+  const float* gains;    /* [device] slots numbers, or NULL (all 1): multiplies alpha */
+  float alpha;           /* [host] adapter scale (finite) */
+} loftq_adapters_t;
+
+/* The plan of a batch: its tokens in the order of their slots, made once and read by every
+ * layer's calls (one launch up to 4096 tokens, two beyond).
+ *   slot_of  [device] n_tok numbers, 4-byte aligned; one outside 0 .. slots - 1: a token without
+ *            an adapter
+ *   plan     [device] loftq_adapters_plan_bytes(n_tok, slots) bytes.  Its int32 words:
+ *              0 .. slots + 1   starts: the tokens of slot s are order[starts[s]] .. order[starts[s + 1] - 1],
+ *                               those without an adapter begin at starts[slots], starts[slots + 1] = n_tok
+ *              from word (slots + 5) / 4 * 4 on   order: n_tok token numbers, a slot's in rising order
+ *            and what the kernels divide their work by.
+ * A plan read by a call of other sizes gives wrong outputs (no access outside the buffers).
+ * UNSUPPORTED: slots > 1024, n_tok >= 2^25. */
+loftq_status_t loftq_adapters_plan(const int32_t* slot_of, int64_t n_tok, int32_t slots, int32_t* plan,
+                                   size_t plan_bytes, void* stream);
+size_t loftq_adapters_plan_bytes(int64_t n_tok, int32_t slots);
+
+/* Each token's own adapter, added to what the shared projection gave:
+ *   Y = Y0 + g s (keep(X) bf16(A_s)^T) bf16(B_s)^T   with the token's slot s, g = alpha gains[s]
+ *   Y = Y0                                           for a token without an adapter
+ * (the second s is dropout's scale).  Sums are in fp32, X A^T between the products is kept to
+ * 24 bits, and Y is rounded once.
+ *   X     [device] n_tok x cols bf16
+ *   ad    [host] the pool
+ *   plan  [device] of this n_tok and these slots
+ *   drop  [host] or NULL (serving)
+ *   Y0    [device] n_tok x rows of dtype ydt, or NULL (zeros); may be Y
+ *   Y     [device] n_tok x rows of dtype ydt out
+ *   ws    [device] loftq_adapters_forward_workspace_bytes(n_tok, rows, cols, slots, rank) bytes
+ * n_tok = 0 or rows = 0 writes nothing.
+ * UNSUPPORTED: cols % 8 != 0, cols = 0, rank > 64, slots > 1024, n_tok >= 2^25, rows or cols >= 2^22, or a
+ * launch of 2^22 workgroups (one per 256 rows of n_tok / 64 + min(n_tok, slots + 1) tiles). */
+loftq_status_t loftq_adapters_forward(const void* X, int64_t n_tok, int64_t rows, int64_t cols,
+                                      const loftq_adapters_t* ad, const int32_t* plan, size_t plan_bytes,
+                                      const loftq_dropout_t* drop, const void* Y0, void* Y, loftq_dtype_t ydt, void* ws,
+                                      size_t ws_bytes, void* stream);
+size_t loftq_adapters_forward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t slots, int32_t rank);
+
+/* Its gradient, with G = dY and the forward's drop and plan:
+ *   dX   = dX0 + g s keep((G bf16(B_s)) bf16(A_s))     a token's own slot; dX0 without an adapter
+ *   dB_s = g s G_s^T (keep(X_s) bf16(A_s)^T)           sums over the slot's tokens; zeros without any
+ *   dA_s = g s (G_s bf16(B_s))^T keep(X_s)             and past the slot's own rank
+ *   dY      [device] n_tok x rows bf16
+ *   X       [device] n_tok x cols bf16; may be NULL without dB and dA
+ *   dX0     [device] n_tok x cols of dtype xdt (the base's gradient), or NULL (zeros); may be dX
+ *   dX      [device] n_tok x cols of dtype xdt out, or NULL
+ *   dB, dA  [device] fp32, the pool's shapes, out, or both NULL; overwritten, not added to
+ *   ws      [device] loftq_adapters_backward_workspace_bytes(n_tok, rows, cols, slots, rank) bytes
+ * UNSUPPORTED as the forward (its launches per 256 columns), and rows = 0. */
+loftq_status_t loftq_adapters_backward(const void* dY, const void* X, int64_t n_tok, int64_t rows, int64_t cols,
+                                       const loftq_adapters_t* ad, const int32_t* plan, size_t plan_bytes,
+                                       const loftq_dropout_t* drop, const void* dX0, void* dX, loftq_dtype_t xdt,
+                                       float* dB, float* dA, void* ws, size_t ws_bytes, void* stream);
+size_t loftq_adapters_backward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t slots, int32_t rank);
+
+/* ---- The optimizer's step ----
+ *
+ * AdamW (Loshchilov and Hutter, "Decoupled weight decay regularization", ICLR 2019) over all
+ * tensors of a model at once, as QLoRA trains its adapters: gradients clipped to a global norm,
+ * states in fp32 or in 8 bits.  Per element, in fp32 (b1, b2 the decays; numbers that do not
+ * depend on the element are formed in fp64 and rounded once):
+ *   g = c grad            c = min(1, max_norm / (norm + 1e-6)), norm = the 2-norm of all gradients (fp64);
+ *                         c = 1 without max_norm
+ *   m = b1 m + (1 - b1) g,   v = b2 v + ((1 - b2) g) g
+ *   p = p (1 - l weight_decay) - l / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps),   l = lr lr_scale
+ * each operation rounded by itself, but for the last quotient, which is off by up to 2 ulp.  p is
+ * rounded to its type once.
+ *
+ * States in 8 bits: blocks of 256 consecutive elements (a tensor's last may be shorter) with an
+ * fp32 scale each, m in OCP e4m3 and v in OCP e5m2.  With a the largest magnitude of the block,
+ * scale = fl(a / 448) for m and fl(a / 57344) for v, 0 where a < 2^-100; code: fl(x fl(1 / scale))
+ * to the nearest, ties to even; a positive v never becomes zero but the smallest code, so that no
+ * step divides by eps alone; value = fl(code scale).  The update takes m and v before they are
+ * rounded.  A block that holds an infinity or a NaN gets the scale NaN. */
+typedef struct {
+  void* param;          /* [device] n elements of dtype pdt */
+  const void* grad;     /* [device] n elements of dtype gdt */
+  void *m, *v;          /* [device] n fp32 numbers, or n bytes each */
+  float *m_scale, *v_scale;   /* [device] ceil(n / 256) numbers each with states in 8 bits, else NULL */
+  void* copy;           /* [device] n bf16: the new parameters rounded, for the products; or NULL */
+  int64_t n;            /* 0: nothing to do, no address is needed */
+  float lr_scale;       /* multiplies lr (LoRA's two factors may learn at different rates) */
+  float weight_decay;
+} loftq_adamw_tensor_t;
+
+typedef struct {
+  double lr, beta1, beta2, eps;   /* lr >= 0, 0 <= beta < 1, eps > 0 */
+  double max_norm;                /* > 0: gradients are clipped; where their norm is infinite or NaN the step
+                                     changes nothing.  0: no norm is formed */
+  int64_t t;                      /* number of the step, from 1 */
+  const int64_t* step;            /* [device] 8-byte aligned, added to t when the kernels run, or NULL */
+  const float* lr_factor;         /* [device] 4-byte aligned, multiplies lr when the kernels run, or NULL */
+} loftq_adamw_t;
+
+/* A step's tensors laid out for the kernels: filled by loftq_adamw_plan, read by every step over
+ * the same tensors (their addresses are in the table). */
+typedef struct {
+  const void* table;      /* [device] */
+  int64_t chunks;
+  int32_t count, bits;
+  loftq_dtype_t pdt, gdt;
+} loftq_adamw_plan_t;
+
+/*   tensors  [host] count tensors, none overlapping another; read before the call returns
+ *   bits     32 or 8 (states)
+ *   table    [device] loftq_adamw_plan_bytes(tensors, count) bytes; also the steps' scratch: two steps over
+ *            one table must not run at the same time
+ *   plan     [host] out
+ * UNSUPPORTED: count > 65536, 2^36 elements or more; bits other than 32 and 8. */
+loftq_status_t loftq_adamw_plan(const loftq_adamw_tensor_t* tensors, int32_t count, loftq_dtype_t pdt,
+                                loftq_dtype_t gdt, int32_t bits, void* table, size_t table_bytes,
+                                loftq_adamw_plan_t* plan, void* stream);
+size_t loftq_adamw_plan_bytes(const loftq_adamw_tensor_t* tensors, int32_t count);
+
+/* One step.  norm: [device] 1 fp32 out (the norm before clipping), or NULL; needs max_norm > 0. */
+loftq_status_t loftq_adamw(const loftq_adamw_plan_t* plan, const loftq_adamw_t* step, float* norm, void* stream);
+
 /* Low-rank step ("LoftQ...", §2.3: best rank-r approximation of W - Q from its
  * r largest singular triplets, Delta = U_r S_r V_r^T).  exact = 1: the SVD of E
  * itself by one-sided (Hestenes) Jacobi on its min(rows, cols) <= 512 short-side

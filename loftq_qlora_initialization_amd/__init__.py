@@ -18,6 +18,8 @@ _BINDING_NAMES = {
     "loftq_dropout", "loftq_qlora_forward_dropout", "loftq_qlora_backward", "loftq_mxfp4_quantize", "loftq_mxfp4_dequantize",
     "loftq_mxfp4_forward", "loftq_mxfp4_backward", "LoftqDropout", "qlora_forward_dropout_workspace_bytes",
     "qlora_backward_workspace_bytes", "mxfp4_forward_workspace_bytes", "mxfp4_backward_workspace_bytes",
+    "loftq_adapters_plan", "loftq_adapters_forward", "loftq_adapters_backward", "AdaptersPlan", "adapters_plan_bytes",
+    "adapters_forward_workspace_bytes", "adapters_backward_workspace_bytes", "loftq_adamw", "AdamWTensors",
 }
 
 

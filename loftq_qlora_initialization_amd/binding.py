@@ -9,7 +9,8 @@ The functions carry the C entry points' names (see include/loftq.h):
     loftq_nf4_quantize, loftq_double_quant, loftq_nf4_dequantize,
     loftq_nf4_merge, loftq_nf4_unmerge, loftq_lowrank_svd, loftq_init,
     loftq_qlora_forward, loftq_dropout, loftq_qlora_forward_dropout, loftq_qlora_backward,
-    loftq_mxfp4_quantize, loftq_mxfp4_dequantize, loftq_mxfp4_forward, loftq_mxfp4_backward
+    loftq_mxfp4_quantize, loftq_mxfp4_dequantize, loftq_mxfp4_forward, loftq_mxfp4_backward,
+    loftq_adapters_plan, loftq_adapters_forward, loftq_adapters_backward, loftq_adamw
 and return freshly allocated torch tensors on the input's device (or fill the
 caller's ``out`` / ``buffers`` where those are given).
 With ``stream`` a call runs there instead of on the current stream, and what it returns
@@ -46,7 +47,10 @@ EXPORTS = ["loftq_init_batch", "loftq_batch_workspace_bytes", "loftq_nf4_quantiz
            "loftq_dropout", "loftq_qlora_forward_dropout", "loftq_qlora_forward_dropout_workspace_bytes",
            "loftq_qlora_backward", "loftq_qlora_backward_workspace_bytes", "loftq_mxfp4_packed_bytes",
            "loftq_mxfp4_scale_bytes", "loftq_mxfp4_quantize", "loftq_mxfp4_dequantize", "loftq_mxfp4_forward",
-           "loftq_mxfp4_forward_workspace_bytes", "loftq_mxfp4_backward", "loftq_mxfp4_backward_workspace_bytes"]
+           "loftq_mxfp4_forward_workspace_bytes", "loftq_mxfp4_backward", "loftq_mxfp4_backward_workspace_bytes",
+           "loftq_adapters_plan", "loftq_adapters_plan_bytes", "loftq_adapters_forward",
+           "loftq_adapters_forward_workspace_bytes", "loftq_adapters_backward",
+           "loftq_adapters_backward_workspace_bytes", "loftq_adamw_plan", "loftq_adamw_plan_bytes", "loftq_adamw"]
 
 
 class LoftqConfig(ctypes.Structure):
@@ -67,6 +71,26 @@ class LoftqMatrix(ctypes.Structure):
 
 class LoftqDropout(ctypes.Structure):
     _fields_ = [("p", ctypes.c_float), ("seed", _U64), ("offset", _U64), ("step", _P)]
+
+
+class LoftqAdapters(ctypes.Structure):
+    _fields_ = [("B", _P), ("A", _P), ("dt", ctypes.c_int), ("slots", _I32), ("rank", _I32), ("ranks", _P),
+                ("gains", _P), ("alpha", ctypes.c_float)]
+
+
+class LoftqAdamwTensor(ctypes.Structure):
+    _fields_ = [("param", _P), ("grad", _P), ("m", _P), ("v", _P), ("m_scale", _P), ("v_scale", _P), ("copy", _P),
+                ("n", _I64), ("lr_scale", ctypes.c_float), ("weight_decay", ctypes.c_float)]
+
+
+class LoftqAdamw(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("max_norm", ctypes.c_double), ("t", _I64), ("step", _P), ("lr_factor", _P)]
+
+
+class LoftqAdamwPlan(ctypes.Structure):
+    _fields_ = [("table", _P), ("chunks", _I64), ("count", _I32), ("bits", _I32), ("pdt", ctypes.c_int),
+                ("gdt", ctypes.c_int)]
 
 
 def _sig(name, res, args):
@@ -113,6 +137,20 @@ _c_mx_scales = _sig("loftq_mxfp4_scale_bytes", _SZ, [_I64, _I64])
 _c_mx_quant = _sig("loftq_mxfp4_quantize", ctypes.c_int, [_P, ctypes.c_int, _I64, _I64, _P, _P, _I32, _P, _P, _P])
 _c_mx_deq = _sig("loftq_mxfp4_dequantize", ctypes.c_int,
                  [_P, _P, _I64, _I64, _P, ctypes.c_int, _P, ctypes.c_int, _P])
+_POOL = ctypes.POINTER(LoftqAdapters)
+_c_ad_plan = _sig("loftq_adapters_plan", ctypes.c_int, [_P, _I64, _I32, _P, _SZ, _P])
+_c_ad_plan_bytes = _sig("loftq_adapters_plan_bytes", _SZ, [_I64, _I32])
+_c_ad_fwd = _sig("loftq_adapters_forward", ctypes.c_int,
+                 [_P, _I64, _I64, _I64, _POOL, _P, _SZ, _DROP, _P, _P, ctypes.c_int, _P, _SZ, _P])
+_c_ad_bwd = _sig("loftq_adapters_backward", ctypes.c_int,
+                 [_P, _P, _I64, _I64, _I64, _POOL, _P, _SZ, _DROP, _P, _P, ctypes.c_int, _P, _P, _P, _SZ, _P])
+_c_ad_fwd_ws = _sig("loftq_adapters_forward_workspace_bytes", _SZ, [_I64, _I64, _I64, _I32, _I32])
+_c_ad_bwd_ws = _sig("loftq_adapters_backward_workspace_bytes", _SZ, [_I64, _I64, _I64, _I32, _I32])
+_TENSORS = ctypes.POINTER(LoftqAdamwTensor)
+_c_adamw_plan = _sig("loftq_adamw_plan", ctypes.c_int,
+                     [_TENSORS, _I32, ctypes.c_int, ctypes.c_int, _I32, _P, _SZ, ctypes.POINTER(LoftqAdamwPlan), _P])
+_c_adamw_bytes = _sig("loftq_adamw_plan_bytes", _SZ, [_TENSORS, _I32])
+_c_adamw = _sig("loftq_adamw", ctypes.c_int, [ctypes.POINTER(LoftqAdamwPlan), ctypes.POINTER(LoftqAdamw), _P, _P])
 _c_svd = _sig("loftq_lowrank_svd", ctypes.c_int,
               [_P, _I64, _I64, _I32, _I32, _I32, _I32, _P, _U64, _I32, _P, _P, _P, _P, _SZ, _P])
 _c_svd_ws = _sig("loftq_lowrank_svd_workspace_bytes", _SZ, [_I64, _I64, _I32, _I32, _I32])
@@ -624,6 +662,216 @@ def loftq_mxfp4_backward(dY: torch.Tensor, X: Optional[torch.Tensor], packed: to
     return _layer_backward("loftq_mxfp4_backward", _c_mx_bwd, _c_mx_bwd_ws, dY, X, dev,
                            _mx_args(dev, packed, scales, rows, cols), rows, cols, B, A, alpha,
                            _dropout(p, seed, offset, step, dev), need_dx, out, dx_dtype, ws, stream)
+
+
+# ---- many adapters beside one shared weight ----
+
+class AdaptersPlan:
+    """A batch's tokens in the order of their slots, made by loftq_adapters_plan and read by every layer's calls.
+    starts[s] .. starts[s + 1]: where slot s's tokens lie in `order` (token numbers); those without an adapter begin
+    at starts[slots], and starts[slots + 1] is the number of tokens."""
+
+    def __init__(self, n_tok: int, slots: int, device="cuda", stream=None):
+        self.n_tok, self.slots = int(n_tok), int(slots)
+        self.nbytes = adapters_plan_bytes(n_tok, slots)
+        if self.nbytes == 0:
+            raise LoftqError("loftq_adapters_plan_bytes", 2)
+        self.buffer = _empty(self.nbytes // 4, torch.int32, device, stream)
+        at = (self.slots + 5) // 4 * 4
+        self.starts, self.order = self.buffer[:self.slots + 2], self.buffer[at:at + self.n_tok]
+
+
+def adapters_plan_bytes(n_tok: int, slots: int) -> int:
+    return int(_c_ad_plan_bytes(n_tok, slots))
+
+
+def adapters_forward_workspace_bytes(n_tok: int, rows: int, cols: int, slots: int, rank: int) -> int:
+    return int(_c_ad_fwd_ws(n_tok, rows, cols, slots, rank))
+
+
+def adapters_backward_workspace_bytes(n_tok: int, rows: int, cols: int, slots: int, rank: int) -> int:
+    return int(_c_ad_bwd_ws(n_tok, rows, cols, slots, rank))
+
+
+def loftq_adapters_plan(slot_of: torch.Tensor, slots: int, plan: Optional[AdaptersPlan] = None,
+                        stream=None) -> AdaptersPlan:
+    """The plan of a batch whose token i has the adapter of slot slot_of[i] (int32), or none where that is not one of
+    0 .. slots - 1 (-1, say)."""
+    dev = _first(slot_of, "slot_of")
+    if slot_of.dtype is not torch.int32 or slot_of.dim() != 1:
+        raise TypeError("slot_of must be a vector of int32")
+    n = slot_of.shape[0]
+    if plan is None:
+        plan = AdaptersPlan(n, slots, slot_of.device, stream)
+    elif plan.n_tok != n or plan.slots != slots or plan.buffer.get_device() != dev:
+        raise ValueError(f"plan must be one of {n} tokens and {slots} slots on device {dev}")
+    _call("loftq_adapters_plan", _c_ad_plan, dev, stream, slot_of.data_ptr(), n, slots, plan.buffer.data_ptr(),
+          plan.nbytes)
+    return plan
+
+
+def _pool(dev, B, A, ranks, gains, alpha, plan, n):
+    """(the pool's struct, slots, rows, rank, cols)"""
+    if B.dim() != 3 or A.dim() != 3:
+        raise ValueError("B and A must be slots x rows x rank and slots x rank x cols")
+    slots, rows, rank = B.shape
+    cols = A.shape[2]
+    b = _expect(B, "B", dev, None, (slots, rows, rank))
+    a = _expect(A, "A", dev, B.dtype, (slots, rank, cols))
+    k = None if ranks is None else _expect(ranks, "ranks", dev, torch.int32, (slots,))
+    g = None if gains is None else _expect(gains, "gains", dev, torch.float32, (slots,))
+    if plan.n_tok != n or plan.slots != slots or plan.buffer.get_device() != dev:
+        raise ValueError(f"plan must be one of {n} tokens and {slots} slots on device {dev}")
+    dt = LOFTQ_BF16 if B.dtype is torch.bfloat16 else LOFTQ_F32
+    return ctypes.byref(LoftqAdapters(b, a, dt, slots, rank, k, g, alpha)), slots, rows, rank, cols
+
+
+def loftq_adapters_forward(X: torch.Tensor, B: torch.Tensor, A: torch.Tensor, plan: AdaptersPlan,
+                           ranks: Optional[torch.Tensor] = None, gains: Optional[torch.Tensor] = None,
+                           alpha: float = 1.0, p: float = 0.0, seed: int = 0, offset: int = 0,
+                           step: Optional[torch.Tensor] = None, base: Optional[torch.Tensor] = None,
+                           out: Optional[torch.Tensor] = None, out_dtype=torch.float32,
+                           ws: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """base + alpha gains[s] / (1 - p) (keep(X) bf16(A[s])^T) bf16(B[s])^T, s being each token's slot, for bf16 X
+    (n_tok x cols) and pools B (slots x rows x rank) and A (slots x rank x cols); `base` (n_tok x rows, zeros where
+    not given) is what the shared projection gave and may be `out`."""
+    dev = _tokens(X, "X", A.shape[-1])
+    n = X.shape[0]
+    pool, slots, rows, rank, cols = _pool(dev, B, A, ranks, gains, alpha, plan, n)
+    out_dtype = _out_dtype(out if out is not None else base, out_dtype)
+    y0 = None if base is None else _expect(base, "base", dev, out_dtype, (n, rows))
+    if out is None:
+        out = _empty((n, rows), out_dtype, X.device, stream)
+    y = _expect(out, "out", dev, out_dtype, (n, rows))
+    ws, w, ws_bytes = _workspace(ws, _c_ad_fwd_ws, (n, rows, cols, slots, rank), X, stream)
+    _call("loftq_adapters_forward", _c_ad_fwd, dev, stream, X.data_ptr(), n, rows, cols, pool, plan.buffer.data_ptr(),
+          plan.nbytes, _dropout(p, seed, offset, step, dev), y0, y,
+          LOFTQ_BF16 if out_dtype is torch.bfloat16 else LOFTQ_F32, w, ws_bytes)
+    return out
+
+
+def loftq_adapters_backward(dY: torch.Tensor, X: Optional[torch.Tensor], B: torch.Tensor, A: torch.Tensor,
+                            plan: AdaptersPlan, ranks: Optional[torch.Tensor] = None,
+                            gains: Optional[torch.Tensor] = None, alpha: float = 1.0, p: float = 0.0, seed: int = 0,
+                            offset: int = 0, step: Optional[torch.Tensor] = None, base: Optional[torch.Tensor] = None,
+                            need_dx: bool = True, out=None, dx_dtype=torch.bfloat16, ws: Optional[torch.Tensor] = None,
+                            stream=None):
+    """(dX, dB, dA) of loftq_adapters_forward for bf16 dY (n_tok x rows) and the forward's X, mask and plan: dX with
+    `base` (the shared projection's gradient, which may be dX itself) added, dB and dA fp32 pools with zeros for
+    slots without tokens.  `out`: the three tensors to fill, None for one that is not wanted (dB and dA both or
+    neither)."""
+    dev = _tokens(dY, "dY", B.shape[1] if B.dim() == 3 else -1)
+    n = dY.shape[0]
+    pool, slots, rows, rank, cols = _pool(dev, B, A, ranks, gains, alpha, plan, n)
+    if out is not None:
+        dX, dB, dA = out
+    else:
+        dx_dtype = _out_dtype(base, dx_dtype)
+        dX = _empty((n, cols), dx_dtype, dY.device, stream) if need_dx else None
+        dB, dA = (_empty(t.shape, torch.float32, dY.device, stream) for t in (B, A))
+    if X is None and dB is not None:
+        raise ValueError("X must be given for dB and dA")
+    x = None if X is None else _expect(X, "X", dev, torch.bfloat16, (n, cols))
+    gx = None if dX is None else _expect(dX, "dX", dev, None, (n, cols))
+    g0 = None if base is None or dX is None else _expect(base, "base", dev, dX.dtype, (n, cols))
+    gb = None if dB is None else _expect(dB, "dB", dev, torch.float32, (slots, rows, rank))
+    ga = None if dA is None else _expect(dA, "dA", dev, torch.float32, (slots, rank, cols))
+    ws, w, ws_bytes = _workspace(ws, _c_ad_bwd_ws, (n, rows, cols, slots, rank), dY, stream)
+    _call("loftq_adapters_backward", _c_ad_bwd, dev, stream, dY.data_ptr(), x, n, rows, cols, pool,
+          plan.buffer.data_ptr(), plan.nbytes, _dropout(p, seed, offset, step, dev), g0, gx,
+          LOFTQ_F32 if dX is not None and dX.dtype is torch.float32 else LOFTQ_BF16, gb, ga, w, ws_bytes)
+    return dX, dB, dA
+
+
+# ---- the optimizer's step ----
+
+class AdamWTensors:
+    """The tensors that loftq_adamw steps over: parameters, their gradients and states, laid out once for the kernels.
+    Keeps the tensors; their memory must stay where it is.
+
+    params, grads     lists of contiguous device tensors, each list of one type (float32 or bfloat16)
+    bits              32 (states in float32) or 8 (m in float8_e4m3fn, v in float8_e5m2, a float32 scale per 256)
+    m, v (m_scale, v_scale)  the states, new ones of zeros where not given (their type then says the bits)
+    copies            bfloat16 tensors that take the new parameters rounded, or None
+    lr_scale, weight_decay   a number, or one per tensor
+    """
+
+    def __init__(self, params, grads, bits: int = 32, m=None, v=None, m_scale=None, v_scale=None, copies=None,
+                 lr_scale=1.0, weight_decay=0.0, stream=None):
+        params, grads = list(params), list(grads)
+        count = len(params)
+        if count == 0:
+            raise ValueError("params must hold a tensor")
+        dev = _first(params[0], "params")
+        pdt, gdt = _wdtype(params[0]), _wdtype(grads[0])
+        if m is not None:
+            bits = 32 if m[0].dtype is torch.float32 else 8
+        if bits not in (32, 8):
+            raise LoftqError("loftq_adamw_plan", 2)
+        m_dtype, v_dtype = (torch.float32, torch.float32) if bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
+
+        def states(given, dtype, per=1):
+            if given is not None:
+                return list(given)
+            with _on(stream):
+                return [torch.zeros(p.shape if per == 1 else -(-p.numel() // per), dtype=dtype, device=p.device)
+                        for p in params]
+
+        self.params, self.grads = params, grads
+        self.m, self.v = states(m, m_dtype), states(v, v_dtype)
+        self.m_scale = states(m_scale, torch.float32, 256) if bits == 8 else None
+        self.v_scale = states(v_scale, torch.float32, 256) if bits == 8 else None
+        self.copies = None if copies is None else list(copies)
+        lists = dict(params=(params, params[0].dtype, 1), grads=(grads, grads[0].dtype, 1), m=(self.m, m_dtype, 1),
+                     v=(self.v, v_dtype, 1), m_scale=(self.m_scale, torch.float32, 256),
+                     v_scale=(self.v_scale, torch.float32, 256), copies=(self.copies, torch.bfloat16, 1))
+        at = {}
+        for name, (tensors, dtype, per) in lists.items():
+            if tensors is None:
+                at[name] = [None] * count
+                continue
+            if len(tensors) != count:
+                raise ValueError(f"{name} must hold {count} tensors")
+            at[name] = [_expect(t, name, dev, dtype) for t in tensors]
+            for t, p in zip(tensors, params):
+                if t.numel() != -(-p.numel() // per):
+                    raise ValueError(f"{name} must have as many elements as its parameter"
+                                     + ("" if per == 1 else " has blocks of 256"))
+        per_tensor = [list(x) if hasattr(x, "__len__") else [x] * count for x in (lr_scale, weight_decay)]
+        if any(len(x) != count for x in per_tensor):
+            raise ValueError(f"lr_scale and weight_decay are numbers or lists of {count}")
+        descs = (LoftqAdamwTensor * count)(*[
+            LoftqAdamwTensor(*(at[k][i] for k in ("params", "grads", "m", "v", "m_scale", "v_scale", "copies")),
+                             p.numel(), per_tensor[0][i], per_tensor[1][i]) for i, p in enumerate(params)])
+        self.bits, self.device = bits, params[0].device
+        self.table = _scratch(_c_adamw_bytes(descs, count), self.device, stream)
+        if stream is not None:   # later steps may run elsewhere
+            self.table.record_stream(torch.cuda.current_stream(self.device))
+        self.plan = LoftqAdamwPlan()
+        _call("loftq_adamw_plan", _c_adamw_plan, dev, stream, descs, count, pdt, gdt, bits, self.table.data_ptr(),
+              self.table.numel(), ctypes.byref(self.plan))
+
+
+def loftq_adamw(tensors: AdamWTensors, lr: float, beta1: float = 0.9, beta2: float = 0.999, eps: float = 1e-8,
+                t: int = 1, max_norm: float = 0.0, step: Optional[torch.Tensor] = None,
+                lr_factor: Optional[torch.Tensor] = None, norm: Optional[torch.Tensor] = None, stream=None):
+    """One AdamW step, the t-th (from 1), over all tensors in place.  With max_norm the gradients are clipped to it
+    and their norm before clipping is returned (`norm`, one fp32 element); where that is infinite or NaN nothing is
+    changed.  `step` (one int64 element, added to t) and `lr_factor` (one fp32 element, multiplies lr) are read when
+    the kernels run."""
+    dev = tensors.params[0].get_device()
+    at = None if step is None else _expect(step, "step", dev, torch.int64, (1,))
+    factor = None if lr_factor is None else _expect(lr_factor, "lr_factor", dev, torch.float32)
+    if factor is not None and lr_factor.numel() != 1:
+        raise ValueError("lr_factor must hold one element")
+    if norm is None and max_norm > 0:
+        norm = _empty((), torch.float32, tensors.device, stream)
+    to = None if norm is None else _expect(norm, "norm", dev, torch.float32)
+    if norm is not None and norm.numel() != 1:
+        raise ValueError("norm must hold one element")
+    how = LoftqAdamw(lr, beta1, beta2, eps, max_norm, t, at, factor)
+    _call("loftq_adamw", _c_adamw, dev, stream, ctypes.byref(tensors.plan), ctypes.byref(how), to)
+    return norm
 
 
 def lowrank_workspace_bytes(rows: int, cols: int, r: int, oversample: int, exact: bool) -> int:

@@ -1,0 +1,224 @@
+// C-ABI entry points of many adapters beside one shared weight: argument validation, workspace
+// layout, then launches.
+#include <cmath>
+
+#include "adapters.h"
+#include "layer.h"
+
+using namespace loftq;
+
+namespace {
+
+typedef int64_t i64;
+
+constexpr i64 kMostTokens = i64(1) << 25, kMostWidth = i64(1) << 22, kMostWorkgroups = i64(1) << 22;
+
+struct Arena {
+  char* base;
+  size_t used = 0;
+  template <typename T>
+  T* take(i64 count) {
+    T* p = base != nullptr ? reinterpret_cast<T*>(base + used) : nullptr;
+    used += (static_cast<size_t>(count) * sizeof(T) + 255) / 256 * 256;
+    return p;
+  }
+};
+
+int rank_pad(int r) { return (r + 15) / 16 * 16; }
+i64 pad8(i64 n) { return (n + 7) / 8 * 8; }
+
+bool plan_sizes_ok(i64 n, int slots) { return n < kMostTokens && slots <= kMostSlots; }
+
+// Every launch of a call stays below 2^32 work-items.
+bool sizes_ok(i64 n, i64 rows, i64 cols, int slots, int rank, bool backward) {
+  if (!plan_sizes_ok(n, slots) || rank > 64 || rows >= kMostWidth || cols >= kMostWidth || cols == 0 || cols % 8 != 0) return false;
+  if (backward && rows == 0) return false;
+  const PlanLayout p = plan_layout(n, slots);
+  const i64 features = backward ? cols : rows;
+  if (p.max_tiles * ((features + 255) / 256) >= kMostWorkgroups) return false;
+  if (!backward) return true;
+  if (p.max_chunks * ((pad8(rows) + 127) / 128 + (cols + 127) / 128) >= 2 * kMostWorkgroups) return false;
+  return n * (pad8(rows) / 8) < (i64(1) << 32) - 4096;
+}
+
+struct ForwardSpace {
+  float* partials;   // of X A^T
+  int ks;
+  size_t bytes;
+};
+ForwardSpace forward_space(void* ws, i64 n, i64 cols, int slots, int rank) {
+  Arena a{static_cast<char*>(ws)};
+  ForwardSpace f{};
+  f.ks = adapters_down_splits(n, slots, cols);
+  f.partials = a.take<float>(adapters_down_tiles_bound(n, slots, cols) * kTile * rank_pad(rank));
+  f.bytes = a.used;
+  return f;
+}
+
+struct BackwardSpace {
+  __bf16 *G, *Pt, *Ht;
+  float *down_p, *down_h, *P, *grad_b, *grad_a;
+  int ks_p, ks_h;
+  size_t bytes;
+};
+BackwardSpace backward_space(void* ws, i64 n, i64 rows, i64 cols, int slots, int rank) {
+  Arena a{static_cast<char*>(ws)};
+  BackwardSpace f{};
+  const i64 rows8 = pad8(rows);
+  const int rp = rank_pad(rank);
+  const PlanLayout p = plan_layout(n, slots);
+  f.ks_p = adapters_down_splits(n, slots, rows8);
+  f.ks_h = adapters_down_splits(n, slots, cols);
+  if (rows8 != rows) f.G = a.take<__bf16>(n * rows8);
+  f.down_p = a.take<float>(adapters_down_tiles_bound(n, slots, rows8) * kTile * rp);
+  f.down_h = a.take<float>(adapters_down_tiles_bound(n, slots, cols) * kTile * rp);
+  f.P = a.take<float>(p.max_tiles * kTile * rp);
+  f.Pt = a.take<__bf16>(3 * p.max_tiles * kTile * rp);
+  f.Ht = a.take<__bf16>(3 * p.max_tiles * kTile * rp);
+  f.grad_b = a.take<float>(p.max_chunks * rows8 * rp);
+  f.grad_a = a.take<float>(p.max_chunks * cols * rp);
+  f.bytes = a.used;
+  return f;
+}
+
+bool dtype_ok(loftq_dtype_t t) { return t == LOFTQ_F32 || t == LOFTQ_BF16; }
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+bool drop_ok(const loftq_dropout_t* d) {
+  return d == nullptr || (std::isfinite(d->p) && d->p >= 0.f && d->p <= 1.f &&
+                          (reinterpret_cast<uintptr_t>(d->step) & 7u) == 0);
+}
+DropArg drop_arg(const loftq_dropout_t* d) {
+  if (d == nullptr) return DropArg{0, 0, nullptr, 0, 1.f};
+  const uint32_t thr = static_cast<uint32_t>(static_cast<double>(d->p) * 65536.0 + 0.5);
+  const float scale = thr >= 65536u ? 0.f : static_cast<float>(65536.0 / (65536.0 - thr));
+  return DropArg{d->seed, d->offset, d->step, thr, scale};
+}
+
+// Sizes, types and numbers of a call; then, where it has work, its pool.
+loftq_status_t check_call(i64 n, i64 rows, i64 cols, const loftq_adapters_t* ad, const loftq_dropout_t* drop) {
+  if (!shape_ok(rows, cols) || n < 0 || n >= (i64(1) << 31) || ad == nullptr) return LOFTQ_ERR_INVALID_ARG;
+  if (ad->slots < 1 || ad->rank < 1 || !dtype_ok(ad->dt) || !std::isfinite(ad->alpha) || !drop_ok(drop)) return LOFTQ_ERR_INVALID_ARG;
+  return std::isfinite(ad->alpha * drop_arg(drop).scale) ? LOFTQ_OK : LOFTQ_ERR_INVALID_ARG;
+}
+loftq_status_t check_pool(const loftq_adapters_t* ad, const int32_t* plan, size_t plan_bytes, i64 n) {
+  if (!ad->B || !ad->A || !aligned16(ad->B) || !aligned16(ad->A)) return LOFTQ_ERR_INVALID_ARG;
+  if (!aligned4(ad->ranks) || !aligned4(ad->gains)) return LOFTQ_ERR_INVALID_ARG;
+  if (!plan || !aligned16(plan)) return LOFTQ_ERR_INVALID_ARG;
+  return plan_bytes < static_cast<size_t>(plan_layout(n, ad->slots).words) * 4 ? LOFTQ_ERR_WORKSPACE : LOFTQ_OK;
+}
+Pool pool_of(const loftq_adapters_t* ad, const DropArg& d) {
+  return Pool{ad->B, ad->A, ad->dt, ad->slots, ad->rank, rank_pad(ad->rank), ad->ranks, ad->gains, ad->alpha * d.scale};
+}
+
+#define LQ_TRY(call)                                  \
+  do {                                                \
+    const hipError_t lq_e_ = (call);                  \
+    if (lq_e_ != hipSuccess) return LOFTQ_ERR_HIP;    \
+  } while (0)
+
+bool query_ok(i64 n, i64 rows, i64 cols, int32_t slots, int32_t rank, bool backward) {
+  return shape_ok(rows, cols) && n >= 0 && n < (i64(1) << 31) && slots >= 1 && rank >= 1 &&
+         sizes_ok(n, rows, cols, slots, rank, backward);
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t loftq_adapters_plan_bytes(int64_t n_tok, int32_t slots) {
+  if (n_tok < 0 || slots < 1 || !plan_sizes_ok(n_tok, slots)) return 0;
+  return static_cast<size_t>(plan_layout(n_tok, slots).words) * 4;
+}
+
+loftq_status_t loftq_adapters_plan(const int32_t* slot_of, int64_t n_tok, int32_t slots, int32_t* plan, size_t plan_bytes,
+                                   void* stream) {
+  if (n_tok < 0 || n_tok >= (i64(1) << 31) || slots < 1) return LOFTQ_ERR_INVALID_ARG;
+  if (!plan_sizes_ok(n_tok, slots)) return LOFTQ_ERR_UNSUPPORTED;
+  if ((n_tok > 0 && !slot_of) || !aligned4(slot_of) || !plan || !aligned16(plan)) return LOFTQ_ERR_INVALID_ARG;
+  const PlanLayout p = plan_layout(n_tok, slots);
+  if (plan_bytes < static_cast<size_t>(p.words) * 4) return LOFTQ_ERR_WORKSPACE;
+  return from_hip(launch_adapters_plan(slot_of, plan, p, static_cast<hipStream_t>(stream)));
+}
+
+size_t loftq_adapters_forward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t slots, int32_t rank) {
+  return query_ok(n_tok, rows, cols, slots, rank, false) && n_tok > 0 ? forward_space(nullptr, n_tok, cols, slots, rank).bytes : 0;
+}
+
+loftq_status_t loftq_adapters_forward(const void* X, int64_t n_tok, int64_t rows, int64_t cols, const loftq_adapters_t* ad,
+                                      const int32_t* plan, size_t plan_bytes, const loftq_dropout_t* drop, const void* Y0,
+                                      void* Y, loftq_dtype_t ydt, void* ws, size_t ws_bytes, void* stream) {
+  loftq_status_t st = check_call(n_tok, rows, cols, ad, drop);
+  if (st != LOFTQ_OK) return st;
+  if (!dtype_ok(ydt)) return LOFTQ_ERR_INVALID_ARG;
+  if (n_tok == 0 || rows == 0) return LOFTQ_OK;   // nothing to write
+  if (!sizes_ok(n_tok, rows, cols, ad->slots, ad->rank, false)) return LOFTQ_ERR_UNSUPPORTED;
+  st = check_pool(ad, plan, plan_bytes, n_tok);
+  if (st != LOFTQ_OK) return st;
+  if (!X || !Y || !ws || !aligned16(X) || !aligned16(Y0) || !aligned16(Y) || !aligned16(ws)) return LOFTQ_ERR_INVALID_ARG;
+  const ForwardSpace f = forward_space(ws, n_tok, cols, ad->slots, ad->rank);
+  if (ws_bytes < f.bytes) return LOFTQ_ERR_WORKSPACE;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const DropArg d = drop_arg(drop), none = drop_arg(nullptr);
+  const PlanView view = plan_view(plan, plan_layout(n_tok, ad->slots));
+  const Pool pool = pool_of(ad, d);
+  LQ_TRY(launch_adapters_down(AdapterDownJobs{{{}, {static_cast<const __bf16*>(X), cols, rows, f.partials, f.ks, 0, d}}}, view, pool, s));
+  return from_hip(launch_adapters_up(AdapterUp{f.partials, f.ks, rows, Y0, Y, ydt, false, none}, view, pool, s));
+}
+
+size_t loftq_adapters_backward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t slots, int32_t rank) {
+  return query_ok(n_tok, rows, cols, slots, rank, true) && n_tok > 0 ? backward_space(nullptr, n_tok, rows, cols, slots, rank).bytes
+                                                                     : 0;
+}
+
+loftq_status_t loftq_adapters_backward(const void* dY, const void* X, int64_t n_tok, int64_t rows, int64_t cols,
+                                       const loftq_adapters_t* ad, const int32_t* plan, size_t plan_bytes,
+                                       const loftq_dropout_t* drop, const void* dX0, void* dX, loftq_dtype_t xdt, float* dB,
+                                       float* dA, void* ws, size_t ws_bytes, void* stream) {
+  loftq_status_t st = check_call(n_tok, rows, cols, ad, drop);
+  if (st != LOFTQ_OK) return st;
+  if (dX && !dtype_ok(xdt)) return LOFTQ_ERR_INVALID_ARG;
+  if ((dB == nullptr) != (dA == nullptr)) return LOFTQ_ERR_INVALID_ARG;
+  if (!dX && !dB && n_tok > 0) return LOFTQ_ERR_INVALID_ARG;   // without tokens dX has no elements and may have no address
+  if (!sizes_ok(n_tok, rows, cols, ad->slots, ad->rank, true)) return LOFTQ_ERR_UNSUPPORTED;
+  st = check_pool(ad, plan, plan_bytes, n_tok);
+  if (st != LOFTQ_OK) return st;
+  if (!aligned16(dX0) || !aligned16(dX) || !aligned16(dB) || !aligned16(dA)) return LOFTQ_ERR_INVALID_ARG;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const DropArg d = drop_arg(drop), none = drop_arg(nullptr);
+  const PlanView view = plan_view(plan, plan_layout(n_tok, ad->slots));
+  const Pool pool = pool_of(ad, d);
+  if (n_tok == 0) {   // sums over no tokens
+    if (dB) LQ_TRY(launch_adapters_grad_sum(AdapterGradJobs{{{nullptr, nullptr, nullptr, dB, rows, rows, none}, {nullptr, nullptr, nullptr, dA, cols, cols, none}}}, view, pool, s));
+    return LOFTQ_OK;
+  }
+  if (!dY || !ws || !aligned16(dY) || !aligned16(ws)) return LOFTQ_ERR_INVALID_ARG;
+  if (dB && (!X || !aligned16(X))) return LOFTQ_ERR_INVALID_ARG;
+  const BackwardSpace f = backward_space(ws, n_tok, rows, cols, ad->slots, ad->rank);
+  if (ws_bytes < f.bytes) return LOFTQ_ERR_WORKSPACE;
+  const i64 rows8 = pad8(rows);
+  const __bf16* G = static_cast<const __bf16*>(dY);
+  const __bf16* Xb = static_cast<const __bf16*>(X);
+  if (f.G != nullptr) {
+    LQ_TRY(launch_adapters_pad(G, f.G, n_tok, rows, rows8, s));
+    G = f.G;
+  }
+  // P = G B for dX and dA, H = keep(X) A^T for dB
+  AdapterDownJobs down{{{G, rows8, rows, f.down_p, f.ks_p, 0, none}, {}}};
+  AdapterSumJobs sum{{{f.down_p, f.ks_p, dX ? f.P : nullptr, dB ? f.Pt : nullptr}, {}}};
+  if (dB) {
+    down.job[1] = AdapterDown{Xb, cols, rows, f.down_h, f.ks_h, 0, d};
+    sum.job[1] = AdapterSum{f.down_h, f.ks_h, nullptr, f.Ht};
+  }
+  LQ_TRY(launch_adapters_down(down, view, pool, s));
+  LQ_TRY(launch_adapters_sum(sum, view, pool.rp, s));
+  if (dB) {
+    const AdapterGradJobs grad{{{G, f.Ht, f.grad_b, dB, rows8, rows, none}, {Xb, f.Pt, f.grad_a, dA, cols, cols, d}}};
+    LQ_TRY(launch_adapters_grad(grad, view, pool, s));
+    LQ_TRY(launch_adapters_grad_sum(grad, view, pool, s));
+  }
+  if (!dX) return LOFTQ_OK;
+  return from_hip(launch_adapters_up(AdapterUp{f.P, 1, cols, dX0, dX, xdt, true, d}, view, pool, s));
+}
+
+}  // extern "C"

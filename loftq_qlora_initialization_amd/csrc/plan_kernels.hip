@@ -1,0 +1,153 @@
+// The plan of a batch: a stable counting sort of its tokens by slot, and the tiles and chunks
+// that the products divide their work by.  Stable without atomics on the order: a wave owns
+// consecutive tokens, its own counters, and ranks 64 of them at a time by ballots over the
+// bits of their slots.
+//
+// Bound by latency: 64 tokens are one workgroup's few dependent steps.
+#include "adapters.h"
+
+namespace loftq {
+namespace {
+
+constexpr int kWaves = kPlanThreads / 64;
+
+__device__ __forceinline__ int group_of(const int32_t* slot_of, int64_t i, int slots) {
+  const int s = slot_of[i];
+  return static_cast<unsigned>(s) < static_cast<unsigned>(slots) ? s : slots;
+}
+
+// tokens by slot of a workgroup's share
+__global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(const int32_t* __restrict__ slot_of, PlanLayout p,
+                                                                  int32_t* __restrict__ plan) {
+  __shared__ int hist[kMostSlots + 1];
+  for (int s = threadIdx.x; s <= p.slots; s += kPlanThreads) hist[s] = 0;
+  __syncthreads();
+  const int64_t begin = blockIdx.x * p.per_wg, end = begin + p.per_wg < p.n ? begin + p.per_wg : p.n;
+  for (int64_t i = begin + threadIdx.x; i < end; i += kPlanThreads) atomicAdd(&hist[group_of(slot_of, i, p.slots)], 1);
+  __syncthreads();
+  for (int s = threadIdx.x; s <= p.slots; s += kPlanThreads)
+    plan[p.counts + static_cast<int64_t>(blockIdx.x) * (p.slots + 1) + s] = hist[s];
+}
+
+struct Three {
+  int tokens, tiles, chunks;
+};
+__device__ __forceinline__ Three operator+(Three a, Three b) {
+  return Three{a.tokens + b.tokens, a.tiles + b.tiles, a.chunks + b.chunks};
+}
+
+__global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t* __restrict__ slot_of, PlanLayout p,
+                                                                  int32_t* __restrict__ plan) {
+  __shared__ int count[kWaves][kMostSlots + 1];   // a wave's tokens by slot, then the place of its next one
+  __shared__ Three first[kMostSlots + 2];         // a slot's first token, tile and chunk
+  __shared__ Three wave_sum[kWaves];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, groups = p.slots + 1;
+  for (int i = tid; i < kWaves * (kMostSlots + 1); i += kPlanThreads) (&count[0][0])[i] = 0;
+  __syncthreads();
+  const int64_t per_wave = p.per_wg / kWaves;
+  const int64_t begin = blockIdx.x * p.per_wg + w * per_wave, end = begin + per_wave < p.n ? begin + per_wave : p.n;
+  for (int64_t i = begin + lane; i < end; i += 64) atomicAdd(&count[w][group_of(slot_of, i, p.slots)], 1);
+  __syncthreads();
+  // a slot's total, and the place of each wave's first token among the slot's
+  const int each = (groups + kPlanThreads - 1) / kPlanThreads, s0 = tid * each;
+  Three mine{0, 0, 0};
+  for (int s = s0; s < s0 + each && s < groups; ++s) {
+    int before = 0, total = 0;
+    if (p.wgs > 1)
+      for (int b = 0; b < p.wgs; ++b) {
+        const int c = plan[p.counts + static_cast<int64_t>(b) * groups + s];
+        before += b < static_cast<int>(blockIdx.x) ? c : 0;
+        total += c;
+      }
+    for (int v = 0; v < kWaves; ++v) {
+      const int c = count[v][s];
+      count[v][s] = before;
+      before += c;
+    }
+    if (p.wgs == 1) total = before;
+    const int tiles = (total + kTile - 1) / kTile;
+    const Three own{total, tiles, s < p.slots ? (tiles + p.chunk_tiles - 1) / p.chunk_tiles : 0};
+    first[s] = mine;     // within the thread, made whole below
+    mine = mine + own;
+  }
+  Three upto = mine;     // sums over the wave's lanes up to this one
+  for (int d = 1; d < 64; d <<= 1) {
+    const Three o{__shfl_up(upto.tokens, d), __shfl_up(upto.tiles, d), __shfl_up(upto.chunks, d)};
+    if (lane >= d) upto = upto + o;
+  }
+  if (lane == 63) wave_sum[w] = upto;
+  __syncthreads();
+  Three base{upto.tokens - mine.tokens, upto.tiles - mine.tiles, upto.chunks - mine.chunks};
+  for (int v = 0; v < w; ++v) base = base + wave_sum[v];
+  for (int s = s0; s < s0 + each && s < groups; ++s) first[s] = first[s] + base;
+  if (tid == 0) {
+    Three all{0, 0, 0};
+    for (int v = 0; v < kWaves; ++v) all = all + wave_sum[v];
+    first[groups] = all;
+  }
+  __syncthreads();
+  if (blockIdx.x == 0) {
+    for (int s = tid; s <= groups; s += kPlanThreads) plan[s] = first[s].tokens;
+    for (int s = tid; s < groups; s += kPlanThreads) plan[p.slot_chunks + s] = first[s].chunks;
+    if (tid == 0)
+      *reinterpret_cast<int4*>(plan + p.info) =
+          make_int4(first[groups].tiles, first[groups].chunks, static_cast<int>(p.n), p.slots);
+  }
+  volatile int* next = count[w];
+  for (int64_t i0 = begin; i0 < end; i0 += 64) {
+    const int64_t i = i0 + lane;
+    const bool live = i < end;
+    const int g = live ? group_of(slot_of, i, p.slots) : kMostSlots + 1;
+    // the lanes with this lane's slot
+    uint64_t peers = ~0ull;
+#pragma unroll
+    for (int b = 0; b < 11; ++b) {
+      const uint64_t set = __ballot((g >> b) & 1);
+      peers &= (g >> b) & 1 ? set : ~set;
+    }
+    const int rank = __popcll(peers & ((1ull << lane) - 1));
+    const int from = live ? next[g] : 0;
+    __builtin_amdgcn_wave_barrier();   // every lane has read before the last of its peers writes
+    if (live && (peers >> lane) == 1ull) next[g] = from + rank + 1;
+    __builtin_amdgcn_wave_barrier();
+    if (!live) continue;
+    const int k = from + rank, total = first[g + 1].tokens - first[g].tokens;   // the k-th of its slot
+    const int tile = first[g].tiles + k / kTile, at = first[g].tokens + k;
+    plan[p.order + at] = static_cast<int>(i);
+    int32_t* rows = plan + p.rows + static_cast<int64_t>(tile) * kTile;
+    rows[k % kTile] = static_cast<int>(i);
+    if (k % kTile == 0) {
+      const int left = total - k;
+      reinterpret_cast<int4*>(plan + p.tiles)[tile] = make_int4(g < p.slots ? g : -1, at, left < kTile ? left : kTile, 0);
+      const int index = k / kTile, tiles = (total + kTile - 1) / kTile;
+      if (g < p.slots && index % p.chunk_tiles == 0)
+        reinterpret_cast<int4*>(plan + p.chunks)[first[g].chunks + index / p.chunk_tiles] =
+            make_int4(g, tile, tiles - index < p.chunk_tiles ? tiles - index : p.chunk_tiles,
+                      (tiles + p.chunk_tiles - 1) / p.chunk_tiles);
+    }
+    if (k == total - 1)
+      for (int j = k % kTile + 1; j < kTile; ++j) rows[j] = static_cast<int>(i);
+  }
+}
+
+// without tokens
+__global__ void plan_empty_kernel(PlanLayout p, int32_t* __restrict__ plan) {
+  for (int s = threadIdx.x; s < p.slots + 2; s += blockDim.x) plan[s] = 0;
+  for (int s = threadIdx.x; s < p.slots + 1; s += blockDim.x) plan[p.slot_chunks + s] = 0;
+  if (threadIdx.x == 0) *reinterpret_cast<int4*>(plan + p.info) = make_int4(0, 0, 0, p.slots);
+}
+
+}  // namespace
+
+hipError_t launch_adapters_plan(const int32_t* slot_of, int32_t* plan, const PlanLayout& p, hipStream_t s) {
+  if (p.n == 0) {
+    LQ_LAUNCH("adapters_plan", plan_empty_kernel, dim3(1), dim3(256), 0, s, p, plan);
+    return hipGetLastError();
+  }
+  if (p.wgs > 1)
+    LQ_LAUNCH("adapters_plan_count", plan_count_kernel, dim3(p.wgs), dim3(kPlanThreads), 0, s, slot_of, p, plan);
+  LQ_LAUNCH("adapters_plan", plan_place_kernel, dim3(p.wgs), dim3(kPlanThreads), 0, s, slot_of, p, plan);
+  return hipGetLastError();
+}
+
+}  // namespace loftq

@@ -40,6 +40,8 @@ Parity status of each function (pins live in tests/test_oracle_*.py):
   mx_quantize             pinned (every FP4 midpoint and its neighbours, scale bytes by hand,
                           round trip of representable values)
   layer_forward/backward  pinned (differences of the forward; the mask's closed forms)
+  adapters_*              pinned (one slot reduces to layer_*; differences of the forward; a plan by hand)
+  adamw_step / state_*    pinned (torch.optim.AdamW in fp64; torch's own float8 conversions)
   warm_sketch             pinned (T = 1 reduces to the cold start; a warm sketch
                           spanning a rank-r E's row space recovers the exact SVD
                           with no power iteration)
@@ -55,6 +57,8 @@ from .forward import bf16_round, qlora_forward
 from .dropout import drop_threshold, drop_scale, keep_mask, dropout
 from .mxfp4 import E2M1, mx_scale_bytes, mx_quantize, mx_values, mx_pack, mx_unpack
 from .layer import layer_forward, layer_backward
+from .adapters import adapters_plan, adapters_forward, adapters_backward
+from .adamw import adamw_clip, adamw_step, state_codes, state_values, STATE_FORMATS
 
 __all__ = [
     "nf4_codebook", "nf_codebook", "nf_delta", "norm_ppf", "nf4_midpoints", "block_absmax", "nf4_encode", "pack_nibbles",
@@ -62,5 +66,6 @@ __all__ = [
     "splitmix64_stream", "rademacher_sketch", "householder_qr", "jacobi_svd", "randomized_svd",
     "exact_svd", "lora_factors", "loftq_step", "loftq_init", "objective", "merge_adapter", "unmerge_adapter", "warm_sketch", "bf16_round", "qlora_forward",
     "drop_threshold", "drop_scale", "keep_mask", "dropout", "E2M1", "mx_scale_bytes", "mx_quantize", "mx_values", "mx_pack",
-    "mx_unpack", "layer_forward", "layer_backward",
+    "mx_unpack", "layer_forward", "layer_backward", "adapters_plan", "adapters_forward", "adapters_backward", "adamw_clip",
+    "adamw_step", "state_codes", "state_values", "STATE_FORMATS",
 ]

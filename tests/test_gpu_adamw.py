@@ -1,0 +1,293 @@
+"""The AdamW step over many tensors on the GPU against the oracle in fp64.
+
+Bars, with u = 2^-24 (a rounding to nearest in fp32).  m: two products and a sum, the decay's and the clip's
+rounding: 6 u (|b1 m| + |(1 - b1) g|).  v: the same with one product more, all terms positive: 8 u v.  p: the
+old value's product and the difference, 3 u (|p| + |d|) for a step d, and d itself, whose factors (m, the root
+of v, the bias corrections) are off by 6 u of the magnitudes of m, 4 u, and 8 u for its own operations and the 2
+ulp of its quotient: 24 u of the step with magnitudes for m.  Parameters in bf16 add half a step, 2^-8 |p|.
+8-bit states, as values: half a step of the format (2^-4 of the value for m, 2^-3 for v, or half of the smallest
+code's value; all of it for v, which does not round to zero), and the scale's and the quotient's rounding."""
+import numpy as np
+import pytest
+import torch
+
+import oracle
+
+pytestmark = pytest.mark.gpu
+U = 2.0 ** -24
+HOW = dict(lr=1e-2, beta1=0.9, beta2=0.99, eps=1e-8)
+FLOAT8 = (torch.float8_e4m3fn, torch.float8_e5m2)
+
+
+def host(t):
+    torch.cuda.synchronize()
+    return (t.float() if t.dtype in FLOAT8 else t).double().cpu().numpy()
+
+
+class Model:
+    """Tensors of the given lengths, with states after some steps."""
+
+    def __init__(self, lib, sizes, bits=32, param=torch.float32, grad=torch.float32, copies=False, seed=0, decay=0.1,
+                 lr_scale=1.0):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+
+        def normal(n, std):   # magnitudes over some binades
+            return torch.randn(n, generator=g, device="cuda") * std * torch.exp(torch.randn(n, generator=g, device="cuda"))
+
+        self.params = [normal(n, 0.1).to(param) for n in sizes]
+        self.grads = [normal(n, 0.01).to(grad) for n in sizes]
+        self.decay = [decay] * len(sizes) if not isinstance(decay, list) else decay
+        self.lr_scale = [lr_scale] * len(sizes) if not isinstance(lr_scale, list) else lr_scale
+        self.copies = [torch.zeros(n, dtype=torch.bfloat16, device="cuda") for n in sizes] if copies else None
+        states = dict(m=[normal(n, 0.01) for n in sizes], v=[normal(n, 0.01) ** 2 for n in sizes])
+        if bits == 8:
+            coded = {k: [oracle.state_codes(x.cpu().numpy(), k) for x in v] for k, v in states.items()}
+            for k, dtype in zip("mv", FLOAT8):
+                states[k] = [torch.from_numpy(c).cuda().view(dtype) for c, _ in coded[k]]
+                states[k + "_scale"] = [torch.from_numpy(s).cuda() for _, s in coded[k]]
+        self.bits = bits
+        self.tensors = lib.AdamWTensors(self.params, self.grads, copies=self.copies, weight_decay=decay,
+                                        lr_scale=lr_scale, **states)
+
+    def values(self):
+        t = self.tensors
+        out = []
+        for i, p in enumerate(self.params):
+            m, v = host(t.m[i]), host(t.v[i])
+            if self.bits == 8:
+                m, v = (oracle.state_values(x.view(torch.uint8).cpu().numpy(), s.cpu().numpy(), k)
+                        for x, s, k in ((t.m[i], t.m_scale[i], "m"), (t.v[i], t.v_scale[i], "v")))
+            out.append((host(p), host(self.grads[i]), m, v))
+        return out
+
+    def check(self, before, t, clip=1.0, **how):
+        how = dict(HOW, **how)
+        b1, b2 = how["beta1"], how["beta2"]
+        for i, ((p, g, m, v), (p1, _, m1, v1)) in enumerate(zip(before, self.values())):
+            if p.size == 0:
+                continue
+            lr = how["lr"] * float(np.float32(self.lr_scale[i]))
+            decay = float(np.float32(self.decay[i]))
+            want = oracle.adamw_step(p, g, m, v, lr, b1, b2, how["eps"], t, decay, clip)
+            size_m = abs(b1 * m) + abs((1 - b1) * clip * g)
+            root = np.sqrt(want[2] / (1 - b2 ** t)) + how["eps"]
+            d = lr / (1 - b1 ** t) * size_m / root
+            tol = 3 * U * (abs(p) + d) + 24 * U * d
+            if self.params[i].dtype == torch.bfloat16:
+                tol = tol + 2.0 ** -8 * (abs(want[0]) + tol)
+            assert np.all(abs(p1 - want[0]) <= tol), np.max(abs(p1 - want[0]) - tol)
+            if self.copies is not None:
+                assert torch.equal(self.copies[i], self.params[i].bfloat16())
+            if self.bits == 32:
+                assert np.all(abs(m1 - want[1]) <= 6 * U * size_m)
+                assert np.all(abs(v1 - want[2]) <= 8 * U * want[2])
+                continue
+            for got, ref, size, kind, scale, half in ((m1, want[1], size_m, "m", self.tensors.m_scale[i], 2.0 ** -4),
+                                                      (v1, want[2], want[2], "v", self.tensors.v_scale[i], 2.0 ** -3)):
+                codes, scales = oracle.state_codes(ref.astype(np.float32), kind)
+                s = host(scale)
+                assert np.all(abs(s - scales) <= 16 * U * np.abs(scales))
+                e, f, bias, _ = oracle.STATE_FORMATS[kind]
+                small = 2.0 ** (1 - bias - f) * np.repeat(s, 256)[:ref.size] * (1.0 if kind == "v" else 0.5)
+                assert np.all(abs(got - ref) <= np.maximum(half * abs(ref), small) + 16 * U * size)
+                # the same code, but where rounding in fp32 reaches a border: 16 u of the value against steps of
+                # 2^-3 of it or more, so one in 2^16 of them at most, and a few in such a sample
+                same = got == oracle.state_values(codes, s.astype(np.float32), kind)
+                assert (~same).sum() <= 2 + same.size // 1000
+
+
+SIZES = [[1], [3], [4], [255, 256, 257], [4096], [4095, 1, 0, 8193], [64 * 33, 70 * 64, 5]]
+
+
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("param", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("sizes", SIZES, ids=str)
+def test_step(lib, sizes, bits, param, grad):
+    m = Model(lib, sizes, bits, param, grad, seed=len(sizes) + bits)
+    for t in (1, 2, 1000):
+        before = m.values()
+        assert lib.loftq_adamw(m.tensors, t=t, **HOW) is None
+        m.check(before, t)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("max_norm", [1e-3, 1e6])
+def test_clipping_and_copies(lib, bits, max_norm):
+    m = Model(lib, [300, 5000, 64, 100000], bits, copies=True, seed=2)
+    before = m.values()
+    norm = lib.loftq_adamw(m.tensors, t=3, max_norm=max_norm, **HOW)
+    want, clip = oracle.adamw_clip([b[1] for b in before], max_norm)
+    assert abs(float(norm) - want) <= 2 * U * want
+    m.check(before, 3, clip=clip)
+
+
+def test_many_tensors(lib):
+    """More than one table's worth, of many lengths; each with its own decay and rate."""
+    sizes = [(37 * i) % 5000 + 1 for i in range(150)]
+    m = Model(lib, sizes, decay=[0.01 * (i % 3) for i in range(150)], lr_scale=[1.0 + i % 4 for i in range(150)], seed=3)
+    before = m.values()
+    norm = lib.loftq_adamw(m.tensors, t=5, max_norm=0.5, **HOW)
+    want, clip = oracle.adamw_clip([b[1] for b in before], 0.5)
+    assert abs(float(norm) - want) <= 2 * U * want
+    m.check(before, 5, clip=clip)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_from_nothing(lib, bits):
+    """New states are zeros; a zero gradient leaves them so and the parameters but for the decay."""
+    p, g = [torch.randn(700, device="cuda")], [torch.zeros(700, device="cuda")]
+    t = lib.AdamWTensors(p, g, bits=bits, weight_decay=0.5)
+    was = p[0].clone()
+    lib.loftq_adamw(t, lr=0.1)
+    assert torch.equal(p[0], was * np.float32(1 - 0.1 * 0.5))
+    assert not host(t.m[0]).any() and not host(t.v[0]).any()
+    if bits == 8:
+        assert not t.m_scale[0].any() and not t.v_scale[0].any()
+    g[0].copy_(torch.randn(700, device="cuda"))
+    was = p[0].clone()
+    lib.loftq_adamw(t, lr=0.1, t=1)
+    # the first step from nothing: m / (1 - b1) = g and sqrt(v / (1 - b2)) = |g|, so lr g / (|g| + eps), which for a
+    # gradient of 4e-5 is 2e-4 of lr less than lr
+    want = was.double() * 0.95 - 0.1 * g[0].double() / (g[0].double().abs() + 1e-8)
+    assert ((p[0] - want).abs() <= 1e-5 * (1 + want.abs())).all()
+
+
+def test_small_second_moments_do_not_vanish(lib):
+    """A block with one large gradient: the others' v is kept at the smallest code, so that a step stays a step."""
+    p, g = [torch.zeros(256, device="cuda")], [torch.full((256,), 1e-6, device="cuda")]
+    g[0][7] = 1e3
+    t = lib.AdamWTensors(p, g, bits=8)
+    lib.loftq_adamw(t, lr=0.1)
+    codes = t.v[0].view(torch.uint8)
+    assert codes[7] == 0x7B and (codes[torch.arange(256, device="cuda") != 7] == 1).all()
+    g[0].zero_()
+    was = p[0].clone()
+    for k in range(2, 6):
+        lib.loftq_adamw(t, lr=0.1, t=k)
+    assert ((p[0] - was).abs() <= 4 * 0.1 * 10).all()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_gradients_that_are_not_finite(lib, bits, bad):
+    m = Model(lib, [600, 300], bits, copies=True, seed=4)
+    m.grads[0][300] = bad
+    t = m.tensors
+    states = [t.m, t.v, m.params, m.copies] + ([t.m_scale, t.v_scale] if bits == 8 else [])
+    was = [[x.clone() for x in s] for s in states]
+    norm = lib.loftq_adamw(t, max_norm=1.0, **HOW)   # a step that is clipped changes nothing
+    assert not torch.isfinite(norm)
+    for now, old in zip(states, was):
+        assert all(torch.equal(x.view(torch.uint8), y.view(torch.uint8)) for x, y in zip(now, old))
+    lib.loftq_adamw(t, **HOW)                        # one that is not is spoilt where the formulas say
+    at = torch.arange(600, device="cuda") != 300
+    assert torch.isnan(m.params[0][300]) and torch.isfinite(m.params[0][at]).all() and torch.isfinite(m.params[1]).all()
+    if bits == 8:
+        assert torch.isnan(t.m_scale[0]).tolist() == [False, True, False] == torch.isnan(t.v_scale[0]).tolist()
+
+
+def test_step_and_rate_from_the_device(lib):
+    a, b = Model(lib, [1000, 77], seed=5), Model(lib, [1000, 77], seed=5)
+    step, factor = torch.tensor([6], device="cuda"), torch.tensor([0.25], device="cuda")
+    lib.loftq_adamw(a.tensors, t=1, step=step, lr_factor=factor, **HOW)
+    lib.loftq_adamw(b.tensors, t=7, **dict(HOW, lr=HOW["lr"] / 4))
+    for x, y in zip(a.params + a.tensors.m + a.tensors.v, b.params + b.tensors.m + b.tensors.v):
+        # the bias corrections are formed by another library's power, off by an ulp of fp64
+        assert torch.equal(x, y) or (x - y).abs().max() <= 2 * U * y.abs().max()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_captured_steps(lib, bits):
+    """A step in a graph that counts itself, replayed with eager work between, against eager steps."""
+    a, b = (Model(lib, [3000, 40, 256], bits, copies=True, seed=6) for _ in range(2))
+    step = torch.zeros(1, dtype=torch.int64, device="cuda")
+    norm = torch.empty((), device="cuda")
+
+    def train(m):
+        lib.loftq_adamw(m.tensors, t=1, step=step, max_norm=0.05, norm=norm, **HOW)
+
+    for k in range(2):   # the capture's warm-up, on both
+        step.fill_(k)
+        train(a), train(b)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        train(a)
+        step.add_(1)
+    step.fill_(2)
+    for k in range(2, 6):
+        for x, y in zip(a.grads, b.grads):
+            x.copy_(torch.randn_like(x) * 0.01)
+            y.copy_(x)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert step.item() == k + 1
+        got = norm.clone()
+        step.fill_(k)
+        train(b)
+        step.fill_(k + 1)
+        assert torch.equal(got, norm)
+        for x, y in zip(a.params + a.copies + a.tensors.m + a.tensors.v, b.params + b.copies + b.tensors.m + b.tensors.v):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_nothing_behind_the_tensors_is_touched(lib):
+    for bits in (32, 8):
+        sizes = [257, 5, 4099]
+        want = Model(lib, sizes, bits, copies=True, seed=7)
+        m = Model(lib, sizes, bits, copies=True, seed=7)
+        t = m.tensors
+        fences, lists = [], dict(params=m.params, grads=m.grads, m=t.m, v=t.v, copies=m.copies)
+        if bits == 8:
+            lists.update(m_scale=t.m_scale, v_scale=t.v_scale)
+        moved = {}
+        for k, ts in lists.items():
+            moved[k] = []
+            for x in ts:
+                raw = x.view(torch.uint8)
+                big = torch.full((raw.numel() + 4096,), 255, dtype=torch.uint8, device="cuda")
+                big[: raw.numel()] = raw
+                moved[k].append(big[: raw.numel()].view(x.dtype))
+                fences.append(big[raw.numel():])
+        fenced = lib.AdamWTensors(moved.pop("params"), moved.pop("grads"), weight_decay=0.1, **moved)
+        for tensors in (want.tensors, fenced):
+            lib.loftq_adamw(tensors, t=2, max_norm=0.01, **HOW)
+        torch.cuda.synchronize()
+        assert all((f == 255).all() for f in fences)
+        for x, y in zip(fenced.params + fenced.m + fenced.v + fenced.copies,
+                        want.params + want.tensors.m + want.tensors.v + want.copies):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_on_another_stream(lib):
+    a, b = Model(lib, [100000, 33], seed=8), Model(lib, [100000, 33], seed=8)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    norm = lib.loftq_adamw(a.tensors, t=2, max_norm=0.1, stream=side, **HOW)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(norm, lib.loftq_adamw(b.tensors, t=2, max_norm=0.1, **HOW))
+    assert all(torch.equal(x, y) for x, y in zip(a.params, b.params))
+
+
+def test_binding_checks(lib):
+    p, g = [torch.zeros(8, device="cuda")], [torch.zeros(8, device="cuda")]
+    with pytest.raises(ValueError):
+        lib.AdamWTensors([], [])
+    with pytest.raises(ValueError):
+        lib.AdamWTensors(p, [torch.zeros(9, device="cuda")])
+    with pytest.raises(TypeError):
+        lib.AdamWTensors(p, [torch.zeros(8, dtype=torch.float16, device="cuda")])
+    with pytest.raises(TypeError):
+        lib.AdamWTensors(p, g, copies=[torch.zeros(8, device="cuda")])
+    with pytest.raises(lib.LoftqError):
+        lib.AdamWTensors(p, g, bits=4)
+    with pytest.raises(ValueError):
+        lib.AdamWTensors(p, g, weight_decay=[0.1, 0.2])
+    with pytest.raises(ValueError):
+        lib.AdamWTensors([torch.zeros(8)], g)
+    t = lib.AdamWTensors(p, g)
+    for how in (dict(t=0), dict(eps=0.0), dict(beta1=1.0), dict(beta2=-0.1), dict(lr=-1.0), dict(lr=float("nan")),
+                dict(max_norm=-1.0), dict(max_norm=float("inf")), dict(norm=torch.zeros((), device="cuda"))):
+        with pytest.raises(lib.LoftqError):
+            lib.loftq_adamw(t, **{"lr": 0.1, **how})
