@@ -19,6 +19,7 @@ struct PlanLayout {
   int64_t rows;         // [max_tiles][kTile]: a tile's tokens, the slot's last one again past them
   int64_t chunks;       // [max_chunks][4]: slot, first tile, tiles, chunks of the slot
   int64_t slot_chunks;  // [slots + 1]: a slot's first chunk
+  int64_t slot_used;    // [slots + 1]: slots with tokens before a slot
   int64_t counts;       // [plan_wgs][slots + 1]: tokens by workgroup and slot (more than one workgroup)
   int64_t words;
   int64_t max_tiles, max_chunks;
@@ -49,7 +50,8 @@ inline PlanLayout plan_layout(int64_t n, int slots) {
   p.rows = p.tiles + 4 * p.max_tiles;
   p.chunks = p.rows + kTile * p.max_tiles;
   p.slot_chunks = p.chunks + 4 * p.max_chunks;
-  p.counts = p.slot_chunks + pad(slots + 1);
+  p.slot_used = p.slot_chunks + pad(slots + 1);
+  p.counts = p.slot_used + pad(slots + 1);
   p.words = p.counts + (p.wgs > 1 ? pad(static_cast<int64_t>(p.wgs) * (slots + 1)) : 0);
   return p;
 }
@@ -63,11 +65,12 @@ struct PlanView {
   const int32_t* rows;
   const int4* chunks;
   const int32_t* slot_chunks;
+  const int32_t* slot_used;
   int32_t n, slots, max_tiles, max_chunks;
 };
 inline PlanView plan_view(const int32_t* plan, const PlanLayout& p) {
   return PlanView{plan + p.info, reinterpret_cast<const int4*>(plan + p.tiles), plan + p.rows,
-                  reinterpret_cast<const int4*>(plan + p.chunks), plan + p.slot_chunks, static_cast<int32_t>(p.n),
+                  reinterpret_cast<const int4*>(plan + p.chunks), plan + p.slot_chunks, plan + p.slot_used, static_cast<int32_t>(p.n),
                   static_cast<int32_t>(p.slots), static_cast<int32_t>(p.max_tiles), static_cast<int32_t>(p.max_chunks)};
 }
 
@@ -81,25 +84,43 @@ struct Pool {
   float gain;            // alpha times dropout's scale
 };
 
+// Slots with tokens that a batch may have: the slots of the factors' prepared forms.
+inline int64_t used_slots(int64_t n, int slots) { return n < slots ? n : slots; }
+
+// Forms of a pool's factors in bf16 that the products read, for the slots with tokens, one after another.  Ranks
+// past a slot's own are zeros.  Null where not wanted.
+struct Prepare {
+  __bf16* Bp;      // [used][rows][rp]
+  __bf16* Bt;      // [used][rp][rows8]: zeros past `rows`
+  __bf16* Ab;      // [used][rp][cols]
+  __bf16* At;      // [used][cols][rp]
+  int64_t rows, rows8, cols;
+  unsigned wgs;    // a slot's workgroups, set by the launcher
+};
+hipError_t launch_adapters_prepare(Prepare p, const PlanView& plan, const Pool& pool, hipStream_t s);
+
 // P = keep(L) F^T over the tokens of each tile, as partial sums over `ks` K ranges [ks][max_tiles 64][rp].  L has K
-// columns (8 | K).  Of the pool's factors A is read along its rows, B (for L = dY) along its columns, whose `rows`
-// may be fewer than K.
+// columns (8 | K), F a row of K elements for each rank, slot after slot.
 struct AdapterDown {
   const __bf16* L;       // null: no such job
-  int64_t K, rows;
+  int64_t K;
+  const void* F;         // of the launch's type
+  int64_t slot_elems;    // elements from slot to slot
+  bool prepared;         // one of Prepare's forms: its slots are the ones with tokens
   float* out;
   int ks;
   unsigned wgs;          // set by the launcher
   DropArg drop;
 };
-int adapters_down_splits(int64_t n, int slots, int64_t K);
-// at least adapters_down_splits(m, ...) times the plan's max_tiles for every m <= n
-int64_t adapters_down_tiles_bound(int64_t n, int slots, int64_t K);
-// job[0]: over B (its L is dY), job[1]: over A
+int adapters_down_splits(int64_t n, int slots, int64_t K, int rp);
+// at least the partials of every call of up to n tokens and of rank up to rp
+int64_t adapters_down_floats_bound(int64_t n, int slots, int64_t K, int rp);
 struct AdapterDownJobs {
   AdapterDown job[2];
 };
-hipError_t launch_adapters_down(AdapterDownJobs jobs, const PlanView& plan, const Pool& pool, hipStream_t s);
+// with the forms of `prepare` in the same launch (they are for the launch after it)
+hipError_t launch_adapters_down(AdapterDownJobs jobs, loftq_dtype_t factor, const Prepare& prepare, const PlanView& plan,
+                                const Pool& pool, hipStream_t s);
 
 // The partials in range order: their sum (fp32, [max_tiles 64][rp]) and as three bf16 pieces rank-major
 // [3][rp][max_tiles 64], zeros past a tile's tokens.  Either may be null.
@@ -114,17 +135,18 @@ struct AdapterSumJobs {
 };
 hipError_t launch_adapters_sum(AdapterSumJobs jobs, const PlanView& plan, int rp, hipStream_t s);
 
-// out = in + gain keep(H F): H the partial sums of `ks` ranges, F the pool's B (features = its rows) or A
-// (`over_a`, features = its columns).
+// out = in + gain keep(H F^T): H the partial sums of `ks` ranges, F [slot][features][ld] in bf16.
 struct AdapterUp {
   const float* H;
   int ks;
   int64_t features;
+  const __bf16* F;
+  int64_t ld;            // 8 | ld
+  bool prepared;
   const void* in;        // or null
   void* out;
   loftq_dtype_t odt;
-  bool over_a;
-  DropArg drop;          // thr != 0 only over A
+  DropArg drop;          // thr != 0: 4 | features
 };
 hipError_t launch_adapters_up(const AdapterUp& u, const PlanView& plan, const Pool& pool, hipStream_t s);
 

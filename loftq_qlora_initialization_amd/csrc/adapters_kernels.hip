@@ -10,6 +10,8 @@
 #include "adapters.h"
 #include "buffer.h"
 
+#include <type_traits>
+
 namespace loftq {
 namespace {
 
@@ -49,11 +51,10 @@ struct TileInfo {
   int slot, count;
 };
 __device__ __forceinline__ TileInfo tile_info(const PlanView& p, int tile) {
-  const int4 info = *reinterpret_cast<const int4*>(p.info);
-  const bool ours = info.z == p.n && info.w == p.slots;
-  if (!ours || tile >= info.x) return TileInfo{-2, 0};
-  const int4 t = p.tiles[tile];
-  return TileInfo{t.x >= p.slots ? -2 : t.x, t.z < 0 ? 0 : (t.z > kTile ? kTile : t.z)};
+  const int4 info = *reinterpret_cast<const int4*>(p.info), t = p.tiles[tile];   // neither load waits for the other
+  const bool ours = info.z == p.n && info.w == p.slots && tile < info.x && t.x < p.slots;
+  const int count = t.z < 0 ? 0 : (t.z > kTile ? kTile : t.z);
+  return TileInfo{__builtin_amdgcn_readfirstlane(ours ? t.x : -2), __builtin_amdgcn_readfirstlane(ours ? count : 0)};
 }
 __device__ __forceinline__ int64_t token_at(const PlanView& p, int64_t place) {
   const int t = p.rows[place];
@@ -65,166 +66,249 @@ __device__ __forceinline__ int slot_rank(const Pool& pool, int slot) {
   return r < 0 ? 0 : (r > pool.rank ? pool.rank : r);
 }
 
-// Eight elements of a factor for consecutive ranks or columns, as bf16.
+// Eight elements of a factor in a row, as they lie and as bf16.
 template <typename F>
 struct Factor;
 template <>
 struct Factor<__bf16> {
   static constexpr uint32_t kSize = 2;
-  static __device__ __forceinline__ u32x4 run(__amdgpu_buffer_rsrc_t b, uint32_t at) {   // eight in a row
-    return __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0);
+  typedef u32x4 raw_t;
+  static __device__ __forceinline__ raw_t load(__amdgpu_buffer_rsrc_t b, uint32_t at, int more) {
+    return __builtin_amdgcn_raw_buffer_load_b128(b, at, more, 0);
   }
-  static __device__ __forceinline__ u32x4 strided(__amdgpu_buffer_rsrc_t b, const uint32_t (&at)[8]) {
-    u32x4 v;
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      v[j] = static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b16(b, at[2 * j], 0, 0)) |
-             static_cast<uint32_t>(__builtin_amdgcn_raw_buffer_load_b16(b, at[2 * j + 1], 0, 0)) << 16;
-    return v;
-  }
+  static __device__ __forceinline__ u32x4 bf16(raw_t v) { return v; }
 };
 template <>
 struct Factor<float> {
   static constexpr uint32_t kSize = 4;
-  static __device__ __forceinline__ u32x4 round8(const float (&x)[8]) {
+  struct raw_t {
+    u32x4 lo, hi;
+  };
+  static __device__ __forceinline__ raw_t load(__amdgpu_buffer_rsrc_t b, uint32_t at, int more) {
+    return raw_t{__builtin_amdgcn_raw_buffer_load_b128(b, at, more, 0), __builtin_amdgcn_raw_buffer_load_b128(b, at, more + 16, 0)};
+  }
+  static __device__ __forceinline__ u32x4 bf16(raw_t v) {
     bf16x8 o;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = static_cast<__bf16>(x[j]);
+    for (int j = 0; j < 8; ++j) o[j] = static_cast<__bf16>(__uint_as_float(j < 4 ? v.lo[j & 3] : v.hi[j & 3]));
     return __builtin_bit_cast(u32x4, o);
-  }
-  static __device__ __forceinline__ u32x4 run(__amdgpu_buffer_rsrc_t b, uint32_t at) {
-    const u32x4 lo = __builtin_amdgcn_raw_buffer_load_b128(b, at, 0, 0);
-    const u32x4 hi = __builtin_amdgcn_raw_buffer_load_b128(b, at == kNowhere ? at : at + 16, 0, 0);
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(j < 4 ? lo[j & 3] : hi[j & 3]);
-    return round8(x);
-  }
-  static __device__ __forceinline__ u32x4 strided(__amdgpu_buffer_rsrc_t b, const uint32_t (&at)[8]) {
-    float x[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(b, at[j], 0, 0));
-    return round8(x);
   }
 };
 
-// ---- thin product over the features: a K range's part of keep(L) F^T ----
-// A workgroup takes half a tile (32 tokens) and one range, which its eight waves share U steps of
-// 32 at a time.  All loads of U steps are issued before the first product.  The waves' sums meet
-// in LDS.
-constexpr int kDownThreads = 512, kDownWaves = kDownThreads / 64;
+// The place of a slot among those with tokens.
+__device__ __forceinline__ int64_t used_place(const PlanView& p, int slot) {
+  const int u = p.slot_used[slot];
+  return u < 0 ? 0 : (u < p.slots ? (u < p.n ? u : p.n - 1) : 0);
+}
 
-template <int NT, typename F, bool kOverB>
-__device__ __forceinline__ void down_job(const AdapterDown& jb, uint32_t wg, const PlanView& plan, const Pool& pool,
-                                         float (*part)[2 * NT * 4 * 64]) {
-  constexpr int U = NT <= 2 ? 4 : 2;
+constexpr int kThreads = 256, kDownThreads = 512, kDownWaves = kDownThreads / 64;
+
+// ---- the factors' forms for the products, eight elements a thread ----
+// Element j of the eight at `at`, `stride` elements apart, zero where j >= live: every load in flight at once.
+template <typename T>
+__device__ __forceinline__ bf16x8 pool_eight(const T* f, int64_t at, int64_t stride, int live) {
+  T x[8];
+  if (stride == 1 && live >= 8 && at % 8 == 0) {   // 16-byte loads
+    typedef T eight __attribute__((ext_vector_type(8)));
+    const eight v = *reinterpret_cast<const eight*>(f + at);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) x[j] = f[at + (j < live ? j * stride : 0)];   // past them the first again
+  }
+  bf16x8 o;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o[j] = static_cast<__bf16>(j < live ? static_cast<float>(x[j]) : 0.f);
+  return o;
+}
+template <typename T>
+__device__ __forceinline__ void prepare_slot(const Prepare& q, int64_t i, int slot, int64_t place, const Pool& pool) {
+  const int64_t rows = q.rows, cols = q.cols;
+  const int R = pool.rank, r = slot_rank(pool, slot), rp = pool.rp, groups = rp / 8;
+  const T* B = static_cast<const T*>(pool.B) + slot * (rows * R);
+  const T* A = static_cast<const T*>(pool.A) + slot * (R * cols);
+  const bf16x8 zero = {};
+  if (q.Bp != nullptr) {
+    if (i < rows * groups) {
+      const int64_t row = i / groups;
+      const int e = static_cast<int>(i % groups) * 8;
+      *reinterpret_cast<bf16x8*>(q.Bp + (place * rows + row) * rp + e) = e < r ? pool_eight(B, row * R + e, 1, r - e) : zero;
+      return;
+    }
+    i -= rows * groups;
+  }
+  if (q.Bt != nullptr) {   // neighbouring threads take neighbouring ranks, whose reads are one run
+    if (i < q.rows8 / 8 * rp) {
+      const int e = static_cast<int>(i % rp);
+      const int64_t row = i / rp * 8;
+      *reinterpret_cast<bf16x8*>(q.Bt + (place * rp + e) * q.rows8 + row) =
+          e < r ? pool_eight(B, row * R + e, R, static_cast<int>(rows - row)) : zero;
+      return;
+    }
+    i -= q.rows8 / 8 * rp;
+  }
+  if (q.Ab != nullptr) {
+    if (i < cols / 8 * rp) {
+      const int64_t e = i / (cols / 8), c = i % (cols / 8) * 8;
+      *reinterpret_cast<bf16x8*>(q.Ab + (place * rp + e) * cols + c) = e < r ? pool_eight(A, e * cols + c, 1, 8) : zero;
+      return;
+    }
+    i -= cols / 8 * rp;
+  }
+  if (q.At != nullptr && i < cols * groups) {   // neighbouring threads take neighbouring columns
+    const int64_t c = i % cols;
+    const int e = static_cast<int>(i / cols) * 8;
+    *reinterpret_cast<bf16x8*>(q.At + (place * cols + c) * rp + e) = e < r ? pool_eight(A, e * cols + c, cols, r - e) : zero;
+  }
+}
+__device__ __forceinline__ void prepare_job(const Prepare& q, uint32_t wg, int threads, const PlanView& plan, const Pool& pool) {
+  const int slot = wg / q.wgs;
+  const int4 info = *reinterpret_cast<const int4*>(plan.info);
+  if (info.z != plan.n || info.w != plan.slots || plan.slot_used[slot + 1] == plan.slot_used[slot]) return;
+  const int64_t i = static_cast<int64_t>(wg % q.wgs) * threads + threadIdx.x, place = used_place(plan, slot);
+  if (pool.dt == LOFTQ_BF16) prepare_slot<__bf16>(q, i, slot, place, pool);
+  else prepare_slot<float>(q, i, slot, place, pool);
+}
+__global__ __launch_bounds__(kThreads) void prepare_kernel(Prepare q, PlanView plan, Pool pool) {
+  prepare_job(q, blockIdx.x, kThreads, plan, pool);
+}
+
+// ---- thin product over the features: a K range's part of keep(L) F^T ----
+// A workgroup takes a tile and one range, which its eight waves share in runs of D steps of 32, D steps'
+// loads in flight all the time.  A wave multiplies all of the tile's tokens: what bounds it is the
+// number of loads, and a row of F serves 64 tokens so (16 tokens a wave, each with its own loads of F: 54
+// instead of 38 us at 2048 tokens of 11008 + 4096 columns, rank 64).  The waves' sums meet in LDS.
+template <int NT, int MT, typename F, bool kWide>
+__device__ __forceinline__ void down_job(const AdapterDown& jb, int tile, int q, const TileInfo& t, const PlanView& plan,
+                                         const Pool& pool, float* part) {
+  constexpr int D = MT == 4 ? 2 : 4;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), li = lane & 15, lg = lane >> 4;
-  const int q = wg % jb.ks, half = wg / jb.ks % 2, tile = wg / jb.ks / 2;
-  const TileInfo t = tile_info(plan, tile);
-  if (t.slot < 0 || half * 32 >= t.count) return;
-  const int64_t K = jb.K, place = static_cast<int64_t>(tile) * kTile + half * 32;
+  const int64_t K = jb.K, place = static_cast<int64_t>(tile) * kTile;
   const int steps = static_cast<int>((K + 31) / 32), per = (steps + jb.ks - 1) / jb.ks;
   const int begin = q * per, end = begin + per < steps ? begin + per : steps;
-  const int r = slot_rank(pool, t.slot), R = pool.rank;
-  const uint32_t thr = kOverB ? 0 : jb.drop.thr;
+  const int r = slot_rank(pool, t.slot), width = static_cast<int>(K);
+  const uint32_t thr = jb.drop.thr;
   const uint64_t key = thr != 0 ? drop_key(jb.drop) : 0;
-  const __bf16* row[2];
-  uint64_t element[2];
+  const char* base = static_cast<const char*>(jb.F) + (jb.prepared ? used_place(plan, t.slot) : t.slot) * jb.slot_elems * Factor<F>::kSize;
+  const int l_records = records_of(static_cast<int64_t>(plan.n) * K * 2), f_records = records_of(r * K * Factor<F>::kSize);
+  int64_t row[MT];         // this lane's first element of a token
+  uint32_t offset[MT];     // in bytes, of a tensor of less than 2^31
+  uint64_t word[MT];       // of the mask: the generator's state there
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    const int64_t token = token_at(plan, place + 16 * m + li);
-    row[m] = jb.L + token * K;
-    element[m] = static_cast<uint64_t>(token * K);
+  for (int m = 0; m < MT; ++m) {
+    row[m] = token_at(plan, place + 16 * m + li) * K + 8 * lg;
+    offset[m] = 16 * m + li < t.count ? static_cast<uint32_t>(row[m]) * 2 : kNowhere;
+    word[m] = key + ((static_cast<uint64_t>(row[m]) >> 2) + 1) * kMixGamma;
   }
-  // A: rank p's row is K columns (records end with the slot's rank); B: column p of `rows` rows
-  const int64_t slot_elems = kOverB ? jb.rows * R : static_cast<int64_t>(R) * K;
-  const char* base = static_cast<const char*>(kOverB ? pool.B : pool.A) + t.slot * slot_elems * Factor<F>::kSize;
-  const __amdgpu_buffer_rsrc_t rsrc = buffer_of(base, (kOverB ? slot_elems : r * K) * Factor<F>::kSize);
-  f32x4 acc[2][NT];
+  uint32_t fat[NT];
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int p = 0; p < NT; ++p) fat[p] = static_cast<uint32_t>((16 * p + li) * K + 8 * lg) * Factor<F>::kSize;
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int p = 0; p < NT; ++p) acc[m][p] = f32x4{0.f, 0.f, 0.f, 0.f};
-  for (int s0 = begin + w * U; s0 < end; s0 += kDownWaves * U) {
-    u32x4 x[U][2], b[U][NT];
+  u32x4 x[D][MT];
+  typename Factor<F>::raw_t f[D][NT];
+  auto load = [&](int set, int step) __attribute__((always_inline)) {
+    const int k0 = step * 32;
+    const bool any = step < end, live = k0 + 8 * lg < width;
+    const __amdgpu_buffer_rsrc_t fb = buffer_with(base, any ? f_records : 0);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int k = (s0 + u) * 32 + 8 * lg;
-      const bool live = s0 + u < end && k < K;
+    for (int p = 0; p < NT; ++p) f[set][p] = Factor<F>::load(fb, live ? fat[p] : kNowhere, k0 * static_cast<int>(Factor<F>::kSize));
+    if constexpr (kWide) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        x[u][m] = u32x4{0u, 0u, 0u, 0u};
-        if (live) x[u][m] = *reinterpret_cast<const u32x4*>(row[m] + k);
+      for (int m = 0; m < MT; ++m) {
+        x[set][m] = u32x4{0u, 0u, 0u, 0u};
+        if (any && live && 16 * m + li < t.count) x[set][m] = *reinterpret_cast<const u32x4*>(jb.L + row[m] + k0);
       }
+    } else {
+      const __amdgpu_buffer_rsrc_t xb = buffer_with(jb.L, any ? l_records : 0);
 #pragma unroll
-      for (int p = 0; p < NT; ++p) {
-        const int rank = 16 * p + li;
-        if constexpr (kOverB) {
-          uint32_t at[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) at[j] = live && rank < r ? static_cast<uint32_t>((k + j) * R + rank) * Factor<F>::kSize : kNowhere;
-          b[u][p] = Factor<F>::strided(rsrc, at);
-        } else {
-          b[u][p] = Factor<F>::run(rsrc, live ? static_cast<uint32_t>(rank * K + k) * Factor<F>::kSize : kNowhere);
-        }
-      }
+      for (int m = 0; m < MT; ++m) x[set][m] = __builtin_amdgcn_raw_buffer_load_b128(xb, live ? offset[m] : kNowhere, k0 * 2, 0);
     }
+    __builtin_amdgcn_sched_barrier(0);   // steps in the order in which they are waited for
+  };
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+  for (int d = 0; d < D; ++d) load(d, begin + w * D + d);
+  for (int s0 = begin + w * D; s0 < end; s0 += kDownWaves * D) {
 #pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        u32x4 v = x[u][m];
-        if (thr != 0) v = drop8(v, key, element[m] + static_cast<uint64_t>((s0 + u) * 32 + 8 * lg), thr);
+    for (int d = 0; d < D; ++d) {
+      u32x4 b[NT];
 #pragma unroll
-        for (int p = 0; p < NT; ++p) acc[m][p] = mfma16(v, b[u][p], acc[m][p]);
+      for (int p = 0; p < NT; ++p) b[p] = Factor<F>::bf16(f[d][p]);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        u32x4 v = x[d][m];
+        if (thr != 0) {   // eight words of the mask a step
+          const uint64_t z = word[m] + static_cast<uint64_t>(s0 + d) * (8 * kMixGamma);
+          const uint64_t w0 = mix64(z), w1 = mix64(z + kMixGamma);
+          v[0] = drop_pair(v[0], w0, 0, thr);
+          v[1] = drop_pair(v[1], w0, 2, thr);
+          v[2] = drop_pair(v[2], w1, 0, thr);
+          v[3] = drop_pair(v[3], w1, 2, thr);
+        }
+#pragma unroll
+        for (int p = 0; p < NT; ++p) acc[m][p] = mfma16(v, b[p], acc[m][p]);
       }
+      __builtin_amdgcn_sched_barrier(0);
+      load(d, s0 + d + kDownWaves * D);
+    }
   }
   // the upper half of the waves parks its sums and the lower half adds them, until one is left
-  auto at = [&](int m, int p, int v) { return ((m * NT + p) * 4 + v) * 64 + lane; };
+  auto at = [&](int wave, int m, int p, int v) { return (((wave * MT + m) * NT + p) * 4 + v) * 64 + lane; };
 #pragma unroll
   for (int left = kDownWaves / 2; left >= 1; left /= 2) {
     if (w >= left && w < 2 * left)
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int p = 0; p < NT; ++p)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) part[w - left][at(m, p, v)] = acc[m][p][v];
+          for (int v = 0; v < 4; ++v) part[at(w - left, m, p, v)] = acc[m][p][v];
     __syncthreads();
     if (w < left)
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int p = 0; p < NT; ++p)
 #pragma unroll
-          for (int v = 0; v < 4; ++v) acc[m][p][v] += part[w][at(m, p, v)];
+          for (int v = 0; v < 4; ++v) acc[m][p][v] += part[at(w, m, p, v)];
     __syncthreads();
   }
   if (w > 0) return;
   float* out = jb.out + (static_cast<int64_t>(q) * plan.max_tiles * kTile + place) * (16 * NT);
 #pragma unroll
-  for (int m = 0; m < 2; ++m)
+  for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int p = 0; p < NT; ++p)
 #pragma unroll
       for (int v = 0; v < 4; ++v) {
         const int tok = 16 * m + 4 * lg + v;
-        if (half * 32 + tok < t.count) out[tok * (16 * NT) + 16 * p + li] = acc[m][p][v];
+        if (tok < t.count) out[tok * (16 * NT) + 16 * p + li] = acc[m][p][v];
       }
 }
 
-template <int NT, typename F>
-__global__ __launch_bounds__(kDownThreads) void down_kernel(AdapterDownJobs jobs, PlanView plan, Pool pool) {
-  __shared__ float part[kDownWaves / 2][2 * NT * 4 * 64];
-  if (blockIdx.x < jobs.job[0].wgs)
-    down_job<NT, F, true>(jobs.job[0], blockIdx.x, plan, pool, part);
-  else
-    down_job<NT, F, false>(jobs.job[1], blockIdx.x - jobs.job[0].wgs, plan, pool, part);
+template <int NT, typename F, bool kWide>
+__global__ __launch_bounds__(kDownThreads) void down_kernel(AdapterDownJobs jobs, Prepare prepare, PlanView plan, Pool pool) {
+  __shared__ float part[kDownWaves / 2 * 4 * NT * 4 * 64];
+  uint32_t wg = blockIdx.x;
+  const int which = wg < jobs.job[0].wgs ? 0 : 1;
+  if (which == 1) wg -= jobs.job[0].wgs;
+  const AdapterDown& jb = jobs.job[which];
+  if (wg >= jb.wgs) {
+    prepare_job(prepare, wg - jb.wgs, kDownThreads, plan, pool);
+    return;
+  }
+  const int q = wg % jb.ks, tile = wg / jb.ks;
+  const TileInfo t = tile_info(plan, tile);
+  if (t.slot < 0 || t.count == 0) return;
+  if (t.count <= 16) down_job<NT, 1, F, kWide>(jb, tile, q, t, plan, pool, part);
+  else down_job<NT, 4, F, kWide>(jb, tile, q, t, plan, pool, part);
 }
 
 // ---- the sum of the partials, and its pieces rank-major ----
-constexpr int kThreads = 256;
-
 __global__ __launch_bounds__(kThreads) void sum_kernel(AdapterSumJobs jobs, PlanView plan, int rp) {
   __shared__ __align__(4) __bf16 turned[3 * 16][32 + 2];
   const AdapterSum& jb = jobs.job[blockIdx.y];
@@ -239,7 +323,18 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(AdapterSumJobs jobs, Plan
     const int tok = i / 16, p = p0 + i % 16;
     float x = 0.f;
     if (half * 32 + tok < t.count)
-      for (int q = 0; q < jb.ks; ++q) x += jb.partials[(q * places + place + tok) * rp + p];
+    {
+      const float* src = jb.partials + (place + tok) * rp + p;
+      int q = 0;
+      for (; q + 4 <= jb.ks; q += 4) {   // four loads in flight, added in order
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = src[(q + e) * places * rp];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x += v[e];
+      }
+      for (; q < jb.ks; ++q) x += src[q * places * rp];
+    }
     if (jb.sum != nullptr) jb.sum[(place + tok) * rp + p] = x;
     if (jb.St != nullptr) {
       __bf16 h[3];
@@ -258,103 +353,28 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(AdapterSumJobs jobs, Plan
 }
 
 // ---- thin product over the ranks, with the addition ----
-// A workgroup takes a tile and 256 features, 64 a wave.  The factor is the first operand; its rows
-// are dealt to the four matrix tiles of a wave so that a lane receives 16 consecutive features of a
-// token (tile a, element v of lane group g: feature 16 g + 4 a + v): whole lines of Y0 and Y a
-// token.  The partial sums of H are added while they are staged in LDS in three bf16 pieces.
-template <typename O, typename F, int KR, bool kVec, bool kOverA>
-__global__ __launch_bounds__(kThreads) void up_kernel(AdapterUp u, PlanView plan, Pool pool, unsigned blocks) {
-  constexpr int kLd = 32 * KR + 8;   // 16 bytes past whole 64: 16 rows read at one rank meet every bank once
-  constexpr int kPer = 16 / static_cast<int>(sizeof(O)), kPieces = 16 / kPer;
-  typedef O piece_t __attribute__((ext_vector_type(kPer)));
-  __shared__ __align__(16) __bf16 hs[3][kTile][kLd];
-  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, li = lane & 15, lg = lane >> 4;
-  const int tile = blockIdx.x / blocks;
-  const TileInfo t = tile_info(plan, tile);
-  if (t.slot == -2 || (t.slot == -1 && u.in == u.out)) return;
-  const int64_t N = u.features, n0 = static_cast<int64_t>(blockIdx.x % blocks) * 256 + w * 64, f0 = n0 + 16 * lg;
-  const int64_t place = static_cast<int64_t>(tile) * kTile;
-  const O* in = static_cast<const O*>(u.in);
-  O* out = static_cast<O*>(u.out);
-
-  f32x4 acc[4];   // of one 16-token group
-  // y = in + g acc (acc where the mask keeps), or a copy of `in`
-  auto store = [&](int m, bool adapter, float g, uint64_t key) __attribute__((always_inline)) {
-    if (16 * m + li >= t.count) return;
-    const int64_t at = token_at(plan, place + 16 * m + li) * N + f0;
-    float y[16];
-#pragma unroll
-    for (int c = 0; c < kPieces; ++c) {
-      if constexpr (kVec) {
-        piece_t v = {};
-        if (in != nullptr && f0 + c * kPer < N) v = *reinterpret_cast<const piece_t*>(in + at + c * kPer);
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) y[c * kPer + j] = static_cast<float>(v[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          y[c * kPer + j] = in != nullptr && f0 + c * kPer + j < N ? static_cast<float>(in[at + c * kPer + j]) : 0.f;
-      }
-    }
-    if (adapter)
-#pragma unroll
-      for (int a = 0; a < 4; ++a) {
-        const uint64_t word = kOverA && u.drop.thr != 0 ? drop_word(key, static_cast<uint64_t>(at + 4 * a) >> 2) : ~0ull;
-#pragma unroll
-        for (int v = 0; v < 4; ++v)
-          if (!kOverA || drop_keeps(word, v, u.drop.thr)) y[4 * a + v] = fmaf(g, acc[a][v], y[4 * a + v]);
-      }
-#pragma unroll
-    for (int c = 0; c < kPieces; ++c) {
-      if constexpr (kVec) {
-        piece_t v;
-#pragma unroll
-        for (int j = 0; j < kPer; ++j) v[j] = static_cast<O>(y[c * kPer + j]);
-        if (f0 + c * kPer < N) *reinterpret_cast<piece_t*>(out + at + c * kPer) = v;
-      } else {
-#pragma unroll
-        for (int j = 0; j < kPer; ++j)
-          if (f0 + c * kPer + j < N) out[at + c * kPer + j] = static_cast<O>(y[c * kPer + j]);
-      }
-    }
-  };
-  if (t.slot < 0) {
-    for (int m = 0; 16 * m < t.count; ++m) store(m, false, 0.f, 0);
-    return;
-  }
-
-  // the factor's operands: rank 32 k + 8 lg + j of feature n0 + 16 (li / 4) + 4 a + li % 4
-  const int r = slot_rank(pool, t.slot), R = pool.rank;
-  const char* base = static_cast<const char*>(kOverA ? pool.A : pool.B) + t.slot * (N * R) * Factor<F>::kSize;
-  const __amdgpu_buffer_rsrc_t rsrc = buffer_of(base, N * R * Factor<F>::kSize);
-  u32x4 f[4][KR];
-#pragma unroll
-  for (int a = 0; a < 4; ++a)
-#pragma unroll
-    for (int k = 0; k < KR; ++k) {
-      const int64_t n = n0 + 16 * (li >> 2) + 4 * a + (li & 3);
-      const int p = 32 * k + 8 * lg;
-      if (!kOverA && R % 8 == 0 && r == R) {
-        f[a][k] = Factor<F>::run(rsrc, n < N && p < R ? static_cast<uint32_t>(n * R + p) * Factor<F>::kSize : kNowhere);
-      } else {
-        uint32_t at[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          at[j] = n < N && p + j < r
-                      ? static_cast<uint32_t>(kOverA ? static_cast<int64_t>(p + j) * N + n : n * R + p + j) * Factor<F>::kSize
-                      : kNowhere;
-        f[a][k] = Factor<F>::strided(rsrc, at);
-      }
-    }
-
-  const int rp = pool.rp;
+// A workgroup takes a tile and a run of blocks of 64 features, which its four waves share.  The partial
+// sums of H are added while they are staged in LDS in three bf16 pieces.  The factor is the first
+// operand, so a lane receives four consecutive features of a token.
+template <int KR, int G>
+__device__ __forceinline__ void stage_pieces(const AdapterUp& u, const PlanView& plan, int64_t place, int count, int r, int rp,
+                                             __bf16 (*hs)[kTile][32 * KR + 8]) {
   const int64_t places = static_cast<int64_t>(plan.max_tiles) * kTile;
-  for (int i = tid; i < kTile * 8 * KR; i += kThreads) {   // four ranks of a token
+#pragma unroll
+  for (int i = threadIdx.x; i < 16 * G * 8 * KR; i += kThreads) {   // four ranks of a token
     const int tok = i / (8 * KR), p = i % (8 * KR) * 4;
     f32x4 x = {0.f, 0.f, 0.f, 0.f};
-    if (tok < t.count && p < rp) {
+    if (tok < count && p < r) {   // the partials hold whole 16s of ranks
       const float* src = u.H + (place + tok) * rp + p;
-      for (int q = 0; q < u.ks; ++q) x += *reinterpret_cast<const f32x4*>(src + q * places * rp);
+      int q = 0;
+      for (; q + 4 <= u.ks; q += 4) {   // four loads in flight, added in order
+        f32x4 v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const f32x4*>(src + (q + e) * places * rp);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x += v[e];
+      }
+      for (; q < u.ks; ++q) x += *reinterpret_cast<const f32x4*>(src + q * places * rp);
     }
     bf16x4 h[3];
 #pragma unroll
@@ -367,22 +387,187 @@ __global__ __launch_bounds__(kThreads) void up_kernel(AdapterUp u, PlanView plan
 #pragma unroll
     for (int q = 0; q < 3; ++q) *reinterpret_cast<bf16x4*>(&hs[q][tok][p]) = h[q];
   }
-  __syncthreads();
-  const float g = pool.gain * (pool.gains != nullptr ? pool.gains[t.slot] : 1.f);
-  const uint64_t key = kOverA && u.drop.thr != 0 ? drop_key(u.drop) : 0;
-  for (int m = 0; 16 * m < t.count; ++m) {
+}
+
+// For outputs in whole 16-byte pieces and of less than 2^31 bytes: every load and store of the loop goes
+// through buffer resources, without a branch.  A wave turns a group of 16 tokens' sums round in LDS, so that
+// Y0 is loaded and Y stored in whole lines of a token (64-byte pieces of 16 tokens, as the matrix
+// cores give them, cost a third of the rate); a group's registers take the next block's loads as soon
+// as it is stored, so that four groups' loads are in flight all the time.
+constexpr int kTurnLd = 64 + 4;   // 16 tokens written at one feature, or one read along its features, meet every bank once
+
+template <typename O, int KR, int G, bool kMask>
+__device__ __forceinline__ void up_blocks(const AdapterUp& u, const PlanView& plan, const Pool& pool, const TileInfo& t,
+                                          int64_t place, int begin, int end, __bf16 (*hs)[kTile][32 * KR + 8],
+                                          float (*turn)[kTurnLd]) {
+  constexpr int kPer = 16 / static_cast<int>(sizeof(O)), kLanes = 64 / kPer, kRows = 64 / kLanes, kPieces = 16 / kRows;
+  typedef O piece_t __attribute__((ext_vector_type(kPer)));
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), li = lane & 15, lg = lane >> 4;
+  const uint32_t N = static_cast<uint32_t>(u.features);
+  const bool adapter = t.slot >= 0;
+  const int slot = adapter ? t.slot : 0;   // without an adapter no rank of it is used
+  const int r = adapter ? slot_rank(pool, slot) : 0;
+  const int64_t ld = u.ld;
+  const int all = records_of(static_cast<int64_t>(plan.n) * N * sizeof(O)), factor_records = records_of(N * ld * 2);
+  const __bf16* factor = u.F + (u.prepared ? used_place(plan, slot) : slot) * (N * ld);
+  const float g = pool.gain * (pool.gains != nullptr ? pool.gains[slot] : 1.f);
+  const uint64_t key = kMask ? drop_key(u.drop) : 0;
+  const __amdgpu_buffer_rsrc_t to = buffer_with(u.out, all);
+  // piece c of group m: token 16 m + kRows c + lane / kLanes, features kPer (lane % kLanes) .. of a block
+  const uint32_t n_lane = kPer * (lane % kLanes);
+  uint32_t offset[G][kPieces];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+  for (int m = 0; m < G; ++m)
 #pragma unroll
-    for (int q = 2; q >= 0; --q)
+    for (int c = 0; c < kPieces; ++c) {
+      const int tok = 16 * m + kRows * c + lane / kLanes;
+      const uint32_t e = static_cast<uint32_t>(token_at(plan, place + tok)) * N + n_lane;
+      offset[m][c] = tok < t.count ? e * static_cast<uint32_t>(sizeof(O)) : kNowhere;
+    }
+  u32x4 y[G][kPieces], f[4][KR];
+  auto load_y = [&](int m, int block) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t from = buffer_with(u.in, u.in != nullptr && block < end ? all : 0);
+#pragma unroll
+    for (int c = 0; c < kPieces; ++c)
+      y[m][c] = __builtin_amdgcn_raw_buffer_load_b128(from, block * 64u + n_lane < N ? offset[m][c] : kNowhere,
+                                                      block * 64 * static_cast<int>(sizeof(O)), 0);
+  };
+  auto load_factor = [&](int block) __attribute__((always_inline)) {
+    const __amdgpu_buffer_rsrc_t from = buffer_with(factor, block < end ? factor_records : 0);
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
 #pragma unroll
       for (int k = 0; k < KR; ++k) {
-        const u32x4 h = *reinterpret_cast<const u32x4*>(&hs[q][16 * m + li][32 * k + 8 * lg]);
-#pragma unroll
-        for (int a = 0; a < 4; ++a) acc[a] = mfma16(f[a][k], h, acc[a]);
+        const uint32_t n = static_cast<uint32_t>(block * 64 + 16 * a + li), p = 32 * k + 8 * lg;
+        f[a][k] = __builtin_amdgcn_raw_buffer_load_b128(
+            from, n < N && static_cast<int>(p) < r ? (n * static_cast<uint32_t>(ld) + p) * 2 : kNowhere, 0, 0);
       }
-    store(m, true, g, key);
+  };
+  int block = begin + w;
+#pragma unroll
+  for (int m = 0; m < G; ++m) {
+    load_y(m, block);
+    __builtin_amdgcn_sched_barrier(0);   // in the order in which they are waited for
   }
+  load_factor(block);
+  stage_pieces<KR, G>(u, plan, place, t.count, r, pool.rp, hs);
+  __syncthreads();
+  for (; block < end; block += 4) {
+    if (r % 8 != 0)   // ranks past the slot's own
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int k = 0; k < KR; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int p = 32 * k + 8 * lg + 2 * j;
+            f[a][k][j] = p + 1 < r ? f[a][k][j] : (p < r ? f[a][k][j] & 0xFFFFu : 0u);
+          }
+#pragma unroll
+    for (int m = 0; m < G; ++m) {
+      f32x4 acc[4];
+#pragma unroll
+      for (int a = 0; a < 4; ++a) acc[a] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 2; q >= 0; --q)
+#pragma unroll
+        for (int k = 0; k < KR; ++k) {
+          const u32x4 h = *reinterpret_cast<const u32x4*>(&hs[q][16 * m + li][32 * k + 8 * lg]);
+#pragma unroll
+          for (int a = 0; a < 4; ++a) acc[a] = mfma16(f[a][k], h, acc[a]);
+        }
+#pragma unroll
+      for (int a = 0; a < 4; ++a) *reinterpret_cast<f32x4*>(&turn[li][16 * a + 4 * lg]) = acc[a];
+      if (m == G - 1) load_factor(block + 4);
+      __builtin_amdgcn_wave_barrier();   // a wave's own rows: its reads come after its writes
+#pragma unroll
+      for (int c = 0; c < kPieces; ++c) {
+        const piece_t before = __builtin_bit_cast(piece_t, y[m][c]);
+        piece_t v;
+#pragma unroll
+        for (int e = 0; e < kPer / 4; ++e) {
+          const f32x4 x = *reinterpret_cast<const f32x4*>(&turn[kRows * c + lane / kLanes][n_lane + 4 * e]);
+          const uint64_t bits =
+              kMask ? drop_word(key, (offset[m][c] / static_cast<uint32_t>(sizeof(O)) + static_cast<uint32_t>(block * 64 + 4 * e)) >> 2) : 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float old = static_cast<float>(before[4 * e + i]);
+            const bool add = adapter && (!kMask || drop_keeps(bits, i, u.drop.thr));
+            v[4 * e + i] = static_cast<O>(add ? fmaf(g, x[i], old) : old);
+          }
+        }
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), to, block * 64u + n_lane < N ? offset[m][c] : kNowhere,
+                                               block * 64 * static_cast<int>(sizeof(O)), 0);
+      }
+      __builtin_amdgcn_wave_barrier();
+      load_y(m, block + 4);
+      __builtin_amdgcn_sched_barrier(0);   // a group's operands and results do not take the next one's registers
+    }
+  }
+}
+
+template <typename O, int KR, bool kMask>
+__global__ __launch_bounds__(kThreads) void up_kernel(AdapterUp u, PlanView plan, Pool pool, unsigned parts, int span) {
+  __shared__ __align__(16) __bf16 hs[3][kTile][32 * KR + 8];   // 16 rows read at one rank meet every bank once
+  __shared__ __align__(16) float turn[kThreads / 64][16][kTurnLd];
+  const int tile = blockIdx.x / parts, begin = static_cast<int>(blockIdx.x % parts) * span;
+  const TileInfo t = tile_info(plan, tile);
+  if (t.slot == -2 || t.count == 0 || (t.slot == -1 && u.in == u.out)) return;
+  const int blocks = static_cast<int>((u.features + 63) / 64), end = begin + span < blocks ? begin + span : blocks;
+  const int64_t place = static_cast<int64_t>(tile) * kTile;
+  if (t.count <= 16) up_blocks<O, KR, 1, kMask>(u, plan, pool, t, place, begin, end, hs, turn[threadIdx.x >> 6]);
+  else up_blocks<O, KR, 4, kMask>(u, plan, pool, t, place, begin, end, hs, turn[threadIdx.x >> 6]);
+}
+
+// For every other shape: 64-bit addresses, element by element.
+template <typename O, int KR>
+__global__ __launch_bounds__(kThreads) void up_any_kernel(AdapterUp u, PlanView plan, Pool pool, unsigned parts, int span) {
+  __shared__ __align__(16) __bf16 hs[3][kTile][32 * KR + 8];
+  const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, li = lane & 15, lg = lane >> 4;
+  const int tile = blockIdx.x / parts, begin = static_cast<int>(blockIdx.x % parts) * span;
+  const TileInfo t = tile_info(plan, tile);
+  if (t.slot == -2 || t.count == 0 || (t.slot == -1 && u.in == u.out)) return;
+  const int64_t N = u.features, ld = u.ld, place = static_cast<int64_t>(tile) * kTile;
+  const int blocks = static_cast<int>((N + 63) / 64), end = begin + span < blocks ? begin + span : blocks;
+  const bool adapter = t.slot >= 0;
+  const int slot = adapter ? t.slot : 0, r = adapter ? slot_rank(pool, slot) : 0;
+  const __amdgpu_buffer_rsrc_t factor = buffer_of(u.F + (u.prepared ? used_place(plan, slot) : slot) * (N * ld), N * ld * 2);
+  const float g = pool.gain * (pool.gains != nullptr ? pool.gains[slot] : 1.f);
+  const uint64_t key = u.drop.thr != 0 ? drop_key(u.drop) : 0;
+  const O* in = static_cast<const O*>(u.in);
+  O* out = static_cast<O*>(u.out);
+  stage_pieces<KR, 4>(u, plan, place, t.count, r, pool.rp, hs);
+  __syncthreads();
+  for (int block = begin + w; block < end; block += 4)
+    for (int a = 0; a < 4; ++a) {
+      const int64_t n0 = static_cast<int64_t>(block) * 64 + 16 * a;
+      u32x4 f[KR];
+#pragma unroll
+      for (int k = 0; k < KR; ++k) {
+        const int64_t n = n0 + li;
+        const int p = 32 * k + 8 * lg;
+        f[k] = __builtin_amdgcn_raw_buffer_load_b128(factor, n < N && p < r ? static_cast<uint32_t>(n * ld + p) * 2 : kNowhere, 0, 0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) f[k][j] = p + 2 * j + 1 < r ? f[k][j] : (p + 2 * j < r ? f[k][j] & 0xFFFFu : 0u);
+      }
+      for (int m = 0; 16 * m < t.count; ++m) {
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int q = 2; q >= 0; --q)
+#pragma unroll
+          for (int k = 0; k < KR; ++k) acc = mfma16(f[k], *reinterpret_cast<const u32x4*>(&hs[q][16 * m + li][32 * k + 8 * lg]), acc);
+        const int64_t row = token_at(plan, place + 16 * m + li) * N;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int64_t n = n0 + 4 * lg + i;
+          if (16 * m + li >= t.count || n >= N) continue;
+          const float x = in != nullptr ? static_cast<float>(in[row + n]) : 0.f;
+          const bool add = adapter && (u.drop.thr == 0 ||
+                                       drop_keeps(drop_word(key, static_cast<uint64_t>(row + n) >> 2), (row + n) & 3, u.drop.thr));
+          out[row + n] = static_cast<O>(add ? fmaf(g, acc[i], x) : x);
+        }
+      }
+    }
 }
 
 // ---- thin product over the tokens: the factors' gradients ----
@@ -393,7 +578,7 @@ __global__ __launch_bounds__(kThreads) void up_kernel(AdapterUp u, PlanView plan
 // one slot's tiles, which its four waves share 32 tokens at a time; past 32 ranks two waves share
 // a step, half of the ranks each.  kRankMajor (dA): S is the first operand, so a lane holds 8
 // consecutive features of a rank; else (dB) a lane's rank is L%16.
-template <int NR, bool kRankMajor>
+template <int NR, bool kRankMajor, bool kWide>
 __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, const PlanView& plan, const Pool& pool,
                                          float (*part)[8 * (NR > 2 ? 2 : NR) * 4 * 64]) {
   constexpr int kParts = NR > 2 ? 2 : 1, NT = NR > 2 ? 2 : NR, kWaves = 4 / kParts;
@@ -419,15 +604,25 @@ __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, con
   for (int j = 0; j < 8; ++j)
 #pragma unroll
     for (int t = 0; t < NT; ++t) acc[j][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-  const int64_t place0 = static_cast<int64_t>(first) * kTile + 8 * lg;
+  const int64_t place0 = static_cast<int64_t>(first) * kTile;
   u32x4 x[2][8], b[3][NT];
-  int64_t token[2][8];
+  uint32_t token[2][8];
+  const uint32_t width = static_cast<uint32_t>(F), bat = static_cast<uint32_t>(li * places + 8 * lg) * 2;
+  const int l_records = records_of(static_cast<int64_t>(plan.n) * F * 2);
   auto load = [&](int set, int s) __attribute__((always_inline)) {
-    if (s >= steps) return;
+    const int32_t* rows = plan.rows + place0 + 32 * static_cast<int64_t>(s < steps ? s : steps - 1) + 8 * lg;
+    const int4 lo = *reinterpret_cast<const int4*>(rows), hi = *reinterpret_cast<const int4*>(rows + 4);
+    const int t[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) token[set][i] = token_at(plan, place0 + 32 * static_cast<int64_t>(s) + i);
+    for (int i = 0; i < 8; ++i) token[set][i] = static_cast<unsigned>(t[i]) < static_cast<unsigned>(plan.n) ? t[i] : 0;
+    const __amdgpu_buffer_rsrc_t xb = buffer_with(jb.L, s < steps ? l_records : 0);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[set][i] = *reinterpret_cast<const u32x4*>(jb.L + token[set][i] * F + f);
+    for (int i = 0; i < 8; ++i) {
+      if constexpr (kWide)
+        x[set][i] = *reinterpret_cast<const u32x4*>(jb.L + token[set][i] * F + f);
+      else
+        x[set][i] = __builtin_amdgcn_raw_buffer_load_b128(xb, (token[set][i] * width + static_cast<uint32_t>(f)) * 2, 0, 0);
+    }
   };
   auto load_s = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
@@ -435,7 +630,8 @@ __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, con
 #pragma unroll
       for (int t = 0; t < NT; ++t) {   // of an odd number of rank tiles the last half's second repeats the first
         const int tile = tile0 + t < NR ? tile0 + t : tile0;
-        b[h][t] = *reinterpret_cast<const u32x4*>(jb.St + (h * 16 * NR + tile * 16 + li) * places + place0 + 32 * static_cast<int64_t>(s));
+        b[h][t] = __builtin_amdgcn_raw_buffer_load_b128(
+            buffer_at(jb.St + static_cast<int64_t>(h * 16 * NR + tile * 16) * places + place0 + 32 * static_cast<int64_t>(s), s < steps), bat, 0, 0);
       }
   };
   auto multiply = [&](int set) __attribute__((always_inline)) {
@@ -530,13 +726,13 @@ __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, con
 }
 
 // job 0: dB over dY; job 1: dA over X
-template <int NT>
+template <int NT, bool kWide>
 __global__ __launch_bounds__(kThreads, 2) void grad_kernel(AdapterGradJobs jobs, PlanView plan, Pool pool, uint32_t first) {
   __shared__ float part[2][8 * (NT > 2 ? 2 : NT) * 4 * 64];
   if (blockIdx.x < first)
-    grad_job<NT, false>(jobs.job[0], blockIdx.x, plan, pool, part);
+    grad_job<NT, false, kWide>(jobs.job[0], blockIdx.x, plan, pool, part);
   else
-    grad_job<NT, true>(jobs.job[1], blockIdx.x - first, plan, pool, part);
+    grad_job<NT, true, kWide>(jobs.job[1], blockIdx.x - first, plan, pool, part);
 }
 
 // gain times the sum of a slot's partials in chunk order; zeros without tokens
@@ -552,13 +748,26 @@ __global__ __launch_bounds__(kThreads) void grad_sum_kernel(AdapterGradJobs jobs
     chunks = plan.slot_chunks[slot + 1] - chunk;
     if (chunks == 1 || chunk < 0 || chunks < 0 || chunk + chunks > plan.max_chunks) return;
   }
-  const int64_t i = static_cast<int64_t>(blockIdx.x - (rank_major ? first : 0)) * kThreads + threadIdx.x, nf = jb.nf;
-  if (i >= nf * R) return;
-  const int64_t at = rank_major ? i / nf * jb.F + i % nf : i / R * rp + i % R;
-  float x = 0.f;
-  for (int q = 0; q < chunks; ++q) x += jb.partials[(chunk + q) * (jb.F * rp) + at];
+  const int64_t i = (static_cast<int64_t>(blockIdx.x - (rank_major ? first : 0)) * kThreads + threadIdx.x) * 4, nf = jb.nf, all = nf * R;
+  if (i >= all) return;
   const float g = pool.gain * (pool.gains != nullptr ? pool.gains[slot] : 1.f);
-  jb.out[slot * (nf * R) + i] = chunks > 0 ? g * x : 0.f;
+  float* out = jb.out + slot * all + i;
+  const float* src = jb.partials + chunk * (jb.F * rp);
+  if (all % 4 == 0 && (rank_major || R % 4 == 0)) {   // four elements in a row in either form
+    const uint32_t e = static_cast<uint32_t>(i), per = static_cast<uint32_t>(R);
+    const int64_t at = rank_major ? i : static_cast<int64_t>(e / per) * rp + e % per;   // nf == F for dA
+    f32x4 x = {0.f, 0.f, 0.f, 0.f};
+    for (int q = 0; q < chunks; ++q) x += *reinterpret_cast<const f32x4*>(src + q * (jb.F * rp) + at);
+    if (chunks > 0) x *= g;
+    *reinterpret_cast<f32x4*>(out) = x;
+    return;
+  }
+  for (int j = 0; j < 4 && i + j < all; ++j) {
+    const int64_t at = rank_major ? i + j : (i + j) / R * rp + (i + j) % R;
+    float x = 0.f;
+    for (int q = 0; q < chunks; ++q) x += src[q * (jb.F * rp) + at];
+    out[j] = chunks > 0 ? g * x : 0.f;
+  }
 }
 
 __global__ __launch_bounds__(kThreads) void pad_kernel(const __bf16* __restrict__ in, __bf16* __restrict__ out, int64_t n,
@@ -574,16 +783,17 @@ __global__ __launch_bounds__(kThreads) void pad_kernel(const __bf16* __restrict_
 
 unsigned blocks_for(int64_t threads) { return static_cast<unsigned>((threads + kThreads - 1) / kThreads); }
 
-// K ranges for about m tiles' halves of tokens
-int splits_for(int64_t halves, int64_t K) {
-  // about a workgroup of eight waves per CU, each range with a step for every wave
-  int64_t ks = 256 / halves;
+// K ranges for about `tiles` tiles: workgroups for every CU several times over (8192 tokens of 11008 columns at rank 16:
+// 81 us with 256 workgroups in all, 61 with 400, 57 with 1100), fewer of them where the waves' sums are larger (2048
+// tokens of 11008 + 4096 columns at rank 64: 37 us with 256, 48 with 550); each range has a step for every wave
+int splits_for(int64_t tiles, int64_t K, int rp) {
+  int64_t ks = 1024 / (rp / 16) / tiles;
   const int64_t most = (K + 31) / 32 / kDownWaves;
   if (ks > most) ks = most;
   return static_cast<int>(ks < 1 ? 1 : (ks > 16 ? 16 : ks));
 }
-// how many halves of tiles a batch may have, the slots' last ones half of the time
-int64_t halves_of(int64_t n, int slots) { return 1 + n / 32 + (n < slots ? n : slots) / 2; }
+// how many tiles a batch may have, the slots' last ones half of the time
+int64_t tiles_of(int64_t n, int slots) { return 1 + n / kTile + (n < slots ? n : slots) / 2; }
 
 }  // namespace
 
@@ -595,36 +805,49 @@ int64_t halves_of(int64_t n, int slots) { return 1 + n / 32 + (n < slots ? n : s
     default: CALL(4); break; \
   }
 
-int adapters_down_splits(int64_t n, int slots, int64_t K) { return splits_for(halves_of(n, slots), K); }
+int adapters_down_splits(int64_t n, int slots, int64_t K, int rp) { return splits_for(tiles_of(n, slots), K, rp); }
 
-int64_t adapters_down_tiles_bound(int64_t n, int slots, int64_t K) {
-  int64_t bound = plan_layout(n, slots).max_tiles * adapters_down_splits(n, slots, K);
-  for (int ks = adapters_down_splits(n, slots, K) + 1; ks <= adapters_down_splits(1, slots, K); ++ks) {
-    // the most tokens that take as many ranges
-    int64_t lo = 1, hi = n;
-    while (lo < hi) {
-      const int64_t mid = (lo + hi + 1) / 2;
-      if (adapters_down_splits(mid, slots, K) >= ks) lo = mid;
-      else hi = mid - 1;
-    }
-    const int64_t tiles = plan_layout(lo, slots).max_tiles * adapters_down_splits(lo, slots, K);
-    if (tiles > bound) bound = tiles;
-  }
-  return bound;
+// A batch has at most twice tiles_of() tiles, so that its ranges and tiles are at most twice what splits_for() divides.
+int64_t adapters_down_floats_bound(int64_t n, int slots, int64_t K, int rp) {
+  const int64_t tiles = plan_layout(n, slots).max_tiles, most = tiles * splits_for(1, K, 16), divided = 2 * 1024 / (rp / 16);
+  const int64_t bound = most < divided ? most : divided;
+  return (bound > tiles ? bound : tiles) * kTile * rp;
 }
 
-hipError_t launch_adapters_down(AdapterDownJobs jobs, const PlanView& plan, const Pool& pool, hipStream_t s) {
-  for (AdapterDown& j : jobs.job) j.wgs = j.L != nullptr ? static_cast<unsigned>(2 * plan.max_tiles * j.ks) : 0;
-  const dim3 grid(jobs.job[0].wgs + jobs.job[1].wgs);
-#define LQ_DOWN(NT)                                                                                                             \
-  do {                                                                                                                          \
-    if (pool.dt == LOFTQ_BF16)                                                                                                  \
-      LQ_LAUNCH("adapters_down", (down_kernel<NT, __bf16>), grid, dim3(kDownThreads), 0, s, jobs, plan, pool);                  \
-    else                                                                                                                        \
-      LQ_LAUNCH("adapters_down", (down_kernel<NT, float>), grid, dim3(kDownThreads), 0, s, jobs, plan, pool);                   \
+static unsigned prepare_wgs(const Prepare& q, const Pool& pool, int threads) {
+  const int64_t rp = pool.rp, work = (q.Bp ? q.rows * (rp / 8) : 0) + (q.Bt ? q.rows8 / 8 * rp : 0) +
+                                     (q.Ab ? q.cols / 8 * rp : 0) + (q.At ? q.cols * (rp / 8) : 0);
+  return static_cast<unsigned>((work + threads - 1) / threads);
+}
+
+hipError_t launch_adapters_prepare(Prepare q, const PlanView& plan, const Pool& pool, hipStream_t s) {
+  q.wgs = prepare_wgs(q, pool, kThreads);
+  if (q.wgs == 0) return hipSuccess;
+  LQ_LAUNCH("adapters_prepare", prepare_kernel, dim3(q.wgs * pool.slots), dim3(kThreads), 0, s, q, plan, pool);
+  return hipGetLastError();
+}
+
+hipError_t launch_adapters_down(AdapterDownJobs jobs, loftq_dtype_t factor, const Prepare& prepare, const PlanView& plan,
+                                const Pool& pool, hipStream_t s) {
+  Prepare q = prepare;
+  q.wgs = prepare_wgs(q, pool, kDownThreads);
+  bool wide = false;   // 32-bit offsets reach the tokens' rows
+  for (AdapterDown& j : jobs.job) {
+    j.wgs = j.L != nullptr ? static_cast<unsigned>(plan.max_tiles * j.ks) : 0;
+    wide = wide || (j.L != nullptr && plan.n * j.K * 2 >= (int64_t(1) << 31));
+  }
+  const dim3 grid(jobs.job[0].wgs + jobs.job[1].wgs + q.wgs * pool.slots), block(kDownThreads);
+#define LQ_DOWN_KERNEL(NT, F, W) LQ_LAUNCH("adapters_down", (down_kernel<NT, F, W>), grid, block, 0, s, jobs, q, plan, pool)
+#define LQ_DOWN(NT)                                                \
+  do {                                                             \
+    if (factor == LOFTQ_BF16 && wide) LQ_DOWN_KERNEL(NT, __bf16, true); \
+    else if (factor == LOFTQ_BF16) LQ_DOWN_KERNEL(NT, __bf16, false);   \
+    else if (wide) LQ_DOWN_KERNEL(NT, float, true);                \
+    else LQ_DOWN_KERNEL(NT, float, false);                         \
   } while (0)
   LQ_BY_RANK(pool.rp, LQ_DOWN)
 #undef LQ_DOWN
+#undef LQ_DOWN_KERNEL
   return hipGetLastError();
 }
 
@@ -634,49 +857,53 @@ hipError_t launch_adapters_sum(AdapterSumJobs jobs, const PlanView& plan, int rp
   return hipGetLastError();
 }
 
-template <typename O, typename F, bool kOverA>
-static void up_by_shape(const AdapterUp& u, const PlanView& plan, const Pool& pool, hipStream_t s) {
-  const unsigned blocks = static_cast<unsigned>((u.features + 255) / 256);
-  const dim3 grid(static_cast<unsigned>(plan.max_tiles) * blocks), block(kThreads);
-  const bool vec = u.features % (16 / static_cast<int64_t>(sizeof(O))) == 0;
-  if (pool.rp <= 32) {
-    if (vec) LQ_LAUNCH("adapters_up", (up_kernel<O, F, 1, true, kOverA>), grid, block, 0, s, u, plan, pool, blocks);
-    else LQ_LAUNCH("adapters_up", (up_kernel<O, F, 1, false, kOverA>), grid, block, 0, s, u, plan, pool, blocks);
-  } else {
-    if (vec) LQ_LAUNCH("adapters_up", (up_kernel<O, F, 2, true, kOverA>), grid, block, 0, s, u, plan, pool, blocks);
-    else LQ_LAUNCH("adapters_up", (up_kernel<O, F, 2, false, kOverA>), grid, block, 0, s, u, plan, pool, blocks);
-  }
-}
-
 hipError_t launch_adapters_up(const AdapterUp& u, const PlanView& plan, const Pool& pool, hipStream_t s) {
-#define LQ_UP(O, F)                                           \
-  do {                                                        \
-    if (u.over_a) up_by_shape<O, F, true>(u, plan, pool, s);  \
-    else up_by_shape<O, F, false>(u, plan, pool, s);          \
+  const int64_t blocks = (u.features + 63) / 64, size = u.odt == LOFTQ_BF16 ? 2 : 4;
+  // about 2048 workgroups, each wave with a block at least
+  int64_t span = tiles_of(plan.n, plan.slots) * blocks / 2048 / 4 * 4;
+  span = span < 4 ? 4 : (span > 64 ? 64 : span);
+  const unsigned parts = static_cast<unsigned>((blocks + span - 1) / span);
+  const dim3 grid(static_cast<unsigned>(plan.max_tiles) * parts), block(kThreads);
+  const bool whole = u.features % (16 / size) == 0 && plan.n * u.features * size < (int64_t(1) << 31), mask = u.drop.thr != 0;
+#define LQ_UP_KERNEL(...) LQ_LAUNCH("adapters_up", (__VA_ARGS__), grid, block, 0, s, u, plan, pool, parts, static_cast<int>(span))
+#define LQ_UP(O, KR)                                        \
+  do {                                                      \
+    if (!whole) LQ_UP_KERNEL(up_any_kernel<O, KR>);         \
+    else if (mask) LQ_UP_KERNEL(up_kernel<O, KR, true>);    \
+    else LQ_UP_KERNEL(up_kernel<O, KR, false>);             \
   } while (0)
   if (u.odt == LOFTQ_BF16) {
-    if (pool.dt == LOFTQ_BF16) LQ_UP(__bf16, __bf16);
-    else LQ_UP(__bf16, float);
+    if (pool.rp <= 32) LQ_UP(__bf16, 1);
+    else LQ_UP(__bf16, 2);
   } else {
-    if (pool.dt == LOFTQ_BF16) LQ_UP(float, __bf16);
-    else LQ_UP(float, float);
+    if (pool.rp <= 32) LQ_UP(float, 1);
+    else LQ_UP(float, 2);
   }
 #undef LQ_UP
+#undef LQ_UP_KERNEL
   return hipGetLastError();
 }
 
 hipError_t launch_adapters_grad(const AdapterGradJobs& jobs, const PlanView& plan, const Pool& pool, hipStream_t s) {
   unsigned wgs[2];
   for (int j = 0; j < 2; ++j) wgs[j] = static_cast<unsigned>((jobs.job[j].F + 127) / 128 * plan.max_chunks);
-#define LQ_GRAD(NT) \
-  LQ_LAUNCH("adapters_grad", (grad_kernel<NT>), dim3(wgs[0] + wgs[1]), dim3(kThreads), 0, s, jobs, plan, pool, wgs[0])
+  // 32-bit offsets reach the tokens' rows
+  const bool wide = plan.n * jobs.job[0].F * 2 >= (int64_t(1) << 31) || plan.n * jobs.job[1].F * 2 >= (int64_t(1) << 31);
+#define LQ_GRAD_KERNEL(NT, W) \
+  LQ_LAUNCH("adapters_grad", (grad_kernel<NT, W>), dim3(wgs[0] + wgs[1]), dim3(kThreads), 0, s, jobs, plan, pool, wgs[0])
+#define LQ_GRAD(NT)                       \
+  do {                                    \
+    if (wide) LQ_GRAD_KERNEL(NT, true);   \
+    else LQ_GRAD_KERNEL(NT, false);       \
+  } while (0)
   LQ_BY_RANK(pool.rp, LQ_GRAD)
 #undef LQ_GRAD
+#undef LQ_GRAD_KERNEL
   return hipGetLastError();
 }
 
 hipError_t launch_adapters_grad_sum(const AdapterGradJobs& jobs, const PlanView& plan, const Pool& pool, hipStream_t s) {
-  const unsigned first = blocks_for(jobs.job[0].nf * pool.rank), second = blocks_for(jobs.job[1].nf * pool.rank);
+  const unsigned first = blocks_for((jobs.job[0].nf * pool.rank + 3) / 4), second = blocks_for((jobs.job[1].nf * pool.rank + 3) / 4);
   LQ_LAUNCH("adapters_grad_sum", grad_sum_kernel, dim3(first + second, pool.slots), dim3(kThreads), 0, s, jobs, plan, pool, first);
   return hipGetLastError();
 }

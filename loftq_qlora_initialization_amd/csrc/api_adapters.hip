@@ -43,20 +43,23 @@ bool sizes_ok(i64 n, i64 rows, i64 cols, int slots, int rank, bool backward) {
 
 struct ForwardSpace {
   float* partials;   // of X A^T
+  __bf16* Bp;        // B in bf16 rows of whole 16 ranks, unless it is read as it lies
   int ks;
   size_t bytes;
 };
-ForwardSpace forward_space(void* ws, i64 n, i64 cols, int slots, int rank) {
+ForwardSpace forward_space(void* ws, i64 n, i64 rows, i64 cols, int slots, int rank) {
   Arena a{static_cast<char*>(ws)};
   ForwardSpace f{};
-  f.ks = adapters_down_splits(n, slots, cols);
-  f.partials = a.take<float>(adapters_down_tiles_bound(n, slots, cols) * kTile * rank_pad(rank));
+  const int rp = rank_pad(rank);
+  f.ks = adapters_down_splits(n, slots, cols, rp);
+  f.partials = a.take<float>(adapters_down_floats_bound(n, slots, cols, rp));
+  f.Bp = a.take<__bf16>(used_slots(n, slots) * rows * rp);
   f.bytes = a.used;
   return f;
 }
 
 struct BackwardSpace {
-  __bf16 *G, *Pt, *Ht;
+  __bf16 *G, *Pt, *Ht, *Bt, *Ab, *At;
   float *down_p, *down_h, *P, *grad_b, *grad_a;
   int ks_p, ks_h;
   size_t bytes;
@@ -64,14 +67,17 @@ struct BackwardSpace {
 BackwardSpace backward_space(void* ws, i64 n, i64 rows, i64 cols, int slots, int rank) {
   Arena a{static_cast<char*>(ws)};
   BackwardSpace f{};
-  const i64 rows8 = pad8(rows);
+  const i64 rows8 = pad8(rows), used = used_slots(n, slots);
   const int rp = rank_pad(rank);
   const PlanLayout p = plan_layout(n, slots);
-  f.ks_p = adapters_down_splits(n, slots, rows8);
-  f.ks_h = adapters_down_splits(n, slots, cols);
+  f.ks_p = adapters_down_splits(n, slots, rows8, rp);
+  f.ks_h = adapters_down_splits(n, slots, cols, rp);
   if (rows8 != rows) f.G = a.take<__bf16>(n * rows8);
-  f.down_p = a.take<float>(adapters_down_tiles_bound(n, slots, rows8) * kTile * rp);
-  f.down_h = a.take<float>(adapters_down_tiles_bound(n, slots, cols) * kTile * rp);
+  f.Bt = a.take<__bf16>(used * rows8 * rp);
+  f.Ab = a.take<__bf16>(used * cols * rp);
+  f.At = a.take<__bf16>(used * cols * rp);
+  f.down_p = a.take<float>(adapters_down_floats_bound(n, slots, rows8, rp));
+  f.down_h = a.take<float>(adapters_down_floats_bound(n, slots, cols, rp));
   f.P = a.take<float>(p.max_tiles * kTile * rp);
   f.Pt = a.take<__bf16>(3 * p.max_tiles * kTile * rp);
   f.Ht = a.take<__bf16>(3 * p.max_tiles * kTile * rp);
@@ -142,7 +148,7 @@ loftq_status_t loftq_adapters_plan(const int32_t* slot_of, int64_t n_tok, int32_
 }
 
 size_t loftq_adapters_forward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t slots, int32_t rank) {
-  return query_ok(n_tok, rows, cols, slots, rank, false) && n_tok > 0 ? forward_space(nullptr, n_tok, cols, slots, rank).bytes : 0;
+  return query_ok(n_tok, rows, cols, slots, rank, false) && n_tok > 0 ? forward_space(nullptr, n_tok, rows, cols, slots, rank).bytes : 0;
 }
 
 loftq_status_t loftq_adapters_forward(const void* X, int64_t n_tok, int64_t rows, int64_t cols, const loftq_adapters_t* ad,
@@ -156,14 +162,23 @@ loftq_status_t loftq_adapters_forward(const void* X, int64_t n_tok, int64_t rows
   st = check_pool(ad, plan, plan_bytes, n_tok);
   if (st != LOFTQ_OK) return st;
   if (!X || !Y || !ws || !aligned16(X) || !aligned16(Y0) || !aligned16(Y) || !aligned16(ws)) return LOFTQ_ERR_INVALID_ARG;
-  const ForwardSpace f = forward_space(ws, n_tok, cols, ad->slots, ad->rank);
+  const ForwardSpace f = forward_space(ws, n_tok, rows, cols, ad->slots, ad->rank);
   if (ws_bytes < f.bytes) return LOFTQ_ERR_WORKSPACE;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const DropArg d = drop_arg(drop), none = drop_arg(nullptr);
   const PlanView view = plan_view(plan, plan_layout(n_tok, ad->slots));
   const Pool pool = pool_of(ad, d);
-  LQ_TRY(launch_adapters_down(AdapterDownJobs{{{}, {static_cast<const __bf16*>(X), cols, rows, f.partials, f.ks, 0, d}}}, view, pool, s));
-  return from_hip(launch_adapters_up(AdapterUp{f.partials, f.ks, rows, Y0, Y, ydt, false, none}, view, pool, s));
+  // B in bf16 with whole eights of ranks is read as it lies; else its form is made beside X A^T
+  const bool as_it_lies = ad->dt == LOFTQ_BF16 && ad->rank % 8 == 0;
+  Prepare prepare{};
+  prepare.Bp = as_it_lies ? nullptr : f.Bp;
+  prepare.rows = rows;
+  prepare.cols = cols;
+  LQ_TRY(launch_adapters_down(AdapterDownJobs{{{}, {static_cast<const __bf16*>(X), cols, ad->A, ad->rank * cols, false, f.partials, f.ks, 0, d}}},
+                              ad->dt, prepare, view, pool, s));
+  AdapterUp up{f.partials, f.ks, rows, as_it_lies ? static_cast<const __bf16*>(ad->B) : f.Bp, as_it_lies ? ad->rank : pool.rp,
+               !as_it_lies, Y0, Y, ydt, none};
+  return from_hip(launch_adapters_up(up, view, pool, s));
 }
 
 size_t loftq_adapters_backward_workspace_bytes(int64_t n_tok, int64_t rows, int64_t cols, int32_t slots, int32_t rank) {
@@ -203,14 +218,24 @@ loftq_status_t loftq_adapters_backward(const void* dY, const void* X, int64_t n_
     LQ_TRY(launch_adapters_pad(G, f.G, n_tok, rows, rows8, s));
     G = f.G;
   }
+  const bool a_as_it_lies = ad->dt == LOFTQ_BF16;
+  Prepare prepare{};
+  prepare.Bt = f.Bt;
+  prepare.Ab = dB && !a_as_it_lies ? f.Ab : nullptr;
+  prepare.At = dX ? f.At : nullptr;
+  prepare.rows = rows;
+  prepare.rows8 = rows8;
+  prepare.cols = cols;
+  LQ_TRY(launch_adapters_prepare(prepare, view, pool, s));
   // P = G B for dX and dA, H = keep(X) A^T for dB
-  AdapterDownJobs down{{{G, rows8, rows, f.down_p, f.ks_p, 0, none}, {}}};
+  AdapterDownJobs down{{{G, rows8, f.Bt, pool.rp * rows8, true, f.down_p, f.ks_p, 0, none}, {}}};
   AdapterSumJobs sum{{{f.down_p, f.ks_p, dX ? f.P : nullptr, dB ? f.Pt : nullptr}, {}}};
   if (dB) {
-    down.job[1] = AdapterDown{Xb, cols, rows, f.down_h, f.ks_h, 0, d};
+    down.job[1] = a_as_it_lies ? AdapterDown{Xb, cols, ad->A, ad->rank * cols, false, f.down_h, f.ks_h, 0, d}
+                               : AdapterDown{Xb, cols, f.Ab, pool.rp * cols, true, f.down_h, f.ks_h, 0, d};
     sum.job[1] = AdapterSum{f.down_h, f.ks_h, nullptr, f.Ht};
   }
-  LQ_TRY(launch_adapters_down(down, view, pool, s));
+  LQ_TRY(launch_adapters_down(down, LOFTQ_BF16, Prepare{}, view, pool, s));
   LQ_TRY(launch_adapters_sum(sum, view, pool.rp, s));
   if (dB) {
     const AdapterGradJobs grad{{{G, f.Ht, f.grad_b, dB, rows8, rows, none}, {Xb, f.Pt, f.grad_a, dA, cols, cols, d}}};
@@ -218,7 +243,7 @@ loftq_status_t loftq_adapters_backward(const void* dY, const void* X, int64_t n_
     LQ_TRY(launch_adapters_grad_sum(grad, view, pool, s));
   }
   if (!dX) return LOFTQ_OK;
-  return from_hip(launch_adapters_up(AdapterUp{f.P, 1, cols, dX0, dX, xdt, true, d}, view, pool, s));
+  return from_hip(launch_adapters_up(AdapterUp{f.P, 1, cols, f.At, pool.rp, true, dX0, dX, xdt, d}, view, pool, s));
 }
 
 }  // extern "C"

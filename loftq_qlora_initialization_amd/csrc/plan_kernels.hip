@@ -29,18 +29,18 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(const int32_t*
     plan[p.counts + static_cast<int64_t>(blockIdx.x) * (p.slots + 1) + s] = hist[s];
 }
 
-struct Three {
-  int tokens, tiles, chunks;
+struct Sums {
+  int tokens, tiles, chunks, used;
 };
-__device__ __forceinline__ Three operator+(Three a, Three b) {
-  return Three{a.tokens + b.tokens, a.tiles + b.tiles, a.chunks + b.chunks};
+__device__ __forceinline__ Sums operator+(Sums a, Sums b) {
+  return Sums{a.tokens + b.tokens, a.tiles + b.tiles, a.chunks + b.chunks, a.used + b.used};
 }
 
 __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t* __restrict__ slot_of, PlanLayout p,
                                                                   int32_t* __restrict__ plan) {
   __shared__ int count[kWaves][kMostSlots + 1];   // a wave's tokens by slot, then the place of its next one
-  __shared__ Three first[kMostSlots + 2];         // a slot's first token, tile and chunk
-  __shared__ Three wave_sum[kWaves];
+  __shared__ Sums first[kMostSlots + 2];         // a slot's first token, tile and chunk, and the used slots before it
+  __shared__ Sums wave_sum[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, groups = p.slots + 1;
   for (int i = tid; i < kWaves * (kMostSlots + 1); i += kPlanThreads) (&count[0][0])[i] = 0;
   __syncthreads();
@@ -50,7 +50,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
   __syncthreads();
   // a slot's total, and the place of each wave's first token among the slot's
   const int each = (groups + kPlanThreads - 1) / kPlanThreads, s0 = tid * each;
-  Three mine{0, 0, 0};
+  Sums mine{0, 0, 0, 0};
   for (int s = s0; s < s0 + each && s < groups; ++s) {
     int before = 0, total = 0;
     if (p.wgs > 1)
@@ -66,29 +66,33 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
     }
     if (p.wgs == 1) total = before;
     const int tiles = (total + kTile - 1) / kTile;
-    const Three own{total, tiles, s < p.slots ? (tiles + p.chunk_tiles - 1) / p.chunk_tiles : 0};
+    const Sums own{total, tiles, s < p.slots ? (tiles + p.chunk_tiles - 1) / p.chunk_tiles : 0,
+                   s < p.slots && total > 0 ? 1 : 0};
     first[s] = mine;     // within the thread, made whole below
     mine = mine + own;
   }
-  Three upto = mine;     // sums over the wave's lanes up to this one
+  Sums upto = mine;     // sums over the wave's lanes up to this one
   for (int d = 1; d < 64; d <<= 1) {
-    const Three o{__shfl_up(upto.tokens, d), __shfl_up(upto.tiles, d), __shfl_up(upto.chunks, d)};
+    const Sums o{__shfl_up(upto.tokens, d), __shfl_up(upto.tiles, d), __shfl_up(upto.chunks, d), __shfl_up(upto.used, d)};
     if (lane >= d) upto = upto + o;
   }
   if (lane == 63) wave_sum[w] = upto;
   __syncthreads();
-  Three base{upto.tokens - mine.tokens, upto.tiles - mine.tiles, upto.chunks - mine.chunks};
+  Sums base{upto.tokens - mine.tokens, upto.tiles - mine.tiles, upto.chunks - mine.chunks, upto.used - mine.used};
   for (int v = 0; v < w; ++v) base = base + wave_sum[v];
   for (int s = s0; s < s0 + each && s < groups; ++s) first[s] = first[s] + base;
   if (tid == 0) {
-    Three all{0, 0, 0};
+    Sums all{0, 0, 0, 0};
     for (int v = 0; v < kWaves; ++v) all = all + wave_sum[v];
     first[groups] = all;
   }
   __syncthreads();
   if (blockIdx.x == 0) {
     for (int s = tid; s <= groups; s += kPlanThreads) plan[s] = first[s].tokens;
-    for (int s = tid; s < groups; s += kPlanThreads) plan[p.slot_chunks + s] = first[s].chunks;
+    for (int s = tid; s < groups; s += kPlanThreads) {
+      plan[p.slot_chunks + s] = first[s].chunks;
+      plan[p.slot_used + s] = first[s].used;
+    }
     if (tid == 0)
       *reinterpret_cast<int4*>(plan + p.info) =
           make_int4(first[groups].tiles, first[groups].chunks, static_cast<int>(p.n), p.slots);
@@ -133,7 +137,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
 // without tokens
 __global__ void plan_empty_kernel(PlanLayout p, int32_t* __restrict__ plan) {
   for (int s = threadIdx.x; s < p.slots + 2; s += blockDim.x) plan[s] = 0;
-  for (int s = threadIdx.x; s < p.slots + 1; s += blockDim.x) plan[p.slot_chunks + s] = 0;
+  for (int s = threadIdx.x; s < p.slots + 1; s += blockDim.x) plan[p.slot_chunks + s] = plan[p.slot_used + s] = 0;
   if (threadIdx.x == 0) *reinterpret_cast<int4*>(plan + p.info) = make_int4(0, 0, 0, p.slots);
 }
 
