@@ -27,7 +27,7 @@ struct AdamTable {
   AdamScalars* scalars;
   size_t bytes;
 };
-constexpr int kNormWorkgroups = 1024;
+constexpr int kNormWorkgroups = 2048;
 
 inline int64_t adam_chunks(int64_t n) { return (n + kChunk - 1) / kChunk; }
 

@@ -119,15 +119,22 @@ __global__ __launch_bounds__(kThreads) void norm_kernel(AdamTable t, int64_t chu
     const int2 at = t.chunks[c];
     const loftq_adamw_tensor_t& x = t.tensors[at.x];
     const int64_t begin = static_cast<int64_t>(at.y) * kChunk + threadIdx.x * 4;
+    constexpr int kLoads = kChunk / (4 * kThreads);
+    float g[kLoads][4];
+    if (static_cast<int64_t>(at.y + 1) * kChunk <= x.n) {   // a whole chunk: every load in flight at once
 #pragma unroll
-    for (int i = 0; i < kChunk / (4 * kThreads); ++i) {
-      const int64_t e = begin + i * (4 * kThreads), left = x.n - e;
-      if (left <= 0) break;
-      float g[4];
-      load4<G>(x.grad, e, left < 4 ? static_cast<int>(left) : 4, g);
+      for (int i = 0; i < kLoads; ++i) load4<G>(x.grad, begin + i * (4 * kThreads), 4, g[i]);
+    } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum = fma(static_cast<double>(g[j]), static_cast<double>(g[j]), sum);
+      for (int i = 0; i < kLoads; ++i) {
+        const int64_t left = x.n - begin - i * (4 * kThreads);
+        load4<G>(x.grad, begin + i * (4 * kThreads), left < 0 ? 0 : (left < 4 ? static_cast<int>(left) : 4), g[i]);
+      }
     }
+#pragma unroll
+    for (int i = 0; i < kLoads; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum = fma(static_cast<double>(g[i][j]), static_cast<double>(g[i][j]), sum);
   }
   for (int d = 32; d > 0; d >>= 1) sum += __shfl_xor(sum, d);
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;

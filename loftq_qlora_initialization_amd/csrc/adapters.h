@@ -37,9 +37,10 @@ inline PlanLayout plan_layout(int64_t n, int slots) {
   const int64_t groups = n < slots + 1 ? n : slots + 1, whole = n / kTile;
   // a group of c tokens has at most (c + 63) / 64 tiles, and those of q tiles (q + c - 1) / c chunks of c
   p.max_tiles = whole + groups;
-  // about eight chunks of a batch with one slot, of 2 to 64 tiles
-  p.chunk_tiles = static_cast<int>(whole <= 16 ? 2 : (whole >= 512 ? 64 : (whole + 7) / 8));
-  p.max_chunks = (whole / 64 > 8 ? whole / 64 : 8) + groups + groups / 2 + 1;   // grows with n
+  // about four chunks of a batch with one slot, of 2 to 128 tiles: with the groups of features they fill the CUs, and
+  // most slots of a batch with several have one, whose sums need no second pass
+  p.chunk_tiles = static_cast<int>(whole <= 8 ? 2 : (whole >= 512 ? 128 : (whole + 3) / 4));
+  p.max_chunks = (whole / 128 > 4 ? whole / 128 : 4) + groups + groups / 2 + 1;   // grows with n
   p.per_wg = (n + 255) / 256;
   p.per_wg = p.per_wg < 4096 ? 4096 : (p.per_wg + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
   p.wgs = static_cast<int>((n + p.per_wg - 1) / p.per_wg);
@@ -94,6 +95,7 @@ struct Prepare {
   __bf16* Bt;      // [used][rp][rows8]: zeros past `rows`
   __bf16* Ab;      // [used][rp][cols]
   __bf16* At;      // [used][cols][rp]
+  float *dB, *dA;  // gradients, or null: zeros for the slots without tokens
   int64_t rows, rows8, cols;
   unsigned wgs;    // a slot's workgroups, set by the launcher
 };
@@ -133,7 +135,8 @@ struct AdapterSum {
 struct AdapterSumJobs {
   AdapterSum job[2];
 };
-hipError_t launch_adapters_sum(AdapterSumJobs jobs, const PlanView& plan, int rp, hipStream_t s);
+// with the forms of `prepare` in the same launch
+hipError_t launch_adapters_sum(AdapterSumJobs jobs, const Prepare& prepare, const PlanView& plan, const Pool& pool, hipStream_t s);
 
 // out = in + gain keep(H F^T): H the partial sums of `ks` ranges, F [slot][features][ld] in bf16.
 struct AdapterUp {
@@ -162,7 +165,7 @@ struct AdapterGradJobs {
   AdapterGrad job[2];
 };
 hipError_t launch_adapters_grad(const AdapterGradJobs& jobs, const PlanView& plan, const Pool& pool, hipStream_t s);
-// the sums of partials, and zeros for slots without tokens (`plan.n` may be 0)
+// the sums of partials; zeros for a batch without tokens
 hipError_t launch_adapters_grad_sum(const AdapterGradJobs& jobs, const PlanView& plan, const Pool& pool, hipStream_t s);
 
 // dY in rows of `to` columns, zeros past `from`

@@ -28,7 +28,7 @@ __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
 
 // 8 values of a masked row, elements e .. e + 7 of the flattening (e % 8 == 0)
 __device__ __forceinline__ u32x4 drop8(u32x4 v, uint64_t key, uint64_t e, uint32_t thr) {
-  const uint64_t w0 = drop_word(key, e >> 2), w1 = drop_word(key, (e >> 2) + 1);
+  const uint64_t z = key + ((e >> 2) + 1) * kMixGamma, w0 = mix64(z), w1 = mix64(z + kMixGamma);
   v[0] = drop_pair(v[0], w0, 0, thr);
   v[1] = drop_pair(v[1], w0, 2, thr);
   v[2] = drop_pair(v[2], w1, 0, thr);
@@ -65,35 +65,6 @@ __device__ __forceinline__ int slot_rank(const Pool& pool, int slot) {
   const int r = pool.ranks[slot];
   return r < 0 ? 0 : (r > pool.rank ? pool.rank : r);
 }
-
-// Eight elements of a factor in a row, as they lie and as bf16.
-template <typename F>
-struct Factor;
-template <>
-struct Factor<__bf16> {
-  static constexpr uint32_t kSize = 2;
-  typedef u32x4 raw_t;
-  static __device__ __forceinline__ raw_t load(__amdgpu_buffer_rsrc_t b, uint32_t at, int more) {
-    return __builtin_amdgcn_raw_buffer_load_b128(b, at, more, 0);
-  }
-  static __device__ __forceinline__ u32x4 bf16(raw_t v) { return v; }
-};
-template <>
-struct Factor<float> {
-  static constexpr uint32_t kSize = 4;
-  struct raw_t {
-    u32x4 lo, hi;
-  };
-  static __device__ __forceinline__ raw_t load(__amdgpu_buffer_rsrc_t b, uint32_t at, int more) {
-    return raw_t{__builtin_amdgcn_raw_buffer_load_b128(b, at, more, 0), __builtin_amdgcn_raw_buffer_load_b128(b, at, more + 16, 0)};
-  }
-  static __device__ __forceinline__ u32x4 bf16(raw_t v) {
-    bf16x8 o;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[j] = static_cast<__bf16>(__uint_as_float(j < 4 ? v.lo[j & 3] : v.hi[j & 3]));
-    return __builtin_bit_cast(u32x4, o);
-  }
-};
 
 // The place of a slot among those with tokens.
 __device__ __forceinline__ int64_t used_place(const PlanView& p, int slot) {
@@ -162,11 +133,20 @@ __device__ __forceinline__ void prepare_slot(const Prepare& q, int64_t i, int sl
     *reinterpret_cast<bf16x8*>(q.At + (place * cols + c) * rp + e) = e < r ? pool_eight(A, e * cols + c, cols, r - e) : zero;
   }
 }
+__device__ __forceinline__ void zero_slot(float* out, int64_t n, int64_t i, int64_t threads) {
+  for (; i < n; i += threads) out[i] = 0.f;
+}
 __device__ __forceinline__ void prepare_job(const Prepare& q, uint32_t wg, int threads, const PlanView& plan, const Pool& pool) {
   const int slot = wg / q.wgs;
   const int4 info = *reinterpret_cast<const int4*>(plan.info);
-  if (info.z != plan.n || info.w != plan.slots || plan.slot_used[slot + 1] == plan.slot_used[slot]) return;
-  const int64_t i = static_cast<int64_t>(wg % q.wgs) * threads + threadIdx.x, place = used_place(plan, slot);
+  if (info.z != plan.n || info.w != plan.slots) return;
+  const int64_t i = static_cast<int64_t>(wg % q.wgs) * threads + threadIdx.x;
+  if (plan.slot_used[slot + 1] == plan.slot_used[slot]) {
+    if (q.dB != nullptr) zero_slot(q.dB + slot * (q.rows * pool.rank), q.rows * pool.rank, i, static_cast<int64_t>(q.wgs) * threads);
+    if (q.dB != nullptr) zero_slot(q.dA + slot * (q.cols * pool.rank), q.cols * pool.rank, i, static_cast<int64_t>(q.wgs) * threads);
+    return;
+  }
+  const int64_t place = used_place(plan, slot);
   if (pool.dt == LOFTQ_BF16) prepare_slot<__bf16>(q, i, slot, place, pool);
   else prepare_slot<float>(q, i, slot, place, pool);
 }
@@ -175,74 +155,94 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Prepare q, PlanView p
 }
 
 // ---- thin product over the features: a K range's part of keep(L) F^T ----
-// A workgroup takes a tile and one range, which its eight waves share in runs of D steps of 32, D steps'
-// loads in flight all the time.  A wave multiplies all of the tile's tokens: what bounds it is the
-// number of loads, and a row of F serves 64 tokens so (16 tokens a wave, each with its own loads of F: 54
-// instead of 38 us at 2048 tokens of 11008 + 4096 columns, rank 64).  The waves' sums meet in LDS.
+// A workgroup takes a tile and one range, whose steps of 64 its eight waves take in turn.  A wave multiplies
+// all of the tile's tokens, so that a row of F serves 64 of them.  Its loads are whole 128-byte lines
+// (eight lanes a row; in the order of the matrix cores' operands neighbouring lanes would read
+// neighbouring rows, and a load would take the address unit three times as long), which pass through
+// the wave's share of LDS into operands while the next step's are in flight: 16-byte piece c of row i
+// lies at place c ^ (i / 2 % 8), so that any 16 rows read at one k meet every bank once.  The waves' sums
+// meet in LDS.
+constexpr int kDownStep = 64;
+
 template <int NT, int MT, typename F, bool kWide>
 __device__ __forceinline__ void down_job(const AdapterDown& jb, int tile, int q, const TileInfo& t, const PlanView& plan,
-                                         const Pool& pool, float* part) {
-  constexpr int D = MT == 4 ? 2 : 4;
+                                         const Pool& pool, char* lds) {
+  constexpr int XL = 2 * MT, FL = NT * static_cast<int>(sizeof(F)), kRowLanes = sizeof(F) == 2 ? 8 : 16;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), li = lane & 15, lg = lane >> 4;
   const int64_t K = jb.K, place = static_cast<int64_t>(tile) * kTile;
-  const int steps = static_cast<int>((K + 31) / 32), per = (steps + jb.ks - 1) / jb.ks;
+  const int width = static_cast<int>(K), steps = (width + kDownStep - 1) / kDownStep, per = (steps + jb.ks - 1) / jb.ks;
   const int begin = q * per, end = begin + per < steps ? begin + per : steps;
-  const int r = slot_rank(pool, t.slot), width = static_cast<int>(K);
+  const int r = slot_rank(pool, t.slot);
   const uint32_t thr = jb.drop.thr;
   const uint64_t key = thr != 0 ? drop_key(jb.drop) : 0;
-  const char* base = static_cast<const char*>(jb.F) + (jb.prepared ? used_place(plan, t.slot) : t.slot) * jb.slot_elems * Factor<F>::kSize;
-  const int l_records = records_of(static_cast<int64_t>(plan.n) * K * 2), f_records = records_of(r * K * Factor<F>::kSize);
-  int64_t row[MT];         // this lane's first element of a token
-  uint32_t offset[MT];     // in bytes, of a tensor of less than 2^31
-  uint64_t word[MT];       // of the mask: the generator's state there
+  const char* base = static_cast<const char*>(jb.F) + (jb.prepared ? used_place(plan, t.slot) : t.slot) * jb.slot_elems * sizeof(F);
+  const int l_records = records_of(static_cast<int64_t>(plan.n) * K * 2), f_records = records_of(r * K * static_cast<int>(sizeof(F)));
+  // load i: row 8 i + lane / 8 of the tile, piece lane % 8 of its 128 bytes
+  int64_t row[XL];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    row[m] = token_at(plan, place + 16 * m + li) * K + 8 * lg;
-    offset[m] = 16 * m + li < t.count ? static_cast<uint32_t>(row[m]) * 2 : kNowhere;
-    word[m] = key + ((static_cast<uint64_t>(row[m]) >> 2) + 1) * kMixGamma;
-  }
-  uint32_t fat[NT];
+  for (int i = 0; i < XL; ++i) row[i] = token_at(plan, place + 8 * i + lane / 8) * K + 8 * (lane % 8);
+  uint64_t word[MT];   // of the mask: the generator's state for this lane's operands' first element
 #pragma unroll
-  for (int p = 0; p < NT; ++p) fat[p] = static_cast<uint32_t>((16 * p + li) * K + 8 * lg) * Factor<F>::kSize;
+  for (int m = 0; m < MT; ++m)
+    word[m] = thr != 0 ? key + ((static_cast<uint64_t>(token_at(plan, place + 16 * m + li) * K + 8 * lg) >> 2) + 1) * kMixGamma : 0;
+  char* xs = lds + w * ((MT + NT) * 2048);
+  char* fs = xs + MT * 2048;
+  u32x4 x[XL], f[FL];
+  auto load = [&](int step) __attribute__((always_inline)) {
+    const int k0 = step * kDownStep;
+    const bool any = step < end, live = k0 + 8 * (lane % 8) < width, flive = k0 + (kDownStep / kRowLanes) * (lane % kRowLanes) < width;
+    const __amdgpu_buffer_rsrc_t xb = buffer_with(jb.L, any ? l_records : 0), fb = buffer_with(base, any ? f_records : 0);
+#pragma unroll
+    for (int i = 0; i < XL; ++i) {
+      if constexpr (kWide) {
+        x[i] = u32x4{0u, 0u, 0u, 0u};
+        if (any && live) x[i] = *reinterpret_cast<const u32x4*>(jb.L + row[i] + k0);
+      } else {
+        x[i] = __builtin_amdgcn_raw_buffer_load_b128(xb, live ? static_cast<uint32_t>(row[i]) * 2 : kNowhere, k0 * 2, 0);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < FL; ++i) {
+      const uint32_t at = static_cast<uint32_t>((64 / kRowLanes * i + lane / kRowLanes) * width) * sizeof(F) + 16 * (lane % kRowLanes);
+      f[i] = __builtin_amdgcn_raw_buffer_load_b128(fb, flive ? at : kNowhere, k0 * static_cast<int>(sizeof(F)), 0);
+    }
+  };
   f32x4 acc[MT][NT];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int p = 0; p < NT; ++p) acc[m][p] = f32x4{0.f, 0.f, 0.f, 0.f};
-  u32x4 x[D][MT];
-  typename Factor<F>::raw_t f[D][NT];
-  auto load = [&](int set, int step) __attribute__((always_inline)) {
-    const int k0 = step * 32;
-    const bool any = step < end, live = k0 + 8 * lg < width;
-    const __amdgpu_buffer_rsrc_t fb = buffer_with(base, any ? f_records : 0);
+  load(begin + w);
+  for (int step = begin + w; step < end; step += kDownWaves) {
+    const int at = (lane % 8 ^ (lane / 16 & 7)) << 4;   // row / 2 % 8 of row 8 i + lane / 8 is (4 i + lane / 16) % 8
 #pragma unroll
-    for (int p = 0; p < NT; ++p) f[set][p] = Factor<F>::load(fb, live ? fat[p] : kNowhere, k0 * static_cast<int>(Factor<F>::kSize));
-    if constexpr (kWide) {
+    for (int i = 0; i < XL; ++i)
+      *reinterpret_cast<u32x4*>(xs + (8 * i + lane / 8) * 128 + (at ^ ((4 * i & 7) << 4))) = x[i];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        x[set][m] = u32x4{0u, 0u, 0u, 0u};
-        if (any && live && 16 * m + li < t.count) x[set][m] = *reinterpret_cast<const u32x4*>(jb.L + row[m] + k0);
+    for (int i = 0; i < FL; ++i) {
+      if constexpr (sizeof(F) == 2) {
+        *reinterpret_cast<u32x4*>(fs + (8 * i + lane / 8) * 128 + (at ^ ((4 * i & 7) << 4))) = f[i];
+      } else {   // four ranks' rows a load, 16 lanes of four values each
+        const int frow = 4 * i + lane / 16, piece = lane % 16 / 2;
+        bf16x4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = static_cast<__bf16>(__uint_as_float(f[i][j]));
+        *reinterpret_cast<bf16x4*>(fs + frow * 128 + ((piece ^ (frow >> 1 & 7)) << 4) + (lane & 1) * 8) = o;
       }
-    } else {
-      const __amdgpu_buffer_rsrc_t xb = buffer_with(jb.L, any ? l_records : 0);
-#pragma unroll
-      for (int m = 0; m < MT; ++m) x[set][m] = __builtin_amdgcn_raw_buffer_load_b128(xb, live ? offset[m] : kNowhere, k0 * 2, 0);
     }
-    __builtin_amdgcn_sched_barrier(0);   // steps in the order in which they are waited for
-  };
+    __builtin_amdgcn_wave_barrier();   // a wave's own share: its reads come after its writes
+    load(step + kDownWaves);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-  for (int d = 0; d < D; ++d) load(d, begin + w * D + d);
-  for (int s0 = begin + w * D; s0 < end; s0 += kDownWaves * D) {
-#pragma unroll
-    for (int d = 0; d < D; ++d) {
+    for (int h = 0; h < kDownStep / 32; ++h) {
       u32x4 b[NT];
 #pragma unroll
-      for (int p = 0; p < NT; ++p) b[p] = Factor<F>::bf16(f[d][p]);
+      for (int p = 0; p < NT; ++p) b[p] = *reinterpret_cast<const u32x4*>(fs + (16 * p + li) * 128 + (((4 * h + lg) ^ (li >> 1 & 7)) << 4));
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        u32x4 v = x[d][m];
-        if (thr != 0) {   // eight words of the mask a step
-          const uint64_t z = word[m] + static_cast<uint64_t>(s0 + d) * (8 * kMixGamma);
+        u32x4 v = *reinterpret_cast<const u32x4*>(xs + (16 * m + li) * 128 + (((4 * h + lg) ^ (li >> 1 & 7)) << 4));
+        if (thr != 0) {   // 16 words of the mask a step
+          const uint64_t z = word[m] + static_cast<uint64_t>(2 * step + h) * (8 * kMixGamma);
           const uint64_t w0 = mix64(z), w1 = mix64(z + kMixGamma);
           v[0] = drop_pair(v[0], w0, 0, thr);
           v[1] = drop_pair(v[1], w0, 2, thr);
@@ -252,12 +252,13 @@ __device__ __forceinline__ void down_job(const AdapterDown& jb, int tile, int q,
 #pragma unroll
         for (int p = 0; p < NT; ++p) acc[m][p] = mfma16(v, b[p], acc[m][p]);
       }
-      __builtin_amdgcn_sched_barrier(0);
-      load(d, s0 + d + kDownWaves * D);
     }
+    __builtin_amdgcn_wave_barrier();
   }
   // the upper half of the waves parks its sums and the lower half adds them, until one is left
+  float* part = reinterpret_cast<float*>(lds);
   auto at = [&](int wave, int m, int p, int v) { return (((wave * MT + m) * NT + p) * 4 + v) * 64 + lane; };
+  __syncthreads();
 #pragma unroll
   for (int left = kDownWaves / 2; left >= 1; left /= 2) {
     if (w >= left && w < 2 * left)
@@ -292,7 +293,8 @@ __device__ __forceinline__ void down_job(const AdapterDown& jb, int tile, int q,
 
 template <int NT, typename F, bool kWide>
 __global__ __launch_bounds__(kDownThreads) void down_kernel(AdapterDownJobs jobs, Prepare prepare, PlanView plan, Pool pool) {
-  __shared__ float part[kDownWaves / 2 * 4 * NT * 4 * 64];
+  // the waves' steps; four waves' sums, 4 NT KiB each, take no more
+  __shared__ __align__(16) char lds[kDownWaves * (4 + NT) * 2048];
   uint32_t wg = blockIdx.x;
   const int which = wg < jobs.job[0].wgs ? 0 : 1;
   if (which == 1) wg -= jobs.job[0].wgs;
@@ -304,13 +306,18 @@ __global__ __launch_bounds__(kDownThreads) void down_kernel(AdapterDownJobs jobs
   const int q = wg % jb.ks, tile = wg / jb.ks;
   const TileInfo t = tile_info(plan, tile);
   if (t.slot < 0 || t.count == 0) return;
-  if (t.count <= 16) down_job<NT, 1, F, kWide>(jb, tile, q, t, plan, pool, part);
-  else down_job<NT, 4, F, kWide>(jb, tile, q, t, plan, pool, part);
+  if (t.count <= 16) down_job<NT, 1, F, kWide>(jb, tile, q, t, plan, pool, lds);
+  else down_job<NT, 4, F, kWide>(jb, tile, q, t, plan, pool, lds);
 }
 
 // ---- the sum of the partials, and its pieces rank-major ----
-__global__ __launch_bounds__(kThreads) void sum_kernel(AdapterSumJobs jobs, PlanView plan, int rp) {
+__global__ __launch_bounds__(kThreads) void sum_kernel(AdapterSumJobs jobs, Prepare prepare, unsigned sums, PlanView plan, Pool pool) {
   __shared__ __align__(4) __bf16 turned[3 * 16][32 + 2];
+  const int rp = pool.rp;
+  if (blockIdx.x >= sums) {
+    if (blockIdx.y == 0) prepare_job(prepare, blockIdx.x - sums, kThreads, plan, pool);
+    return;
+  }
   const AdapterSum& jb = jobs.job[blockIdx.y];
   if (jb.partials == nullptr) return;
   const int parts = rp / 16, p0 = static_cast<int>(blockIdx.x % parts) * 16;
@@ -609,9 +616,13 @@ __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, con
   uint32_t token[2][8];
   const uint32_t width = static_cast<uint32_t>(F), bat = static_cast<uint32_t>(li * places + 8 * lg) * 2;
   const int l_records = records_of(static_cast<int64_t>(plan.n) * F * 2);
-  auto load = [&](int set, int s) __attribute__((always_inline)) {
+  int4 lo, hi;   // the next step's tokens, loaded a step before they are wanted
+  auto load_rows = [&](int s) __attribute__((always_inline)) {
     const int32_t* rows = plan.rows + place0 + 32 * static_cast<int64_t>(s < steps ? s : steps - 1) + 8 * lg;
-    const int4 lo = *reinterpret_cast<const int4*>(rows), hi = *reinterpret_cast<const int4*>(rows + 4);
+    lo = *reinterpret_cast<const int4*>(rows);
+    hi = *reinterpret_cast<const int4*>(rows + 4);
+  };
+  auto load = [&](int set, int s) __attribute__((always_inline)) {
     const int t[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) token[set][i] = static_cast<unsigned>(t[i]) < static_cast<unsigned>(plan.n) ? t[i] : 0;
@@ -623,6 +634,7 @@ __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, con
       else
         x[set][i] = __builtin_amdgcn_raw_buffer_load_b128(xb, (token[set][i] * width + static_cast<uint32_t>(f)) * 2, 0, 0);
     }
+    load_rows(s + kWaves);
   };
   auto load_s = [&](int s) __attribute__((always_inline)) {
 #pragma unroll
@@ -656,6 +668,7 @@ __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, con
     }
   };
   if (w < steps) {
+    load_rows(w);
     load(0, w);
     for (int s = w; s < steps; s += 2 * kWaves) {
       load_s(s);
@@ -735,7 +748,7 @@ __global__ __launch_bounds__(kThreads, 2) void grad_kernel(AdapterGradJobs jobs,
     grad_job<NT, true, kWide>(jobs.job[1], blockIdx.x - first, plan, pool, part);
 }
 
-// gain times the sum of a slot's partials in chunk order; zeros without tokens
+// gain times the sum of the partials of a slot with several chunks, in their order; zeros for a batch without tokens
 __global__ __launch_bounds__(kThreads) void grad_sum_kernel(AdapterGradJobs jobs, PlanView plan, Pool pool, uint32_t first) {
   const bool rank_major = blockIdx.x >= first;
   const AdapterGrad& jb = jobs.job[rank_major ? 1 : 0];
@@ -746,7 +759,7 @@ __global__ __launch_bounds__(kThreads) void grad_sum_kernel(AdapterGradJobs jobs
     if (info.z != plan.n || info.w != plan.slots) return;
     chunk = plan.slot_chunks[slot];
     chunks = plan.slot_chunks[slot + 1] - chunk;
-    if (chunks == 1 || chunk < 0 || chunks < 0 || chunk + chunks > plan.max_chunks) return;
+    if (chunks < 2 || chunk < 0 || chunk + chunks > plan.max_chunks) return;
   }
   const int64_t i = (static_cast<int64_t>(blockIdx.x - (rank_major ? first : 0)) * kThreads + threadIdx.x) * 4, nf = jb.nf, all = nf * R;
   if (i >= all) return;
@@ -788,7 +801,7 @@ unsigned blocks_for(int64_t threads) { return static_cast<unsigned>((threads + k
 // tokens of 11008 + 4096 columns at rank 64: 37 us with 256, 48 with 550); each range has a step for every wave
 int splits_for(int64_t tiles, int64_t K, int rp) {
   int64_t ks = 1024 / (rp / 16) / tiles;
-  const int64_t most = (K + 31) / 32 / kDownWaves;
+  const int64_t most = (K + kDownStep - 1) / kDownStep / kDownWaves;
   if (ks > most) ks = most;
   return static_cast<int>(ks < 1 ? 1 : (ks > 16 ? 16 : ks));
 }
@@ -851,17 +864,22 @@ hipError_t launch_adapters_down(AdapterDownJobs jobs, loftq_dtype_t factor, cons
   return hipGetLastError();
 }
 
-hipError_t launch_adapters_sum(AdapterSumJobs jobs, const PlanView& plan, int rp, hipStream_t s) {
-  LQ_LAUNCH("adapters_sum", sum_kernel, dim3(static_cast<unsigned>(2 * plan.max_tiles * (rp / 16)), 2), dim3(kThreads), 0, s,
-            jobs, plan, rp);
+hipError_t launch_adapters_sum(AdapterSumJobs jobs, const Prepare& prepare, const PlanView& plan, const Pool& pool, hipStream_t s) {
+  Prepare q = prepare;
+  q.wgs = prepare_wgs(q, pool, kThreads);
+  const unsigned sums = static_cast<unsigned>(2 * plan.max_tiles * (pool.rp / 16));
+  LQ_LAUNCH("adapters_sum", sum_kernel, dim3(sums + q.wgs * pool.slots, jobs.job[1].partials != nullptr ? 2 : 1), dim3(kThreads), 0, s,
+            jobs, q, sums, plan, pool);
   return hipGetLastError();
 }
 
 hipError_t launch_adapters_up(const AdapterUp& u, const PlanView& plan, const Pool& pool, hipStream_t s) {
   const int64_t blocks = (u.features + 63) / 64, size = u.odt == LOFTQ_BF16 ? 2 : 4;
-  // about 2048 workgroups, each wave with a block at least
-  int64_t span = tiles_of(plan.n, plan.slots) * blocks / 2048 / 4 * 4;
-  span = span < 4 ? 4 : (span > 64 ? 64 : span);
+  // about 2048 workgroups; where 512 remain each wave has two blocks, so that one's loads pass over the other (2048 tokens
+  // x 11008, rank 64: 50 us with one, 48 with two; 2048 x 4096 has too few: 20 and 21)
+  const int64_t work = tiles_of(plan.n, plan.slots) * blocks, least = work / 8 >= 512 ? 8 : 4;
+  int64_t span = work / 2048 / 4 * 4;
+  span = span < least ? least : (span > 64 ? 64 : span);
   const unsigned parts = static_cast<unsigned>((blocks + span - 1) / span);
   const dim3 grid(static_cast<unsigned>(plan.max_tiles) * parts), block(kThreads);
   const bool whole = u.features % (16 / size) == 0 && plan.n * u.features * size < (int64_t(1) << 31), mask = u.drop.thr != 0;

@@ -12,6 +12,7 @@ namespace {
 typedef int64_t i64;
 
 constexpr i64 kMostTokens = i64(1) << 25, kMostWidth = i64(1) << 22, kMostWorkgroups = i64(1) << 22;
+constexpr i64 kFewAdapterTokens = 256;
 
 struct Arena {
   char* base;
@@ -43,6 +44,7 @@ bool sizes_ok(i64 n, i64 rows, i64 cols, int slots, int rank, bool backward) {
 
 struct ForwardSpace {
   float* partials;   // of X A^T
+  float* H;          // their sum
   __bf16* Bp;        // B in bf16 rows of whole 16 ranks, unless it is read as it lies
   int ks;
   size_t bytes;
@@ -53,6 +55,7 @@ ForwardSpace forward_space(void* ws, i64 n, i64 rows, i64 cols, int slots, int r
   const int rp = rank_pad(rank);
   f.ks = adapters_down_splits(n, slots, cols, rp);
   f.partials = a.take<float>(adapters_down_floats_bound(n, slots, cols, rp));
+  f.H = a.take<float>(plan_layout(n, slots).max_tiles * kTile * rp);
   f.Bp = a.take<__bf16>(used_slots(n, slots) * rows * rp);
   f.bytes = a.used;
   return f;
@@ -174,10 +177,15 @@ loftq_status_t loftq_adapters_forward(const void* X, int64_t n_tok, int64_t rows
   prepare.Bp = as_it_lies ? nullptr : f.Bp;
   prepare.rows = rows;
   prepare.cols = cols;
-  LQ_TRY(launch_adapters_down(AdapterDownJobs{{{}, {static_cast<const __bf16*>(X), cols, ad->A, ad->rank * cols, false, f.partials, f.ks, 0, d}}},
-                              ad->dt, prepare, view, pool, s));
-  AdapterUp up{f.partials, f.ks, rows, as_it_lies ? static_cast<const __bf16*>(ad->B) : f.Bp, as_it_lies ? ad->rank : pool.rp,
-               !as_it_lies, Y0, Y, ydt, none};
+  // Many tokens: the partials are added once, beside the making of B's form, and not by every workgroup that reads
+  // them (2048 tokens, rank 64 in fp32: 84 us without); few tokens save the launch.
+  const bool added = n_tok > kFewAdapterTokens;
+  AdapterDownJobs down{};
+  down.job[1] = AdapterDown{static_cast<const __bf16*>(X), cols, ad->A, ad->rank * cols, false, f.partials, f.ks, 0, d};
+  LQ_TRY(launch_adapters_down(down, ad->dt, added ? Prepare{} : prepare, view, pool, s));
+  if (added) LQ_TRY(launch_adapters_sum(AdapterSumJobs{{{f.partials, f.ks, f.H, nullptr}, {}}}, prepare, view, pool, s));
+  AdapterUp up{added ? f.H : f.partials, added ? 1 : f.ks, rows, as_it_lies ? static_cast<const __bf16*>(ad->B) : f.Bp,
+               as_it_lies ? ad->rank : pool.rp, !as_it_lies, Y0, Y, ydt, none};
   return from_hip(launch_adapters_up(up, view, pool, s));
 }
 
@@ -223,6 +231,8 @@ loftq_status_t loftq_adapters_backward(const void* dY, const void* X, int64_t n_
   prepare.Bt = f.Bt;
   prepare.Ab = dB && !a_as_it_lies ? f.Ab : nullptr;
   prepare.At = dX ? f.At : nullptr;
+  prepare.dB = dB;
+  prepare.dA = dA;
   prepare.rows = rows;
   prepare.rows8 = rows8;
   prepare.cols = cols;
@@ -236,11 +246,11 @@ loftq_status_t loftq_adapters_backward(const void* dY, const void* X, int64_t n_
     sum.job[1] = AdapterSum{f.down_h, f.ks_h, nullptr, f.Ht};
   }
   LQ_TRY(launch_adapters_down(down, LOFTQ_BF16, Prepare{}, view, pool, s));
-  LQ_TRY(launch_adapters_sum(sum, view, pool.rp, s));
+  LQ_TRY(launch_adapters_sum(sum, Prepare{}, view, pool, s));
   if (dB) {
     const AdapterGradJobs grad{{{G, f.Ht, f.grad_b, dB, rows8, rows, none}, {Xb, f.Pt, f.grad_a, dA, cols, cols, d}}};
     LQ_TRY(launch_adapters_grad(grad, view, pool, s));
-    LQ_TRY(launch_adapters_grad_sum(grad, view, pool, s));
+    if (n_tok > plan_layout(n_tok, ad->slots).chunk_tiles * kTile) LQ_TRY(launch_adapters_grad_sum(grad, view, pool, s));
   }
   if (!dX) return LOFTQ_OK;
   return from_hip(launch_adapters_up(AdapterUp{f.P, 1, cols, f.At, pool.rp, true, dX0, dX, xdt, d}, view, pool, s));
