@@ -20,7 +20,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
-constexpr uint32_t kNowhere = 0x7FFFFFFFu;   // an offset past every resource: loads give zeros
+constexpr uint32_t kNowhere = 0x7FFFFFFFu;   // an offset past every resource, also with a row's length added: loads give zeros
 
 __device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -503,8 +503,10 @@ __device__ __forceinline__ void up_blocks(const AdapterUp& u, const PlanView& pl
             v[4 * e + i] = static_cast<O>(add ? fmaf(g, x[i], old) : old);
           }
         }
-        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), to, block * 64u + n_lane < N ? offset[m][c] : kNowhere,
-                                               block * 64 * static_cast<int>(sizeof(O)), 0);
+        // The block's offset is in the lanes' address and not in a scalar: behind a 16-byte store with a scalar offset the
+        // compiler leaves no wait before the next write of the data's registers, and that write has been stored instead.
+        const uint32_t at = offset[m][c] + static_cast<uint32_t>(block * 64) * static_cast<uint32_t>(sizeof(O));
+        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4, v), to, block * 64u + n_lane < N ? at : kNowhere, 0, 0);
       }
       __builtin_amdgcn_wave_barrier();
       load_y(m, block + 4);

@@ -178,6 +178,21 @@ def test_longer(lib, n, rows, cols, slots, rank):
     b.check_backward(b.backward(lib, dtype=torch.float32, **rng), **rng)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,rows,cols,slots,rank", [(2048, 11008, 64, 8, 64), (2050, 64, 11008, 3, 16), (1030, 11004, 4104, 2, 24),
+                                                    (2048, 11008, 128, 4, 32)])
+def test_many_features(lib, n, rows, cols, slots, rank, dtype):
+    """A wave takes several blocks of features, and several steps of the first product, in a loop."""
+    b = Batch(n, rows, cols, slots, rank, ids="runs", ranks=rank == 64, seed=n + rows)
+    plan, rng = b.plan(lib), dict(p=0.1, seed=5, offset=6)
+    Y, grads = b.forward(lib, plan, dtype=dtype, **rng), b.backward(lib, plan, dtype=dtype, **rng)
+    b.check_forward(Y, **rng)
+    b.check_backward(grads, **rng)
+    for _ in range(3):
+        again = (b.forward(lib, plan, dtype=dtype, **rng), *b.backward(lib, plan, dtype=dtype, **rng))
+        assert all(torch.equal(x, y) for x, y in zip(again, (Y, *grads)))
+
+
 def test_everything_dropped(lib):
     b = Batch(70, 64, 128, 3, 8, seed=2)
     rng = dict(p=1.0, seed=3, offset=1)
