@@ -325,12 +325,12 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(AdapterSumJobs jobs, Prep
   const TileInfo t = tile_info(plan, tile);
   if (t.slot < 0) return;
   const int64_t places = static_cast<int64_t>(plan.max_tiles) * kTile, place = static_cast<int64_t>(tile) * kTile + half * 32;
+  const int r = slot_rank(pool, t.slot);
 #pragma unroll
   for (int i = threadIdx.x; i < 32 * 16; i += kThreads) {
     const int tok = i / 16, p = p0 + i % 16;
-    float x = 0.f;
-    if (half * 32 + tok < t.count)
-    {
+    float x = 0.f;   // past the slot's own rank too, where the partials may hold an infinite row's products with zeros
+    if (half * 32 + tok < t.count && p < r) {
       const float* src = jb.partials + (place + tok) * rp + p;
       int q = 0;
       for (; q + 4 <= jb.ks; q += 4) {   // four loads in flight, added in order
@@ -386,6 +386,7 @@ __device__ __forceinline__ void stage_pieces(const AdapterUp& u, const PlanView&
     bf16x4 h[3];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
+      if (p + j >= r) x[j] = 0.f;   // an infinite row's products with the zeros past the slot's rank are NaN
       __bf16 piece[3];
       split3(x[j], piece);
 #pragma unroll
@@ -715,6 +716,7 @@ __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, con
   const int64_t nf = whole ? jb.nf : F;
   const int nr = whole ? pool.rank : 16 * NR;
   const float coef = whole ? pool.gain * (pool.gains != nullptr ? pool.gains[slot] : 1.f) : 1.f;
+  const int r = slot_rank(pool, slot);   // past it zeros, where an infinity of L has met them too
   float* o = whole ? jb.out + slot * (nf * nr) : jb.partials + at_chunk * (F * 16 * NR);
 #pragma unroll
   for (int t = 0; t < NT; ++t)
@@ -722,7 +724,7 @@ __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, con
     for (int v = 0; v < 4; ++v) {
       float y[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = coef * acc[j][t][v];
+      for (int j = 0; j < 8; ++j) y[j] = (tile0 + t) * 16 + (kRankMajor ? 4 * lg + v : li) < r ? coef * acc[j][t][v] : 0.f;
       if constexpr (kRankMajor) {
         const int p = (tile0 + t) * 16 + 4 * lg + v;   // features f0 .. f0 + 7
         if (p < nr && f0 < F)                          // nf == F here, and 8 | F
