@@ -802,8 +802,12 @@ class AdamWTensors:
         count = len(params)
         if count == 0:
             raise ValueError("params must hold a tensor")
+        if len(grads) != count:
+            raise ValueError(f"grads must hold {count} tensors")
         dev = _first(params[0], "params")
         pdt, gdt = _wdtype(params[0]), _wdtype(grads[0])
+        if m is not None and len(m) != count:
+            raise ValueError(f"m must hold {count} tensors")
         if m is not None:
             bits = 32 if m[0].dtype is torch.float32 else 8
         if bits not in (32, 8):
