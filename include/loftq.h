@@ -375,8 +375,9 @@ size_t loftq_adapters_plan_bytes(int64_t n_tok, int32_t slots);
  *   Y     [device] n_tok x rows of dtype ydt out
  *   ws    [device] loftq_adapters_forward_workspace_bytes(n_tok, rows, cols, slots, rank) bytes
  * n_tok = 0 or rows = 0 writes nothing.
- * UNSUPPORTED: cols % 8 != 0, cols = 0, rank > 64, slots > 1024, n_tok >= 2^25, rows or cols >= 2^22, or a
- * launch of 2^22 workgroups (one per 256 rows of n_tok / 64 + min(n_tok, slots + 1) tiles). */
+ * UNSUPPORTED: cols % 8 != 0, cols = 0, rank > 64, slots > 1024, n_tok >= 2^25, rows or cols >= 2^22, a launch
+ * of 2^22 workgroups (one per 256 rows of n_tok / 64 + min(n_tok, slots + 1) tiles), or a pool of 2^31 groups
+ * of eight factor elements (B's, with ranks in whole 16s; for the gradient B's and twice A's). */
 loftq_status_t loftq_adapters_forward(const void* X, int64_t n_tok, int64_t rows, int64_t cols,
                                       const loftq_adapters_t* ad, const int32_t* plan, size_t plan_bytes,
                                       const loftq_dropout_t* drop, const void* Y0, void* Y, loftq_dtype_t ydt, void* ws,

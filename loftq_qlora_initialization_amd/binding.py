@@ -850,7 +850,9 @@ class AdamWTensors:
         self.bits, self.device = bits, params[0].device
         self.table = _scratch(_c_adamw_bytes(descs, count), self.device, stream)
         if stream is not None:   # later steps may run elsewhere
-            self.table.record_stream(torch.cuda.current_stream(self.device))
+            for x in (self.table, *(t for new, tensors in ((m, self.m), (v, self.v), (m_scale, self.m_scale),
+                                                           (v_scale, self.v_scale)) if new is None for t in tensors or ())):
+                x.record_stream(torch.cuda.current_stream(self.device))
         self.plan = LoftqAdamwPlan()
         _call("loftq_adamw_plan", _c_adamw_plan, dev, stream, descs, count, pdt, gdt, bits, self.table.data_ptr(),
               self.table.numel(), ctypes.byref(self.plan))

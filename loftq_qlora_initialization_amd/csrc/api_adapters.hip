@@ -35,7 +35,10 @@ bool sizes_ok(i64 n, i64 rows, i64 cols, int slots, int rank, bool backward) {
   if (!plan_sizes_ok(n, slots) || rank > 64 || rows >= kMostWidth || cols >= kMostWidth || cols == 0 || cols % 8 != 0) return false;
   if (backward && rows == 0) return false;
   const PlanLayout p = plan_layout(n, slots);
-  const i64 features = backward ? cols : rows;
+  const i64 features = backward ? cols : rows, rp = rank_pad(rank);
+  // the threads that make the factors' forms
+  const i64 forms = backward ? pad8(rows) / 8 * rp + 2 * cols * (rp / 8) : rows * (rp / 8);
+  if ((forms + 1024) * slots >= (i64(1) << 31)) return false;
   if (p.max_tiles * ((features + 255) / 256) >= kMostWorkgroups) return false;
   if (!backward) return true;
   if (p.max_chunks * ((pad8(rows) + 127) / 128 + (cols + 127) / 128) >= 2 * kMostWorkgroups) return false;

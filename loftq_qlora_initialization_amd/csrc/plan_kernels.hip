@@ -11,9 +11,19 @@ namespace {
 
 constexpr int kWaves = kPlanThreads / 64;
 
-__device__ __forceinline__ int group_of(const int32_t* slot_of, int64_t i, int slots) {
-  const int s = slot_of[i];
-  return static_cast<unsigned>(s) < static_cast<unsigned>(slots) ? s : slots;
+// The slots of kAhead tokens, `stride` apart from i0 on, with all loads in flight at once; kNone at `end` and past it.
+constexpr int kAhead = 8, kNone = kMostSlots + 1;
+__device__ __forceinline__ void groups_of(const int32_t* slot_of, int64_t i0, int stride, int64_t end, int slots, int (&g)[kAhead]) {
+#pragma unroll
+  for (int e = 0; e < kAhead; ++e) {
+    const int64_t i = i0 + e * stride;
+    g[e] = slot_of[i < end ? i : end - 1];
+  }
+#pragma unroll
+  for (int e = 0; e < kAhead; ++e) {
+    const int in = static_cast<unsigned>(g[e]) < static_cast<unsigned>(slots) ? g[e] : slots;
+    g[e] = i0 + e * stride < end ? in : kNone;
+  }
 }
 
 // tokens by slot of a workgroup's share
@@ -23,7 +33,13 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(const int32_t*
   for (int s = threadIdx.x; s <= p.slots; s += kPlanThreads) hist[s] = 0;
   __syncthreads();
   const int64_t begin = blockIdx.x * p.per_wg, end = begin + p.per_wg < p.n ? begin + p.per_wg : p.n;
-  for (int64_t i = begin + threadIdx.x; i < end; i += kPlanThreads) atomicAdd(&hist[group_of(slot_of, i, p.slots)], 1);
+  for (int64_t i = begin; i < end; i += kAhead * kPlanThreads) {
+    int g[kAhead];
+    groups_of(slot_of, i + threadIdx.x, kPlanThreads, end, p.slots, g);
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e)
+      if (g[e] != kNone) atomicAdd(&hist[g[e]], 1);
+  }
   __syncthreads();
   for (int s = threadIdx.x; s <= p.slots; s += kPlanThreads)
     plan[p.counts + static_cast<int64_t>(blockIdx.x) * (p.slots + 1) + s] = hist[s];
@@ -42,11 +58,17 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
   __shared__ Sums first[kMostSlots + 2];         // a slot's first token, tile and chunk, and the used slots before it
   __shared__ Sums wave_sum[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, groups = p.slots + 1;
-  for (int i = tid; i < kWaves * (kMostSlots + 1); i += kPlanThreads) (&count[0][0])[i] = 0;
+  for (int s = lane; s < groups; s += 64) count[w][s] = 0;
   __syncthreads();
   const int64_t per_wave = p.per_wg / kWaves;
   const int64_t begin = blockIdx.x * p.per_wg + w * per_wave, end = begin + per_wave < p.n ? begin + per_wave : p.n;
-  for (int64_t i = begin + lane; i < end; i += 64) atomicAdd(&count[w][group_of(slot_of, i, p.slots)], 1);
+  for (int64_t i = begin; i < end; i += kAhead * 64) {
+    int g[kAhead];
+    groups_of(slot_of, i + lane, 64, end, p.slots, g);
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e)
+      if (g[e] != kNone) atomicAdd(&count[w][g[e]], 1);
+  }
   __syncthreads();
   // a slot's total, and the place of each wave's first token among the slot's
   const int each = (groups + kPlanThreads - 1) / kPlanThreads, s0 = tid * each;
@@ -54,6 +76,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
   for (int s = s0; s < s0 + each && s < groups; ++s) {
     int before = 0, total = 0;
     if (p.wgs > 1)
+#pragma unroll 8
       for (int b = 0; b < p.wgs; ++b) {
         const int c = plan[p.counts + static_cast<int64_t>(b) * groups + s];
         before += b < static_cast<int>(blockIdx.x) ? c : 0;
@@ -98,10 +121,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
           make_int4(first[groups].tiles, first[groups].chunks, static_cast<int>(p.n), p.slots);
   }
   volatile int* next = count[w];
-  for (int64_t i0 = begin; i0 < end; i0 += 64) {
-    const int64_t i = i0 + lane;
-    const bool live = i < end;
-    const int g = live ? group_of(slot_of, i, p.slots) : kMostSlots + 1;
+  auto place = [&](int64_t i, int g) __attribute__((always_inline)) {
+    const bool live = g != kNone;
     // the lanes with this lane's slot
     uint64_t peers = ~0ull;
 #pragma unroll
@@ -114,7 +135,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
     __builtin_amdgcn_wave_barrier();   // every lane has read before the last of its peers writes
     if (live && (peers >> lane) == 1ull) next[g] = from + rank + 1;
     __builtin_amdgcn_wave_barrier();
-    if (!live) continue;
+    if (!live) return;
     const int k = from + rank, total = first[g + 1].tokens - first[g].tokens;   // the k-th of its slot
     const int tile = first[g].tiles + k / kTile, at = first[g].tokens + k;
     plan[p.order + at] = static_cast<int>(i);
@@ -131,6 +152,13 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
     }
     if (k == total - 1)
       for (int j = k % kTile + 1; j < kTile; ++j) rows[j] = static_cast<int>(i);
+  };
+  for (int64_t i0 = begin; i0 < end; i0 += kAhead * 64) {
+    int g[kAhead];
+    groups_of(slot_of, i0 + lane, 64, end, p.slots, g);
+#pragma unroll
+    for (int e = 0; e < kAhead; ++e)
+      if (i0 + e * 64 < end) place(i0 + e * 64 + lane, g[e]);   // the whole wave
   }
 }
 

@@ -87,6 +87,15 @@ def test_outputs(b):
     assert bwd(b, n=0, dB=None, dA=None) == OK and bwd(b, n=0, dX=None, dB=None, dA=None) == OK
 
 
+def test_pools_of_more_factors_than_a_launch_takes(b):
+    wide = dict(rows=(1 << 22) - 8, cols=(1 << 22) - 8)
+    assert fwd(b, **wide, ad=pool(b, slots=1024, rank=1)) == UNSUPPORTED
+    assert bwd(b, **wide, ad=pool(b, slots=1024, rank=1)) == UNSUPPORTED
+    assert b.adapters_forward_workspace_bytes(16, wide["rows"], 64, 1024, 1) == 0
+    assert b.adapters_backward_workspace_bytes(16, 64, wide["cols"], 1024, 1) == 0
+    assert b.adapters_forward_workspace_bytes(16, wide["rows"], 64, 128, 1) > 0
+
+
 QUERIES = ["adapters_forward_workspace_bytes", "adapters_backward_workspace_bytes"]
 
 
