@@ -233,13 +233,17 @@ loftq_status_t loftq_adapters_backward(const void* dY, const void* X, int64_t n_
   Prepare prepare{};
   prepare.Bt = f.Bt;
   prepare.Ab = dB && !a_as_it_lies ? f.Ab : nullptr;
-  prepare.At = dX ? f.At : nullptr;
   prepare.dB = dB;
   prepare.dA = dA;
   prepare.rows = rows;
   prepare.rows8 = rows8;
   prepare.cols = cols;
   LQ_TRY(launch_adapters_prepare(prepare, view, pool, s));
+  Prepare later{};   // A's columns are wanted last: their form is made beside the sums
+  later.At = dX ? f.At : nullptr;
+  later.rows = rows;
+  later.rows8 = rows8;
+  later.cols = cols;
   // P = G B for dX and dA, H = keep(X) A^T for dB
   AdapterDownJobs down{{{G, rows8, f.Bt, pool.rp * rows8, true, f.down_p, f.ks_p, 0, none}, {}}};
   AdapterSumJobs sum{{{f.down_p, f.ks_p, dX ? f.P : nullptr, dB ? f.Pt : nullptr}, {}}};
@@ -249,7 +253,7 @@ loftq_status_t loftq_adapters_backward(const void* dY, const void* X, int64_t n_
     sum.job[1] = AdapterSum{f.down_h, f.ks_h, nullptr, f.Ht};
   }
   LQ_TRY(launch_adapters_down(down, LOFTQ_BF16, Prepare{}, view, pool, s));
-  LQ_TRY(launch_adapters_sum(sum, Prepare{}, view, pool, s));
+  LQ_TRY(launch_adapters_sum(sum, later, view, pool, s));
   if (dB) {
     const AdapterGradJobs grad{{{G, f.Ht, f.grad_b, dB, rows8, rows, none}, {Xb, f.Pt, f.grad_a, dA, cols, cols, d}}};
     LQ_TRY(launch_adapters_grad(grad, view, pool, s));

@@ -291,3 +291,27 @@ def test_binding_checks(lib):
                 dict(max_norm=-1.0), dict(max_norm=float("inf")), dict(norm=torch.zeros((), device="cuda"))):
         with pytest.raises(lib.LoftqError):
             lib.loftq_adamw(t, **{"lr": 0.1, **how})
+
+
+def test_binding_refuses_lists_of_another_length(lib):
+    p, g = ([torch.zeros(8, device="cuda") for _ in range(2)] for _ in range(2))
+    for grads, more in ((g[:1], {}), ([], {}), (g, dict(m=[], v=g)), (g, dict(m=g[:1], v=g)), (g, dict(m=g, v=g[:1])),
+                        (g, dict(copies=[]))):
+        with pytest.raises(ValueError):
+            lib.AdamWTensors(p, grads, **more)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_states_made_on_another_stream(lib, bits):
+    """The states that the tensors make for themselves, on a stream that is not the steps'."""
+    p = [torch.ones(5000, device="cuda"), torch.ones(3, device="cuda")]
+    q, g = [x.clone() for x in p], [torch.full_like(x, 0.5) for x in p]
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    a = lib.AdamWTensors(p, g, bits=bits, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    b = lib.AdamWTensors(q, g, bits=bits)
+    for t in (1, 2):
+        lib.loftq_adamw(a, lr=0.1, t=t)
+        lib.loftq_adamw(b, lr=0.1, t=t)
+    assert all(torch.equal(x, y) and not torch.equal(x, torch.ones_like(x)) for x, y in zip(p, q))
