@@ -411,15 +411,16 @@ size_t loftq_adapters_backward_workspace_bytes(int64_t n_tok, int64_t rows, int6
  *                         c = 1 without max_norm
  *   m = b1 m + (1 - b1) g,   v = b2 v + ((1 - b2) g) g
  *   p = p (1 - l weight_decay) - l / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps),   l = lr lr_scale
- * each operation rounded by itself, but for the last quotient, which is off by up to 2 ulp.  p is
+ * each operation rounded by itself (m and v with states in 8 bits: below), but for the last quotient, which is
+ * off by up to 2 ulp.  p is
  * rounded to its type once.
  *
  * States in 8 bits: blocks of 256 consecutive elements (a tensor's last may be shorter) with an
  * fp32 scale each, m in OCP e4m3 and v in OCP e5m2.  With a the largest magnitude of the block,
- * scale = fl(a / 448) for m and fl(a / 57344) for v, 0 where a < 2^-100; code: fl(x fl(1 / scale))
+ * scale = fl(a / 448) for m and fl(a / 57344) for v (a rounded to fp32), 0 where a < 2^-100; code: x / scale
  * to the nearest, ties to even; a positive v never becomes zero but the smallest code, so that no
- * step divides by eps alone; value = fl(code scale).  The update takes m and v before they are
- * rounded.  A block that holds an infinity or a NaN gets the scale NaN. */
+ * step divides by eps alone; value = code scale.  m and v are formed and coded in fp64, so that no rounding
+ * in between decides a code; p takes fl(m) and fl(v).  A block that holds an infinity or a NaN gets the scale NaN. */
 typedef struct {
   void* param;          /* [device] n elements of dtype pdt */
   const void* grad;     /* [device] n elements of dtype gdt */

@@ -11,12 +11,12 @@ constexpr int kChunk = 4096;       // elements of a workgroup, all of one tensor
 // Numbers of a step that are the same for every element.
 struct AdamScalars {
   double lr, bias1, root2;   // lr lr_factor; 1 - b1^t; 1 / sqrt(1 - b2^t)
-  float clip;                // c; negative: the step changes nothing
-  int pad;
+  double clip;               // c; negative: the step changes nothing
 };
 
 struct AdamDecays {
-  float b1, c1, b2, c2, eps;   // c = 1 - b
+  double b1, c1, b2, c2;   // c = 1 - b
+  float eps;
 };
 
 // The table: tensors, then the chunks (tensor, number within it), then the steps' scratch.

@@ -102,18 +102,27 @@ __device__ __forceinline__ uint32_t block_amax(const float (&x)[4]) {
   return a;
 }
 // A block's scale for values up to `top`, and its inverse (0 where the scale is 0).
-__device__ __forceinline__ float block_scale(uint32_t amax, float top, float& inverse) {
+__device__ __forceinline__ float block_scale(uint32_t amax, float top, double& inverse) {
   if (amax >= 0x7F800000u) {
-    inverse = __uint_as_float(0x7FC00000u);
-    return inverse;
+    const float nan = __uint_as_float(0x7FC00000u);
+    inverse = nan;
+    return nan;
   }
   if (amax < 0x0D800000u) {   // 2^-100
-    inverse = 0.f;
+    inverse = 0.0;
     return 0.f;
   }
   const float scale = __uint_as_float(amax) / top;
-  inverse = 1.f / scale;
+  inverse = 1.0 / static_cast<double>(scale);
   return scale;
+}
+// x in fp32 with its last bit set where it is not exact, so that rounding to fewer bits afterwards goes by x itself.
+__device__ __forceinline__ float to_odd(double x) {
+  const float f = static_cast<float>(x);
+  const double rest = x - static_cast<double>(f);
+  uint32_t b = __float_as_uint(f);
+  if (rest != 0.0) b = (fabs(static_cast<double>(f)) > fabs(x) ? b - 1 : b) | 1u;   // a NaN's rest is not 0: it stays one
+  return __uint_as_float(b);
 }
 
 // sum of the squares of all gradients, a part per workgroup
@@ -163,10 +172,10 @@ __global__ __launch_bounds__(kThreads) void scalars_kernel(AdamTable t, loftq_ad
   s.lr = step.lr * (step.lr_factor != nullptr ? static_cast<double>(*step.lr_factor) : 1.0);
   s.bias1 = 1.0 - pow(step.beta1, static_cast<double>(at));
   s.root2 = 1.0 / sqrt(1.0 - pow(step.beta2, static_cast<double>(at)));
-  s.clip = 1.f;
+  s.clip = 1.0;
   if (step.max_norm > 0.0) {
     const double c = step.max_norm / (norm + 1e-6);
-    s.clip = !isfinite(norm) ? -1.f : (c < 1.0 ? static_cast<float>(c) : 1.f);
+    s.clip = !isfinite(norm) ? -1.0 : (c < 1.0 ? c : 1.0);
     if (norm_out != nullptr) *norm_out = static_cast<float>(norm);
   }
   *t.scalars = s;
@@ -175,7 +184,7 @@ __global__ __launch_bounds__(kThreads) void scalars_kernel(AdamTable t, loftq_ad
 template <typename P, typename G, bool k8Bit>
 __global__ __launch_bounds__(kThreads) void step_kernel(AdamTable t, AdamScalars host, bool on_device, AdamDecays d) {
   const AdamScalars s = on_device ? *t.scalars : host;
-  if (s.clip < 0.f) return;
+  if (s.clip < 0.0) return;
   const int2 at = t.chunks[blockIdx.x];
   const loftq_adamw_tensor_t x = t.tensors[at.x];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -191,41 +200,50 @@ __global__ __launch_bounds__(kThreads) void step_kernel(AdamTable t, AdamScalars
     float p[4], g[4], m[4], v[4];
     load4<P>(x.param, e, left, p);
     load4<G>(x.grad, e, left, g);
+    double m8[4], v8[4];   // with states in 8 bits: what the codes are the nearest to
     if constexpr (k8Bit) {
       const uint32_t mc = load_codes(x.m, e, left), vc = load_codes(x.v, e, left);
-      const float ms = x.m_scale[block], vs = x.v_scale[block];
-      m[0] = __builtin_amdgcn_cvt_f32_fp8(mc, 0) * ms;
-      m[1] = __builtin_amdgcn_cvt_f32_fp8(mc, 1) * ms;
-      m[2] = __builtin_amdgcn_cvt_f32_fp8(mc, 2) * ms;
-      m[3] = __builtin_amdgcn_cvt_f32_fp8(mc, 3) * ms;
-      v[0] = __builtin_amdgcn_cvt_f32_bf8(vc, 0) * vs;
-      v[1] = __builtin_amdgcn_cvt_f32_bf8(vc, 1) * vs;
-      v[2] = __builtin_amdgcn_cvt_f32_bf8(vc, 2) * vs;
-      v[3] = __builtin_amdgcn_cvt_f32_bf8(vc, 3) * vs;
+      const double ms = x.m_scale[block], vs = x.v_scale[block];
+      m8[0] = __builtin_amdgcn_cvt_f32_fp8(mc, 0) * ms;
+      m8[1] = __builtin_amdgcn_cvt_f32_fp8(mc, 1) * ms;
+      m8[2] = __builtin_amdgcn_cvt_f32_fp8(mc, 2) * ms;
+      m8[3] = __builtin_amdgcn_cvt_f32_fp8(mc, 3) * ms;
+      v8[0] = __builtin_amdgcn_cvt_f32_bf8(vc, 0) * vs;
+      v8[1] = __builtin_amdgcn_cvt_f32_bf8(vc, 1) * vs;
+      v8[2] = __builtin_amdgcn_cvt_f32_bf8(vc, 2) * vs;
+      v8[3] = __builtin_amdgcn_cvt_f32_bf8(vc, 3) * vs;
     } else {
       load4<float>(x.m, e, left, m);
       load4<float>(x.v, e, left, v);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const float gj = s.clip * g[j];
-      m[j] = d.b1 * m[j] + d.c1 * gj;
-      v[j] = d.b2 * v[j] + (d.c2 * gj) * gj;
+      if constexpr (k8Bit) {   // in fp64: a rounding to fp32 in between would move values over the codes' borders
+        const double gj = s.clip * static_cast<double>(g[j]);
+        m8[j] = d.b1 * m8[j] + d.c1 * gj;
+        v8[j] = d.b2 * v8[j] + (d.c2 * gj) * gj;
+        m[j] = static_cast<float>(m8[j]);
+        v[j] = static_cast<float>(v8[j]);
+      } else {
+        const float gj = static_cast<float>(s.clip) * g[j];
+        m[j] = static_cast<float>(d.b1) * m[j] + static_cast<float>(d.c1) * gj;
+        v[j] = static_cast<float>(d.b2) * v[j] + (static_cast<float>(d.c2) * gj) * gj;
+      }
       p[j] = p[j] * shrink - size * (m[j] / (sqrtf(v[j]) * root2 + d.eps));
     }
     store4<P>(x.param, e, left, p);
     if (x.copy != nullptr) store4<__bf16>(x.copy, e, left, p);
     if constexpr (k8Bit) {
-      float mi, vi;   // inverse scales
+      double mi, vi;   // inverse scales
       const float ms = block_scale(block_amax(m), 448.f, mi), vs = block_scale(block_amax(v), 57344.f, vi);
       uint32_t mc = 0, vc = 0;
-      mc = __builtin_amdgcn_cvt_pk_fp8_f32(m[0] * mi, m[1] * mi, mc, false);
-      mc = __builtin_amdgcn_cvt_pk_fp8_f32(m[2] * mi, m[3] * mi, mc, true);
-      vc = __builtin_amdgcn_cvt_pk_bf8_f32(v[0] * vi, v[1] * vi, vc, false);
-      vc = __builtin_amdgcn_cvt_pk_bf8_f32(v[2] * vi, v[3] * vi, vc, true);
+      mc = __builtin_amdgcn_cvt_pk_fp8_f32(to_odd(m8[0] * mi), to_odd(m8[1] * mi), mc, false);
+      mc = __builtin_amdgcn_cvt_pk_fp8_f32(to_odd(m8[2] * mi), to_odd(m8[3] * mi), mc, true);
+      vc = __builtin_amdgcn_cvt_pk_bf8_f32(to_odd(v8[0] * vi), to_odd(v8[1] * vi), vc, false);
+      vc = __builtin_amdgcn_cvt_pk_bf8_f32(to_odd(v8[2] * vi), to_odd(v8[3] * vi), vc, true);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (v[j] > 0.f && vi > 0.f && (vc >> (8 * j) & 255u) == 0) vc |= 1u << (8 * j);
+        if (v[j] > 0.f && vi > 0.0 && (vc >> (8 * j) & 255u) == 0) vc |= 1u << (8 * j);
       store_codes(x.m, e, left, mc);
       store_codes(x.v, e, left, vc);
       if (lane == 0) {
@@ -273,11 +291,10 @@ hipError_t launch_adamw(const loftq_adamw_plan_t& plan, const AdamTable& t, cons
     host.lr = step.lr;
     host.bias1 = 1.0 - std::pow(step.beta1, static_cast<double>(step.t));
     host.root2 = 1.0 / std::sqrt(1.0 - std::pow(step.beta2, static_cast<double>(step.t)));
-    host.clip = 1.f;
+    host.clip = 1.0;
   }
   if (plan.chunks == 0) return hipGetLastError();
-  const AdamDecays d{static_cast<float>(step.beta1), static_cast<float>(1.0 - step.beta1), static_cast<float>(step.beta2),
-                     static_cast<float>(1.0 - step.beta2), static_cast<float>(step.eps)};
+  const AdamDecays d{step.beta1, 1.0 - step.beta1, step.beta2, 1.0 - step.beta2, static_cast<float>(step.eps)};
   const dim3 grid(static_cast<unsigned>(plan.chunks)), block(kThreads);
 #define LQ_STEP(P, G, E) LQ_LAUNCH("adamw_step", (step_kernel<P, G, E>), grid, block, 0, s, t, host, on_device, d)
 #define LQ_STEP_G(P, G)               \

@@ -315,3 +315,36 @@ def test_states_made_on_another_stream(lib, bits):
         lib.loftq_adamw(a, lr=0.1, t=t)
         lib.loftq_adamw(b, lr=0.1, t=t)
     assert all(torch.equal(x, y) and not torch.equal(x, torch.ones_like(x)) for x, y in zip(p, q))
+
+
+@pytest.mark.parametrize("max_norm", [0.0, 0.05])
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+def test_codes_are_the_nearest(lib, grad, max_norm):
+    """Every code of the new states is the one nearest to the moment's quotient in fp64 (ties to the even code): what a
+    rounding to fp32 in between would decide, about one code in 2^17, is not left to it."""
+    a = Model(lib, [300000, 4097], bits=8, grad=grad, seed=31)
+
+    def whole(codes, scale, kind):   # the product of code and scale in fp64: 4 or 3 bits by 24
+        ones = np.ones(scale.numel(), np.float32)
+        return oracle.state_values(codes.view(torch.uint8).cpu().numpy(), ones, kind) * np.repeat(host(scale), 256)[:codes.numel()]
+
+    t = a.tensors
+    before = [(p, host(g), whole(t.m[i], t.m_scale[i], "m"), whole(t.v[i], t.v_scale[i], "v"))
+              for i, (p, g) in enumerate(zip(a.params, a.grads))]
+    norm, clip = oracle.adamw_clip([x[1] for x in before], max_norm) if max_norm else (0.0, 1.0)
+    lib.loftq_adamw(a.tensors, t=3, max_norm=max_norm, **HOW)
+    b1, b2 = HOW["beta1"], HOW["beta2"]
+    for i, (_, g, m0, v0) in enumerate(before):
+        want = dict(m=b1 * m0 + (1 - b1) * (clip * g), v=b2 * v0 + ((1 - b2) * (clip * g)) * (clip * g))
+        for kind, codes, scale in (("m", t.m[i], t.m_scale[i]), ("v", t.v[i], t.v_scale[i])):
+            levels = oracle.state_values(np.arange(127 if kind == "m" else 124, dtype=np.uint8), np.ones(1, np.float32), kind)
+            x, s = want[kind], np.repeat(host(scale), 256)[:g.size]
+            y = np.abs(x / s)
+            at = np.clip(np.searchsorted(levels, y), 1, levels.size - 1)
+            lo, hi = y - levels[at - 1], levels[at] - y
+            code = np.where((lo < hi) | ((lo == hi) & (at % 2 == 1)), at - 1, at)
+            if kind == "v":
+                code = np.where(x > 0, np.maximum(code, 1), code)
+            got = codes.view(torch.uint8).cpu().numpy()
+            assert np.array_equal(got & 127, code)
+            assert np.array_equal(got >= 128, np.signbit(x))
