@@ -412,8 +412,7 @@ size_t loftq_adapters_backward_workspace_bytes(int64_t n_tok, int64_t rows, int6
  *   m = b1 m + (1 - b1) g,   v = b2 v + ((1 - b2) g) g
  *   p = p (1 - l weight_decay) - l / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps),   l = lr lr_scale
  * each operation rounded by itself (m and v with states in 8 bits: below), but for the last quotient, which is
- * off by up to 2 ulp.  p is
- * rounded to its type once.
+ * off by up to 2 ulp.  p is rounded to its type once.
  *
  * States in 8 bits: blocks of 256 consecutive elements (a tensor's last may be shorter) with an
  * fp32 scale each, m in OCP e4m3 and v in OCP e5m2.  With a the largest magnitude of the block,
