@@ -112,7 +112,7 @@ __device__ __forceinline__ float block_scale(uint32_t amax, float top, double& i
     inverse = 0.0;
     return 0.f;
   }
-  const float scale = __uint_as_float(amax) / top;
+  const float scale = __uint_as_float(amax) * (1.f / top);   // the constant is rounded, then the product
   inverse = 1.0 / static_cast<double>(scale);
   return scale;
 }

@@ -6,8 +6,8 @@ Test infrastructure only (see the package docstring).
     m = b1 m + (1 - b1) g      v = b2 v + (1 - b2) g g
     p = p (1 - lr decay) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 
-8-bit states: OCP e4m3 (m) and e5m2 (v) with an fp32 scale per 256 elements, fl(a / 448) or
-fl(a / 57344) for a block's largest magnitude a, 0 below 2^-100.
+8-bit states: OCP e4m3 (m) and e5m2 (v) with an fp32 scale per 256 elements, fl(a fl(1 / 448)) or
+fl(a fl(1 / 57344)) for a block's largest magnitude a, 0 below 2^-100.
 """
 from __future__ import annotations
 
@@ -51,8 +51,8 @@ def state_codes(x, kind):
     n, x = x.size, _blocks(x.astype(np.float32))
     levels = _levels(kind)
     amax = np.abs(x).max(1)
-    top = np.float32(STATE_FORMATS[kind][3])
-    scale = np.where(amax < np.float32(2.0 ** -100), np.float32(0), amax / top).astype(np.float32)
+    share = np.float32(1) / np.float32(STATE_FORMATS[kind][3])
+    scale = np.where(amax < np.float32(2.0 ** -100), np.float32(0), amax * share).astype(np.float32)
     inverse = np.zeros_like(scale)
     np.divide(np.float32(1), scale, out=inverse, where=scale > 0)
     y = np.abs(x * inverse[:, None]).astype(np.float64)

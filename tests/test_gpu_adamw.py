@@ -321,7 +321,7 @@ def test_states_made_on_another_stream(lib, bits):
 @pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
 def test_codes_are_the_nearest(lib, grad, max_norm):
     """Every code of the new states is the one nearest to the moment's quotient in fp64 (ties to the even code): what a
-    rounding to fp32 in between would decide, about one code in 2^17, is not left to it."""
+    rounding to fp32 in between would decide, a code in a million or so, is not left to it."""
     a = Model(lib, [300000, 4097], bits=8, grad=grad, seed=31)
 
     def whole(codes, scale, kind):   # the product of code and scale in fp64: 4 or 3 bits by 24
