@@ -17,12 +17,13 @@ struct PlanLayout {
   int64_t info;         // tiles, chunks, n, slots
   int64_t tiles;        // [max_tiles][4]: slot (-1: no adapter), first place in `order`, tokens, 0
   int64_t rows;         // [max_tiles][kTile]: a tile's tokens, the slot's last one again past them
-  int64_t chunks;       // [max_chunks][4]: slot, first tile, tiles, chunks of the slot
-  int64_t slot_chunks;  // [slots + 1]: a slot's first chunk
+  int64_t chunks;       // [max_chunks][4]: slot, first tile, tiles, chunks of the slot; slots of several chunks come first
+  int64_t slot_parts;   // [slots + 1]: chunks of such slots before a slot: where its own lie, if it is one
   int64_t slot_used;    // [slots + 1]: slots with tokens before a slot
   int64_t counts;       // [plan_wgs][slots + 1]: tokens by workgroup and slot (more than one workgroup)
   int64_t words;
   int64_t max_tiles, max_chunks;
+  int64_t max_parts;    // chunks of the slots of several
   int chunk_tiles;      // tiles of a chunk (the last of a slot may have fewer)
   int wgs;
   int64_t per_wg;
@@ -40,7 +41,12 @@ inline PlanLayout plan_layout(int64_t n, int slots) {
   // about four chunks of a batch with one slot, of 2 to 128 tiles: with the groups of features they fill the CUs, and
   // most slots of a batch with several have one, whose sums need no second pass
   p.chunk_tiles = static_cast<int>(whole <= 8 ? 2 : (whole >= 512 ? 128 : (whole + 3) / 4));
-  p.max_chunks = (whole / 128 > 4 ? whole / 128 : 4) + groups + groups / 2 + 1;   // grows with n
+  // whole / chunk_tiles, in a form that grows with n
+  const int64_t full = whole / 128 > 4 ? whole / 128 : 4;
+  // a slot of w whole tiles has at most w / chunk_tiles + 1 chunks: over all slots `full` and one for each slot
+  p.max_chunks = full + groups;
+  // with several of them w / chunk_tiles is 1 at least, so that the slots of several are no more than `full` either
+  p.max_parts = n <= p.chunk_tiles * kTile ? 0 : full + (full < slots ? full : slots);
   p.per_wg = (n + 255) / 256;
   p.per_wg = p.per_wg < 4096 ? 4096 : (p.per_wg + kPlanThreads - 1) / kPlanThreads * kPlanThreads;
   p.wgs = static_cast<int>((n + p.per_wg - 1) / p.per_wg);
@@ -50,8 +56,8 @@ inline PlanLayout plan_layout(int64_t n, int slots) {
   p.tiles = p.info + 4;
   p.rows = p.tiles + 4 * p.max_tiles;
   p.chunks = p.rows + kTile * p.max_tiles;
-  p.slot_chunks = p.chunks + 4 * p.max_chunks;
-  p.slot_used = p.slot_chunks + pad(slots + 1);
+  p.slot_parts = p.chunks + 4 * p.max_chunks;
+  p.slot_used = p.slot_parts + pad(slots + 1);
   p.counts = p.slot_used + pad(slots + 1);
   p.words = p.counts + (p.wgs > 1 ? pad(static_cast<int64_t>(p.wgs) * (slots + 1)) : 0);
   return p;
@@ -65,14 +71,15 @@ struct PlanView {
   const int4* tiles;
   const int32_t* rows;
   const int4* chunks;
-  const int32_t* slot_chunks;
+  const int32_t* slot_parts;
   const int32_t* slot_used;
-  int32_t n, slots, max_tiles, max_chunks;
+  int32_t n, slots, max_tiles, max_chunks, max_parts;
 };
 inline PlanView plan_view(const int32_t* plan, const PlanLayout& p) {
   return PlanView{plan + p.info, reinterpret_cast<const int4*>(plan + p.tiles), plan + p.rows,
-                  reinterpret_cast<const int4*>(plan + p.chunks), plan + p.slot_chunks, plan + p.slot_used, static_cast<int32_t>(p.n),
-                  static_cast<int32_t>(p.slots), static_cast<int32_t>(p.max_tiles), static_cast<int32_t>(p.max_chunks)};
+                  reinterpret_cast<const int4*>(plan + p.chunks), plan + p.slot_parts, plan + p.slot_used, static_cast<int32_t>(p.n),
+                  static_cast<int32_t>(p.slots), static_cast<int32_t>(p.max_tiles), static_cast<int32_t>(p.max_chunks),
+                  static_cast<int32_t>(p.max_parts)};
 }
 
 // A pool of adapters: `ranks` and `gains` may be null.
@@ -154,7 +161,7 @@ struct AdapterUp {
 hipError_t launch_adapters_up(const AdapterUp& u, const PlanView& plan, const Pool& pool, hipStream_t s);
 
 // The gradients of the factors over the tokens of each chunk: job 0 dB (over dY's columns, F = nf in whole 8s), job 1 dA.
-// A slot of one chunk is written to `out` at once, the partial sums of more to `partials` [max_chunks][F rp].
+// A slot of one chunk is written to `out` at once, the partial sums of more to `partials` [max_parts][F rp].
 struct AdapterGrad {
   const __bf16 *L, *St;
   float *partials, *out;

@@ -599,22 +599,22 @@ __global__ __launch_bounds__(kThreads) void up_any_kernel(AdapterUp u, PlanView 
 // 8192 tokens of 4096 + 11008 features at rank 16, X masked: 58 us (4.2 TB/s); 2048 of 11008 + 4096 at rank 64: 45 us, bound
 // by the loads' latency at two waves a SIMD (S's pieces a step ahead need more registers than there are: 54 us).
 template <int NR, bool kRankMajor, bool kWide>
-__device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, const PlanView& plan, const Pool& pool,
+__device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t group_at, int at_chunk, const PlanView& plan, const Pool& pool,
                                          float (*part)[8 * (NR > 2 ? 2 : NR) * 4 * 64]) {
   constexpr int kParts = NR > 2 ? 2 : 1, NT = NR > 2 ? 2 : NR, kWaves = 4 / kParts;
   const int lane = threadIdx.x & 63, li = lane & 15, lg = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int half = wave % kParts, w = wave / kParts, tile0 = half * NT;
   const int64_t F = jb.F, places = static_cast<int64_t>(plan.max_tiles) * kTile;
-  const uint32_t groups = static_cast<uint32_t>((F + 127) / 128);
-  const int64_t group = wg % groups;
-  const int at_chunk = wg / groups;
+  const int64_t group = group_at;
   const int4 info = *reinterpret_cast<const int4*>(plan.info);
   if (info.z != plan.n || info.w != plan.slots || at_chunk >= info.y) return;
   const int4 chunk = plan.chunks[at_chunk];
   const int slot = chunk.x, first = chunk.y, tiles = chunk.z;
   if (static_cast<unsigned>(slot) >= static_cast<unsigned>(plan.slots) || first < 0 || tiles < 1 || first + tiles > plan.max_tiles)
     return;
+  const bool whole = chunk.w == 1;   // the slot's only one
+  if (!whole && at_chunk >= plan.max_parts) return;
   const int64_t f0 = group * 128 + 8 * li, f = f0 < F ? f0 : F - 8;   // 8 | F
   const int steps = 2 * tiles - (tile_info(plan, first + tiles - 1).count > 32 ? 0 : 1);
   const uint32_t thr = kRankMajor ? jb.drop.thr : 0;
@@ -722,7 +722,6 @@ __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, con
   if (w != 0) return;
   add(part[half]);
   // one chunk: the gradient itself; more: a partial sum with whole padded ranks and features
-  const bool whole = chunk.w == 1;
   const int64_t nf = whole ? jb.nf : F;
   const int nr = whole ? pool.rank : 16 * NR;
   const float coef = whole ? pool.gain * (pool.gains != nullptr ? pool.gains[slot] : 1.f) : 1.f;
@@ -752,14 +751,17 @@ __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t wg, con
     }
 }
 
-// job 0: dB over dY; job 1: dA over X
+// job 0: dB over dY, `first` groups of features; job 1: dA over X, `second` groups.  Both jobs of a chunk before the next
+// chunk, so that the workgroups of chunks that the batch does not have come last and the others spread over the CUs.
 template <int NT, bool kWide>
-__global__ __launch_bounds__(kThreads, 2) void grad_kernel(AdapterGradJobs jobs, PlanView plan, Pool pool, uint32_t first) {
+__global__ __launch_bounds__(kThreads, 2) void grad_kernel(AdapterGradJobs jobs, PlanView plan, Pool pool, uint32_t first,
+                                                           uint32_t second) {
   __shared__ float part[2][8 * (NT > 2 ? 2 : NT) * 4 * 64];
-  if (blockIdx.x < first)
-    grad_job<NT, false, kWide>(jobs.job[0], blockIdx.x, plan, pool, part);
+  const uint32_t chunk = blockIdx.x / (first + second), group = blockIdx.x % (first + second);
+  if (group < first)
+    grad_job<NT, false, kWide>(jobs.job[0], group, static_cast<int>(chunk), plan, pool, part);
   else
-    grad_job<NT, true, kWide>(jobs.job[1], blockIdx.x - first, plan, pool, part);
+    grad_job<NT, true, kWide>(jobs.job[1], group - first, static_cast<int>(chunk), plan, pool, part);
 }
 
 // gain times the sum of the partials of a slot with several chunks, in their order; zeros for a batch without tokens
@@ -771,9 +773,9 @@ __global__ __launch_bounds__(kThreads) void grad_sum_kernel(AdapterGradJobs jobs
   if (plan.n > 0) {
     const int4 info = *reinterpret_cast<const int4*>(plan.info);
     if (info.z != plan.n || info.w != plan.slots) return;
-    chunk = plan.slot_chunks[slot];
-    chunks = plan.slot_chunks[slot + 1] - chunk;
-    if (chunks < 2 || chunk < 0 || chunk + chunks > plan.max_chunks) return;
+    chunk = plan.slot_parts[slot];
+    chunks = plan.slot_parts[slot + 1] - chunk;
+    if (chunks < 2 || chunk < 0 || chunk + chunks > plan.max_parts) return;
   }
   const int64_t i = (static_cast<int64_t>(blockIdx.x - (rank_major ? first : 0)) * kThreads + threadIdx.x) * 4, nf = jb.nf, all = nf * R;
   if (i >= all) return;
@@ -917,12 +919,13 @@ hipError_t launch_adapters_up(const AdapterUp& u, const PlanView& plan, const Po
 }
 
 hipError_t launch_adapters_grad(const AdapterGradJobs& jobs, const PlanView& plan, const Pool& pool, hipStream_t s) {
-  unsigned wgs[2];
-  for (int j = 0; j < 2; ++j) wgs[j] = static_cast<unsigned>((jobs.job[j].F + 127) / 128 * plan.max_chunks);
+  unsigned groups[2];
+  for (int j = 0; j < 2; ++j) groups[j] = static_cast<unsigned>((jobs.job[j].F + 127) / 128);
   // 32-bit offsets reach the tokens' rows
   const bool wide = plan.n * jobs.job[0].F * 2 >= (int64_t(1) << 31) || plan.n * jobs.job[1].F * 2 >= (int64_t(1) << 31);
 #define LQ_GRAD_KERNEL(NT, W) \
-  LQ_LAUNCH("adapters_grad", (grad_kernel<NT, W>), dim3(wgs[0] + wgs[1]), dim3(kThreads), 0, s, jobs, plan, pool, wgs[0])
+  LQ_LAUNCH("adapters_grad", (grad_kernel<NT, W>), dim3((groups[0] + groups[1]) * plan.max_chunks), dim3(kThreads), 0, s, jobs, plan, pool, \
+            groups[0], groups[1])
 #define LQ_GRAD(NT)                       \
   do {                                    \
     if (wide) LQ_GRAD_KERNEL(NT, true);   \

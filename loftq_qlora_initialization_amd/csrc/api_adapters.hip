@@ -87,8 +87,8 @@ BackwardSpace backward_space(void* ws, i64 n, i64 rows, i64 cols, int slots, int
   f.P = a.take<float>(p.max_tiles * kTile * rp);
   f.Pt = a.take<__bf16>(3 * p.max_tiles * kTile * rp);
   f.Ht = a.take<__bf16>(3 * p.max_tiles * kTile * rp);
-  f.grad_b = a.take<float>(p.max_chunks * rows8 * rp);
-  f.grad_a = a.take<float>(p.max_chunks * cols * rp);
+  f.grad_b = a.take<float>(p.max_parts * rows8 * rp);
+  f.grad_a = a.take<float>(p.max_parts * cols * rp);
   f.bytes = a.used;
   return f;
 }
@@ -257,7 +257,7 @@ loftq_status_t loftq_adapters_backward(const void* dY, const void* X, int64_t n_
   if (dB) {
     const AdapterGradJobs grad{{{G, f.Ht, f.grad_b, dB, rows8, rows, none}, {Xb, f.Pt, f.grad_a, dA, cols, cols, d}}};
     LQ_TRY(launch_adapters_grad(grad, view, pool, s));
-    if (n_tok > plan_layout(n_tok, ad->slots).chunk_tiles * kTile) LQ_TRY(launch_adapters_grad_sum(grad, view, pool, s));
+    if (plan_layout(n_tok, ad->slots).max_parts > 0) LQ_TRY(launch_adapters_grad_sum(grad, view, pool, s));
   }
   if (!dX) return LOFTQ_OK;
   return from_hip(launch_adapters_up(AdapterUp{f.P, 1, cols, f.At, pool.rp, true, dX0, dX, xdt, d}, view, pool, s));

@@ -47,16 +47,19 @@ __global__ __launch_bounds__(kPlanThreads) void plan_count_kernel(const int32_t*
 }
 
 struct Sums {
-  int tokens, tiles, chunks, used;
+  int tokens, tiles;
+  int parts;   // chunks of the slots of several
+  int slots;   // slots with tokens, and in the high half those of them of one chunk: one exchange less than with a number each
 };
+constexpr int kOne = 1 << 16;
 __device__ __forceinline__ Sums operator+(Sums a, Sums b) {
-  return Sums{a.tokens + b.tokens, a.tiles + b.tiles, a.chunks + b.chunks, a.used + b.used};
+  return Sums{a.tokens + b.tokens, a.tiles + b.tiles, a.parts + b.parts, a.slots + b.slots};
 }
 
 __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t* __restrict__ slot_of, PlanLayout p,
                                                                   int32_t* __restrict__ plan) {
   __shared__ int count[kWaves][kMostSlots + 1];   // a wave's tokens by slot, then the place of its next one
-  __shared__ Sums first[kMostSlots + 2];         // a slot's first token, tile and chunk, and the used slots before it
+  __shared__ Sums first[kMostSlots + 2];         // what lies before a slot
   __shared__ Sums wave_sum[kWaves];
   const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6, groups = p.slots + 1;
   for (int s = lane; s < groups; s += 64) count[w][s] = 0;
@@ -89,20 +92,19 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
       before += c;
     }
     if (p.wgs == 1) total = before;
-    const int tiles = (total + kTile - 1) / kTile;
-    const Sums own{total, tiles, s < p.slots ? (tiles + p.chunk_tiles - 1) / p.chunk_tiles : 0,
-                   s < p.slots && total > 0 ? 1 : 0};
+    const int tiles = (total + kTile - 1) / kTile, chunks = s < p.slots ? (tiles + p.chunk_tiles - 1) / p.chunk_tiles : 0;
+    const Sums own{total, tiles, chunks > 1 ? chunks : 0, chunks > 1 ? 1 : (chunks == 1 ? 1 + kOne : 0)};
     first[s] = mine;     // within the thread, made whole below
     mine = mine + own;
   }
   Sums upto = mine;     // sums over the wave's lanes up to this one
   for (int d = 1; d < 64; d <<= 1) {
-    const Sums o{__shfl_up(upto.tokens, d), __shfl_up(upto.tiles, d), __shfl_up(upto.chunks, d), __shfl_up(upto.used, d)};
+    const Sums o{__shfl_up(upto.tokens, d), __shfl_up(upto.tiles, d), __shfl_up(upto.parts, d), __shfl_up(upto.slots, d)};
     if (lane >= d) upto = upto + o;
   }
   if (lane == 63) wave_sum[w] = upto;
   __syncthreads();
-  Sums base{upto.tokens - mine.tokens, upto.tiles - mine.tiles, upto.chunks - mine.chunks, upto.used - mine.used};
+  Sums base{upto.tokens - mine.tokens, upto.tiles - mine.tiles, upto.parts - mine.parts, upto.slots - mine.slots};
   for (int v = 0; v < w; ++v) base = base + wave_sum[v];
   for (int s = s0; s < s0 + each && s < groups; ++s) first[s] = first[s] + base;
   if (tid == 0) {
@@ -114,13 +116,14 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
   if (blockIdx.x == 0) {
     for (int s = tid; s <= groups; s += kPlanThreads) plan[s] = first[s].tokens;
     for (int s = tid; s < groups; s += kPlanThreads) {
-      plan[p.slot_chunks + s] = first[s].chunks;
-      plan[p.slot_used + s] = first[s].used;
+      plan[p.slot_parts + s] = first[s].parts;
+      plan[p.slot_used + s] = first[s].slots & (kOne - 1);
     }
     if (tid == 0)
       *reinterpret_cast<int4*>(plan + p.info) =
-          make_int4(first[groups].tiles, first[groups].chunks, static_cast<int>(p.n), p.slots);
+          make_int4(first[groups].tiles, first[groups].parts + (first[groups].slots >> 16), static_cast<int>(p.n), p.slots);
   }
+  const int parts = first[groups].parts;
   volatile int* next = count[w];
   auto place = [&](int64_t i, int g) __attribute__((always_inline)) {
     const bool live = g != kNone;
@@ -146,10 +149,12 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
       const int left = total - k;
       reinterpret_cast<int4*>(plan + p.tiles)[tile] = make_int4(g < p.slots ? g : -1, at, left < kTile ? left : kTile, 0);
       const int index = k / kTile, tiles = (total + kTile - 1) / kTile;
-      if (g < p.slots && index % p.chunk_tiles == 0)
-        reinterpret_cast<int4*>(plan + p.chunks)[first[g].chunks + index / p.chunk_tiles] =
+      if (g < p.slots && index % p.chunk_tiles == 0) {   // slots of several chunks come first
+        const int at_chunk = tiles > p.chunk_tiles ? first[g].parts + index / p.chunk_tiles : parts + (first[g].slots >> 16);
+        reinterpret_cast<int4*>(plan + p.chunks)[at_chunk] =
             make_int4(g, tile, tiles - index < p.chunk_tiles ? tiles - index : p.chunk_tiles,
                       (tiles + p.chunk_tiles - 1) / p.chunk_tiles);
+      }
     }
     if (k == total - 1) {
       // to the tile's end, four at once: many slots end in the last workgroup's tokens (65536 tokens of 512 slots: 29 us one
@@ -172,7 +177,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_place_kernel(const int32_t*
 // without tokens
 __global__ void plan_empty_kernel(PlanLayout p, int32_t* __restrict__ plan) {
   for (int s = threadIdx.x; s < p.slots + 2; s += blockDim.x) plan[s] = 0;
-  for (int s = threadIdx.x; s < p.slots + 1; s += blockDim.x) plan[p.slot_chunks + s] = plan[p.slot_used + s] = 0;
+  for (int s = threadIdx.x; s < p.slots + 1; s += blockDim.x) plan[p.slot_parts + s] = plan[p.slot_used + s] = 0;
   if (threadIdx.x == 0) *reinterpret_cast<int4*>(plan + p.info) = make_int4(0, 0, 0, p.slots);
 }
 

@@ -171,3 +171,12 @@ def test_binding_refuses_host_tensors(b):
         b.loftq_adapters_backward(X, X, B, A, None)
     with pytest.raises(ValueError):
         b.AdamWTensors([B], [B])
+
+
+@pytest.mark.parametrize("n,slots,most", [(128, 128, 0.4e9), (8192, 1024, 2.7e9), (8192, 64, 0.3e9), (65536, 512, 1.7e9)])
+def test_gradient_workspace_has_no_room_for_sums_that_no_slot_writes(b, n, slots, most):
+    """Partial sums are those of slots with more tokens than one workgroup adds: a few, whatever the pool's slots.  What
+    grows with the slots is their factors' bf16 forms, (rows + 2 cols) rank 2 bytes each."""
+    rows, cols, rank = 11008, 4096, 64
+    forms = min(n, slots) * (rows + 2 * cols) * rank * 2
+    assert forms < b.adapters_backward_workspace_bytes(n, rows, cols, slots, rank) < most

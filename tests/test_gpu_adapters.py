@@ -376,6 +376,26 @@ def test_smaller_calls_in_a_large_workspace(lib):
         s.check_backward(s.backward(lib, ws=wb))
 
 
+# tokens of each slot: as many slots of several chunks as their tokens allow, each with one token in its last; one slot of
+# all but a few; no more than one chunk each; two of several among many of one, the first and the last slot of the pool
+COUNTS = [[193] * 3, [257] * 4, [65] * 3 + [0, 1], [2000] + [1] * 40, [128] * 20, [700] + [3] * 98 + [900], [8193, 64 * 128, 8200]]
+
+
+@pytest.mark.parametrize("rank", [8, 40])
+@pytest.mark.parametrize("counts", COUNTS, ids=lambda c: f"{len(c)}-{sum(c)}")
+def test_partial_sums_of_slots_of_every_length(lib, counts, rank):
+    """Within a workspace of the size that is asked for, with what lies behind it untouched."""
+    n, rows, cols, slots = sum(counts), 75, 64, len(counts)
+    b = Batch(n, rows, cols, slots, rank, seed=n)
+    b.ids = np.random.default_rng(n).permutation(np.repeat(np.arange(slots), counts))
+    b.idd = dev(b.ids, torch.int32)
+    need = lib.adapters_backward_workspace_bytes(n, rows, cols, slots, rank)
+    ws = torch.full((need + 4096,), 255, dtype=torch.uint8, device="cuda")
+    rng = dict(p=0.1, seed=1, offset=2)
+    b.check_backward(b.backward(lib, ws=ws[:need], **rng), **rng)
+    assert (ws[need:] == 255).all()
+
+
 def test_same_results_again_and_on_streams(lib):
     """Calls with workspaces of their own may overlap on two streams over one plan."""
     b = Batch(300, 320, 512, 5, 16, seed=8)
