@@ -75,18 +75,24 @@ __device__ __forceinline__ int64_t used_place(const PlanView& p, int slot) {
 constexpr int kThreads = 256, kDownThreads = 512, kDownWaves = kDownThreads / 64;
 
 // ---- the factors' forms for the products, eight elements a thread ----
-// Element j of the eight at `at`, `stride` elements apart, zero where j >= live: every load in flight at once.
+// Element j of the eight from p on, `stride` elements apart, zero where j >= live: every load in flight at once.  A
+// slot's factors, and a row of them, begin at any element where rows, rank or their product are odd, so it is the address
+// itself that allows 16-byte loads.
 template <typename T>
-__device__ __forceinline__ bf16x8 pool_eight(const T* f, int64_t at, int64_t stride, int live) {
+__device__ __forceinline__ bf16x8 pool_eight(const T* p, int64_t stride, int live) {
   T x[8];
-  if (stride == 1 && live >= 8 && at % 8 == 0) {   // 16-byte loads
-    typedef T eight __attribute__((ext_vector_type(8)));
-    const eight v = *reinterpret_cast<const eight*>(f + at);
+  if (stride == 1 && live >= 8 && reinterpret_cast<uintptr_t>(p) % 16 == 0) {
+    constexpr int kPer = 16 / static_cast<int>(sizeof(T));
+    typedef T piece_t __attribute__((ext_vector_type(kPer)));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = v[j];
+    for (int c = 0; c < 8 / kPer; ++c) {
+      const piece_t v = reinterpret_cast<const piece_t*>(p)[c];
+#pragma unroll
+      for (int j = 0; j < kPer; ++j) x[c * kPer + j] = v[j];
+    }
   } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = f[at + (j < live ? j * stride : 0)];   // past them the first again
+    for (int j = 0; j < 8; ++j) x[j] = p[j < live ? j * stride : 0];   // past them the first again
   }
   bf16x8 o;
 #pragma unroll
@@ -104,7 +110,7 @@ __device__ __forceinline__ void prepare_slot(const Prepare& q, int64_t i, int sl
     if (i < rows * groups) {
       const int64_t row = i / groups;
       const int e = static_cast<int>(i % groups) * 8;
-      *reinterpret_cast<bf16x8*>(q.Bp + (place * rows + row) * rp + e) = e < r ? pool_eight(B, row * R + e, 1, r - e) : zero;
+      *reinterpret_cast<bf16x8*>(q.Bp + (place * rows + row) * rp + e) = e < r ? pool_eight(B + row * R + e, 1, r - e) : zero;
       return;
     }
     i -= rows * groups;
@@ -114,7 +120,7 @@ __device__ __forceinline__ void prepare_slot(const Prepare& q, int64_t i, int sl
       const int e = static_cast<int>(i % rp);
       const int64_t row = i / rp * 8;
       *reinterpret_cast<bf16x8*>(q.Bt + (place * rp + e) * q.rows8 + row) =
-          e < r ? pool_eight(B, row * R + e, R, static_cast<int>(rows - row)) : zero;
+          e < r ? pool_eight(B + row * R + e, R, static_cast<int>(rows - row)) : zero;
       return;
     }
     i -= q.rows8 / 8 * rp;
@@ -122,7 +128,7 @@ __device__ __forceinline__ void prepare_slot(const Prepare& q, int64_t i, int sl
   if (q.Ab != nullptr) {
     if (i < cols / 8 * rp) {
       const int64_t e = i / (cols / 8), c = i % (cols / 8) * 8;
-      *reinterpret_cast<bf16x8*>(q.Ab + (place * rp + e) * cols + c) = e < r ? pool_eight(A, e * cols + c, 1, 8) : zero;
+      *reinterpret_cast<bf16x8*>(q.Ab + (place * rp + e) * cols + c) = e < r ? pool_eight(A + e * cols + c, 1, 8) : zero;
       return;
     }
     i -= cols / 8 * rp;
@@ -130,7 +136,7 @@ __device__ __forceinline__ void prepare_slot(const Prepare& q, int64_t i, int sl
   if (q.At != nullptr && i < cols * groups) {   // neighbouring threads take neighbouring columns
     const int64_t c = i % cols;
     const int e = static_cast<int>(i / cols) * 8;
-    *reinterpret_cast<bf16x8*>(q.At + (place * cols + c) * rp + e) = e < r ? pool_eight(A, e * cols + c, cols, r - e) : zero;
+    *reinterpret_cast<bf16x8*>(q.At + (place * cols + c) * rp + e) = e < r ? pool_eight(A + e * cols + c, cols, r - e) : zero;
   }
 }
 __device__ __forceinline__ void zero_slot(float* out, int64_t n, int64_t i, int64_t threads) {

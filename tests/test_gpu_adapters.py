@@ -281,6 +281,28 @@ def test_what_the_pool_holds_past_a_rank_is_not_used(lib):
     assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
+@pytest.mark.parametrize("factors", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("n,rows,rank", [(40, 129, 17), (300, 33, 1), (40, 7, 9), (300, 130, 25), (40, 64, 12)])
+def test_slots_that_begin_at_any_element(lib, n, rows, rank, factors):
+    """With odd rows and ranks a slot's factors, and their rows, begin anywhere in a vector; each slot's tokens and
+    gradients are those of a pool of that slot alone, which begins at the start of one."""
+    slots, cols = 5, 72
+    b = Batch(n, rows, cols, slots, rank, seed=rank, factors=factors)
+    Y, (dX, dB, dA) = b.forward(lib), b.backward(lib)
+    b.check_forward(Y)
+    b.check_backward((dX, dB, dA))
+    for s in range(slots):
+        one = Batch(n, rows, cols, 1, rank, seed=rank, factors=factors)
+        one.Xd, one.Gd, one.Y0, one.dX0, one.gd = b.Xd, b.Gd, b.Y0, b.dX0, b.gd[s:s + 1].clone()
+        one.Bd, one.Ad = b.Bd[s:s + 1].clone(), b.Ad[s:s + 1].clone()
+        one.idd = torch.where(b.idd == s, 0, -1).int()
+        mine = b.idd == s
+        Y1, (dX1, dB1, dA1) = one.forward(lib), one.backward(lib)
+        for got, want in ((Y[mine], Y1[mine]), (dX[mine], dX1[mine]), (dB[s], dB1[0]), (dA[s], dA1[0])):
+            # sums over the columns may be divided otherwise among fewer tiles, which in bf16 can turn a rounding: 2^-8 each
+            assert torch.linalg.norm(got.float() - want.float()) <= 2.0 ** -7 * torch.linalg.norm(want.float())
+
+
 def test_slots_do_not_touch_each_other(lib):
     """NaN in one slot's factors, or in one token, reaches that slot's tokens, or that token, alone."""
     b = Batch(200, 64, 128, 4, 16, seed=10)
