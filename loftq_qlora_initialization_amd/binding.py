@@ -791,7 +791,8 @@ class AdamWTensors:
 
     params, grads     lists of contiguous device tensors, each list of one type (float32 or bfloat16)
     bits              32 (states in float32) or 8 (m in float8_e4m3fn, v in float8_e5m2, a float32 scale per 256)
-    m, v (m_scale, v_scale)  the states, new ones of zeros where not given (their type then says the bits)
+    m, v              the states, both or neither: new ones of zeros where not given, else their type says the bits
+    m_scale, v_scale  the given states' scales, with 8 bits; not without m and v, nor with 32 bits
     copies            bfloat16 tensors that take the new parameters rounded, or None
     lr_scale, weight_decay   a number, or one per tensor
     """
@@ -804,14 +805,21 @@ class AdamWTensors:
             raise ValueError("params must hold a tensor")
         if len(grads) != count:
             raise ValueError(f"grads must hold {count} tensors")
-        dev = _first(params[0], "params")
-        pdt, gdt = _wdtype(params[0]), _wdtype(grads[0])
         if m is not None and len(m) != count:
             raise ValueError(f"m must hold {count} tensors")
         if m is not None:
             bits = 32 if m[0].dtype is torch.float32 else 8
         if bits not in (32, 8):
             raise LoftqError("loftq_adamw_plan", 2)
+        # a state without its other half would be continued as one of zeros
+        if (m is None) != (v is None):
+            raise ValueError("m and v are given together")
+        scaled = m is not None and bits == 8
+        if (m_scale is not None) != scaled or (v_scale is not None) != scaled:
+            raise ValueError("m_scale and v_scale are given with m and v in 8 bits" if scaled
+                             else "m_scale and v_scale belong to m and v in 8 bits")
+        dev = _first(params[0], "params")
+        pdt, gdt = _wdtype(params[0]), _wdtype(grads[0])
         m_dtype, v_dtype = (torch.float32, torch.float32) if bits == 32 else (torch.float8_e4m3fn, torch.float8_e5m2)
 
         def states(given, dtype, per=1):

@@ -180,3 +180,19 @@ def test_gradient_workspace_has_no_room_for_sums_that_no_slot_writes(b, n, slots
     rows, cols, rank = 11008, 4096, 64
     forms = min(n, slots) * (rows + 2 * cols) * rank * 2
     assert forms < b.adapters_backward_workspace_bytes(n, rows, cols, slots, rank) < most
+
+
+def test_states_without_their_other_half_are_refused(b):
+    """They would be continued as zeros: codes without scales, one moment without the other."""
+    p, g = [torch.zeros(300)], [torch.zeros(300)]
+    m, v = [torch.zeros(300, dtype=torch.float8_e4m3fn)], [torch.zeros(300, dtype=torch.float8_e5m2)]
+    s = [torch.zeros(2)]
+    for states in (dict(m=m, v=v), dict(m=m, v=v, m_scale=s), dict(m=m, v=v, v_scale=s)):
+        with pytest.raises(ValueError, match="m_scale and v_scale are given with"):
+            b.AdamWTensors(p, g, **states)
+    for states in (dict(m=m, m_scale=s), dict(v=v, v_scale=s, bits=8), dict(m=p), dict(v=p)):
+        with pytest.raises(ValueError, match="m and v are given together"):
+            b.AdamWTensors(p, g, **states)
+    for states in (dict(m=p, v=p, m_scale=s, v_scale=s), dict(m_scale=s, v_scale=s, bits=8), dict(v_scale=s), dict(m=p, v=p, m_scale=s)):
+        with pytest.raises(ValueError, match="m_scale and v_scale belong to"):
+            b.AdamWTensors(p, g, **states)
