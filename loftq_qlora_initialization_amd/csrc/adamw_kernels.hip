@@ -243,7 +243,7 @@ __global__ __launch_bounds__(kThreads) void step_kernel(AdamTable t, AdamScalars
       vc = __builtin_amdgcn_cvt_pk_bf8_f32(to_odd(v8[2] * vi), to_odd(v8[3] * vi), vc, true);
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (v[j] > 0.f && vi > 0.0 && (vc >> (8 * j) & 255u) == 0) vc |= 1u << (8 * j);
+        if (v8[j] > 0.0 && vi > 0.0 && (vc >> (8 * j) & 255u) == 0) vc |= 1u << (8 * j);   // fl(v8) may be 0
       store_codes(x.m, e, left, mc);
       store_codes(x.v, e, left, vc);
       if (lane == 0) {

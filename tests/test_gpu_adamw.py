@@ -168,6 +168,46 @@ def test_small_second_moments_do_not_vanish(lib):
     assert ((p[0] - was).abs() <= 4 * 0.1 * 10).all()
 
 
+@pytest.mark.parametrize("small", [1e-22, 1e-19, 1e-12])
+def test_second_moments_below_fp32_keep_the_smallest_code(lib, small):
+    """A squared gradient that fp32 cannot hold is still a positive v, beside a block's large one and in a block that
+    has no other at its size; where the whole block is below 2^-100 its scale is 0."""
+    n = 3 * 256
+    p, g = [torch.zeros(n, device="cuda")], [torch.full((n,), small, device="cuda")]
+    g[0][7], g[0][300], g[0][511] = 1.0, 1e-3, 0.0
+    t = lib.AdamWTensors(p, g, bits=8)
+    lib.loftq_adamw(t, lr=0.1)
+    codes, scale = t.v[0].view(torch.uint8).cpu(), t.v_scale[0].cpu()
+    want = torch.ones(n, dtype=torch.uint8)
+    want[7] = want[300] = 0x7B
+    want[511] = 0
+    if 1e-3 * small ** 2 < 2.0 ** -100:
+        want[512:] = 0
+        assert scale[2] == 0
+    else:
+        want[512:] = 0x7B
+    assert torch.equal(codes, want) and (scale[:2] > 0).all()
+
+
+def test_a_small_first_moment_is_divided_by_its_root(lib):
+    """Gradients of 5e-6 of the block's largest: m / scale = 448 * 5e-6 = 2.2e-3 keeps a code (the smallest is 2^-9), v / scale
+    = 57344 * 2.5e-11 = 1.4e-6 would round to zero (the smallest is 2^-16).  With no gradients afterwards a step is at
+    most 0.1 * 0.67 (t = 2: b1 (1 - b1) / (1 - b1^2) sqrt(1 - b2^2) / sqrt(b2 (1 - b2))), times 2 where m's code is
+    up to twice m and sqrt(1.5) where v's is down to v / 1.5; over eps alone it would be 0.1 * 200."""
+    p, g = [torch.zeros(256, device="cuda")], [torch.full((256,), 1e-2, device="cuda")]
+    g[0][7], g[0][8:64], g[0][64:128] = 1.0, 2e-3, 5e-6
+    t = lib.AdamWTensors(p, g, bits=8)
+    lib.loftq_adamw(t, lr=0.1)
+    m, v = t.m[0].view(torch.uint8), t.v[0].view(torch.uint8)
+    assert (m[64:128] == 1).all() and (v[64:128] == 1).all() and (m[:64] > 1).all() and (v[:64] > 1).all()
+    g[0].zero_()
+    for k in range(2, 6):
+        was = p[0].clone()
+        lib.loftq_adamw(t, lr=0.1, t=k)
+        step = (p[0] - was).abs()
+        assert (step > 0).all() and (step <= 0.1 * 0.67 * 2 * 1.23).all()
+
+
 @pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_gradients_that_are_not_finite(lib, bits, bad):
