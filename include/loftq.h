@@ -416,10 +416,12 @@ size_t loftq_adapters_backward_workspace_bytes(int64_t n_tok, int64_t rows, int6
  *
  * States in 8 bits: blocks of 256 consecutive elements (a tensor's last may be shorter) with an
  * fp32 scale each, m in OCP e4m3 and v in OCP e5m2.  With a the largest magnitude of the block,
- * scale = fl(a fl(1 / 448)) for m and fl(a fl(1 / 57344)) for v (a rounded to fp32), 0 where a < 2^-100; code: x / scale
- * to the nearest, ties to even; in a block whose scale is not 0 a positive v never becomes zero but the smallest code, so
- * that no step divides by eps alone; value = code scale.  m and v are formed and coded in fp64, so that no rounding
- * in between decides a code; p takes fl(m) and fl(v).  A block that holds an infinity or a NaN gets the scale NaN. */
+ * scale = fl(a fl(1 / 448)) for m and fl(a fl(1 / 57344)) for v (a rounded to fp32), 0 where a < 2^-100: a product with
+ * the formats' rounded inverse tops, off a / 448 and a / 57344 by up to 2^-23 of itself, and the codes go by the
+ * scale that is stored: x / scale to the nearest, ties to even.  In a block whose scale is not 0 a positive v never
+ * becomes zero but the smallest code, so that no step divides by eps alone.  Value = code scale.  m and v are formed
+ * and coded in fp64, so that no rounding in between decides a code; p takes fl(m) and fl(v).  A block that holds an
+ * infinity or a NaN gets the scale NaN. */
 typedef struct {
   void* param;          /* [device] n elements of dtype pdt */
   const void* grad;     /* [device] n elements of dtype gdt */

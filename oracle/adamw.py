@@ -7,7 +7,8 @@ Test infrastructure only (see the package docstring).
     p = p (1 - lr decay) - lr / (1 - b1^t) m / (sqrt(v) / sqrt(1 - b2^t) + eps)
 
 8-bit states: OCP e4m3 (m) and e5m2 (v) with an fp32 scale per 256 elements, fl(a fl(1 / 448)) or
-fl(a fl(1 / 57344)) for a block's largest magnitude a, 0 below 2^-100.
+fl(a fl(1 / 57344)) for a block's largest magnitude a, 0 below 2^-100.  (The C call's definition: not the rounded
+quotient, from which it is up to 2^-23 of itself away.)
 """
 from __future__ import annotations
 

@@ -388,3 +388,28 @@ def test_codes_are_the_nearest(lib, grad, max_norm):
             got = codes.view(torch.uint8).cpu().numpy()
             assert np.array_equal(got & 127, code)
             assert np.array_equal(got >= 128, np.signbit(x))
+
+
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+def test_scales_are_the_products(lib, grad):
+    """Every new scale, bit for bit: the block's largest moment (formed in fp64, rounded to fp32) times the rounded inverse
+    of the format's top, 0 below 2^-100."""
+    n = 256 * 700 + 33
+    a = Model(lib, [n], bits=8, grad=grad, seed=33)
+    t = a.tensors
+    size = torch.exp2(-torch.arange(701, device="cuda") / 8.0)         # from 1 down to 2^-88, whose squares pass 2^-100
+    a.grads[0].mul_(size.repeat_interleave(256)[:n].to(grad))
+    t.m_scale[0].mul_(size), t.v_scale[0].mul_(size * size)
+
+    def whole(codes, scale, kind):   # the product of code and scale in fp64
+        ones = np.ones(scale.numel(), np.float32)
+        return oracle.state_values(codes.view(torch.uint8).cpu().numpy(), ones, kind) * np.repeat(host(scale), 256)[:n]
+
+    g, m, v = host(a.grads[0]), whole(t.m[0], t.m_scale[0], "m"), whole(t.v[0], t.v_scale[0], "v")
+    lib.loftq_adamw(t, t=3, **HOW)
+    b1, b2 = HOW["beta1"], HOW["beta2"]
+    for x, scale, kind in ((b1 * m + (1 - b1) * g, t.m_scale[0], "m"), (b2 * v + ((1 - b2) * g) * g, t.v_scale[0], "v")):
+        amax = np.abs(np.concatenate([x, np.zeros(-n % 256)])).reshape(-1, 256).max(1).astype(np.float32)
+        want = np.where(amax < np.float32(2.0 ** -100), np.float32(0), amax * (np.float32(1) / np.float32(oracle.STATE_FORMATS[kind][3])))
+        assert kind == "m" or ((want == 0).any() and (want > 0).any())
+        assert np.array_equal(scale.cpu().numpy(), want.astype(np.float32))
