@@ -451,7 +451,8 @@ typedef struct {
   loftq_dtype_t pdt, gdt;
 } loftq_adamw_plan_t;
 
-/*   tensors  [host] count tensors, none overlapping another; read before the call returns
+/*   tensors  [host] count tensors; read before the call returns.  What a step writes (all but the gradients) may
+ *            not overlap anything else of it: a parameter that a model uses twice is one tensor (INVALID)
  *   bits     32 or 8 (states)
  *   table    [device] loftq_adamw_plan_bytes(tensors, count) bytes; also the steps' scratch: two steps over
  *            one table must not run at the same time

@@ -789,7 +789,7 @@ class AdamWTensors:
     """The tensors that loftq_adamw steps over: parameters, their gradients and states, laid out once for the kernels.
     Keeps the tensors; their memory must stay where it is.
 
-    params, grads     lists of contiguous device tensors, each list of one type (float32 or bfloat16)
+    params, grads     lists of contiguous device tensors, each list of one type (float32 or bfloat16), each parameter once
     bits              32 (states in float32) or 8 (m in float8_e4m3fn, v in float8_e5m2, a float32 scale per 256)
     m, v              the states, both or neither: new ones of zeros where not given, else their type says the bits
     m_scale, v_scale  the given states' scales, with 8 bits; not without m and v, nor with 32 bits

@@ -1,5 +1,7 @@
 // C-ABI entry points of the optimizer's step: argument validation, the table's layout, then launches.
+#include <algorithm>
 #include <cmath>
+#include <new>
 
 #include "adamw.h"
 #include "layer.h"
@@ -23,6 +25,50 @@ int64_t count_chunks(const loftq_adamw_tensor_t* tensors, int32_t count) {
     chunks += adam_chunks(n);
   }
   return chunks < (int64_t(1) << 24) ? chunks : -1;   // a launch has less than 2^32 work-items
+}
+
+// Memory that a step reads or writes.
+struct Piece {
+  uintptr_t begin, end;
+  bool written;
+};
+enum Overlap { kNone, kSome, kUnknown };
+
+// Whether anything that a step writes lies over anything else of it.  Gradients are only read, and may share theirs.
+Overlap overlap(const loftq_adamw_tensor_t* tensors, int32_t count, loftq_dtype_t pdt, loftq_dtype_t gdt, int32_t bits,
+                const void* table, size_t table_bytes) {
+  Piece* const pieces = new (std::nothrow) Piece[static_cast<size_t>(count) * 7 + 1];
+  if (pieces == nullptr) return kUnknown;
+  Piece* last = pieces;
+  auto add = [&](const void* p, int64_t bytes, bool written) {
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p);
+    if (p != nullptr && bytes > 0) *last++ = Piece{at, at + static_cast<uintptr_t>(bytes), written};
+  };
+  auto size = [](loftq_dtype_t t) { return t == LOFTQ_BF16 ? 2 : 4; };
+  for (int32_t i = 0; i < count; ++i) {
+    const loftq_adamw_tensor_t& x = tensors[i];
+    const int64_t blocks = (x.n + kStateBlock - 1) / kStateBlock;
+    add(x.param, x.n * size(pdt), true);
+    add(x.grad, x.n * size(gdt), false);
+    add(x.m, x.n * (bits / 8), true);
+    add(x.v, x.n * (bits / 8), true);
+    add(x.copy, x.n * 2, true);
+    if (bits == 8) {
+      add(x.m_scale, blocks * 4, true);
+      add(x.v_scale, blocks * 4, true);
+    }
+  }
+  add(table, static_cast<int64_t>(table_bytes), true);
+  std::sort(pieces, last, [](const Piece& a, const Piece& b) { return a.begin < b.begin; });
+  uintptr_t written = 0, any = 0;   // where what begins before a piece ends
+  Overlap found = kNone;
+  for (const Piece* p = pieces; p != last && found == kNone; ++p) {
+    if (p->begin < (p->written ? any : written)) found = kSome;
+    any = std::max(any, p->end);
+    if (p->written) written = std::max(written, p->end);
+  }
+  delete[] pieces;
+  return found;
 }
 
 }  // namespace
@@ -53,6 +99,8 @@ loftq_status_t loftq_adamw_plan(const loftq_adamw_tensor_t* tensors, int32_t cou
   if (!table || !aligned16(table)) return LOFTQ_ERR_INVALID_ARG;
   const AdamTable t = adam_table(table, count, chunks);
   if (table_bytes < t.bytes) return LOFTQ_ERR_WORKSPACE;
+  const Overlap o = overlap(tensors, count, pdt, gdt, bits, table, t.bytes);   // steps would race
+  if (o != kNone) return o == kSome ? LOFTQ_ERR_INVALID_ARG : LOFTQ_ERR_HIP;
   *plan = loftq_adamw_plan_t{table, chunks, count, bits, pdt, gdt};
   return from_hip(launch_adamw_table(tensors, count, t, static_cast<hipStream_t>(stream)));
 }

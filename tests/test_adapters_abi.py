@@ -196,3 +196,50 @@ def test_states_without_their_other_half_are_refused(b):
     for states in (dict(m=p, v=p, m_scale=s, v_scale=s), dict(m_scale=s, v_scale=s, bits=8), dict(v_scale=s), dict(m=p, v=p, m_scale=s)):
         with pytest.raises(ValueError, match="m_scale and v_scale belong to"):
             b.AdamWTensors(p, g, **states)
+
+
+def apart(b, at, n=1000, bits=32, copy=True):
+    """A tensor whose pieces lie one behind another from address `at` on, 8192 bytes each."""
+    places = [at + 8192 * i for i in range(7)]
+    scales = places[4:6] if bits == 8 else (None, None)
+    return tensor(b, *places[:4], *scales, places[6] if copy else None, n=n)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("pdt,gdt", [(0, 0), (1, 1), (0, 1)])
+def test_adamw_refuses_overlapping_tensors(b, bits, pdt, gdt):
+    """Two workgroups of a step would read and write the same numbers: a parameter given twice, above all."""
+    table, size = 1 << 30, (4, 2)
+    one, other = apart(b, 1 << 20, bits=bits), apart(b, 1 << 21, bits=bits)
+
+    def status(*tensors, table=table):
+        return plan(b, *tensors, bits=bits, pdt=pdt, gdt=gdt, table=table, table_bytes=1 << 20)
+
+    fields = ["param", "m", "v", "copy"] + (["m_scale", "v_scale"] if bits == 8 else [])
+    ends = dict(param=1000 * size[pdt], m=1000 * bits // 8, v=1000 * bits // 8, copy=2000, m_scale=16, v_scale=16)
+    assert status(one, other, one) == INVALID
+    for name in fields:
+        twin = apart(b, 1 << 21, bits=bits)
+        setattr(twin, name, getattr(one, name))
+        assert status(one, twin) == INVALID, name                     # the same memory
+        setattr(twin, name, getattr(one, name) + (ends[name] - 1) // 16 * 16)
+        assert status(one, twin) == INVALID, name                     # its last bytes
+        assert status(one, other, table=getattr(one, name)) == INVALID
+    within = apart(b, 1 << 20, bits=bits)
+    within.grad = within.param                                        # read where another workgroup writes
+    assert status(within) == INVALID
+    across = apart(b, 1 << 21, bits=bits)
+    across.grad = one.m
+    assert status(one, across) == INVALID and status(across, one) == INVALID
+
+
+def test_adamw_takes_neighbouring_tensors_and_shared_gradients(b):
+    """No overlap: tensors end to end, gradients in common, tensors without elements anywhere.  Without a GPU the launch
+    behind the checks fails, on its own account."""
+    if torch.cuda.is_available():
+        pytest.skip("the addresses are not memory")
+    one = tensor(b, *(1 << 20 | 4096 * i for i in range(4)), n=1024)
+    next_to = tensor(b, *(1 << 21 | 4096 * i for i in range(4)), n=1024)
+    next_to.grad = one.grad
+    empty = tensor(b, *(1 << 20 for _ in range(4)), n=0)
+    assert plan(b, one, next_to, empty, table=1 << 30) not in (OK, INVALID, UNSUPPORTED, WORKSPACE)
