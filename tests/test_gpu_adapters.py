@@ -544,6 +544,59 @@ def test_offsets_past_32_bits(lib):
     assert not dX[:-8].any()
 
 
+@pytest.mark.parametrize("rank", [4, 40])
+def test_masks_past_32_bits(lib, rank):
+    """The same sizes under a mask, whose words are numbered by the element of the whole call, in every product that reads
+    or writes so much; of one rank tile and of three."""
+    n, rows, cols, tail = 140000, 16448, 16384, 8
+    b = Batch(tail, rows, cols, 2, rank, "runs", seed=12)
+    p, rng = 0.25, dict(p=0.25, seed=9, offset=4)
+    keep = oracle.keep_mask((tail, cols), p, 9, 4, first=(n - tail) * cols)
+    gains = b.gains.astype(np.float64) * 1.5 * oracle.drop_scale(p)
+    ids = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    ids[-tail:] = b.idd
+    plan = lib.loftq_adapters_plan(ids, 2)
+    X8, G8, dX0 = b.Xd, b.Gd, b.dX0
+    b.Xd = torch.zeros(n, cols, dtype=torch.bfloat16, device="cuda")
+    b.Xd[-tail:] = X8
+    for dtype in (torch.bfloat16, torch.float32):
+        Y = b.forward(lib, plan, base=None, out_dtype=dtype, **rng)
+        size = (b.cols + 3 * rank + 16) * U * oracle.adapters_forward(abs(b.X), abs(b.B), abs(b.A), b.ids, gains, None, keep)
+        check(Y[-tail:], oracle.adapters_forward(b.X, b.B, b.A, b.ids, gains, None, keep), size)
+        assert not Y[:-tail].any()
+        del Y
+    b.Gd = torch.zeros(n, rows, dtype=torch.bfloat16, device="cuda")
+    b.Gd[-tail:] = G8
+    ref = oracle.adapters_backward(b.G, b.X, b.B, b.A, b.ids, gains, None, keep, dX0)
+    S = oracle.adapters_backward(abs(b.G), abs(b.X), abs(b.B), abs(b.A), b.ids, gains, None, keep, abs(dX0))
+    for dtype in (torch.bfloat16, torch.float32):
+        base = torch.zeros(n, cols, dtype=dtype, device="cuda")
+        base[-tail:] = dev(dX0, dtype)
+        dX, dB, dA = b.backward(lib, plan, base=base, out=(base, torch.empty_like(b.Bd), torch.empty_like(b.Ad)), **rng)
+        for got, want, s, k in zip((dX[-tail:], dB, dA), ref, S, (rows + 3 * rank, tail + cols, tail + rows)):
+            check(got, want, (k + 16) * U * s)
+        assert not dX[:-tail].any()
+        del base, dX
+
+
+@pytest.mark.parametrize("n", [5, 300])
+def test_without_gains(lib, n):
+    """No gains are gains of one."""
+    b = Batch(n, 72, 136, 4, 24, ranks=True, seed=31)
+    b.gains = np.ones(4, np.float32)
+    rng, ones = dict(p=0.1, seed=1, offset=2), dev(b.gains)
+    b.gd = None
+    got = (b.forward(lib, **rng), *b.backward(lib, dtype=torch.float32, **rng))
+    b.check_forward(got[0], **rng)
+    b.check_backward(got[1:], **rng)
+    b.gd = ones
+    assert all(torch.equal(x, y) for x, y in zip(got, (b.forward(lib, **rng), *b.backward(lib, dtype=torch.float32, **rng))))
+    empty = Batch(0, 72, 136, 4, 24, seed=31)
+    empty.gd = None
+    _, dB, dA = empty.backward(lib, out=(dev(empty.dX0, torch.bfloat16), torch.ones_like(empty.Bd), torch.ones_like(empty.Ad)))
+    assert not dB.any() and not dA.any()
+
+
 def test_binding_checks_on_device(lib):
     b = Batch(8, 64, 128, 3, 8, seed=14)
     plan = b.plan(lib)
