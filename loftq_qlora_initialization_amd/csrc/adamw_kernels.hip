@@ -25,7 +25,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 struct TableArgs {
   loftq_adamw_tensor_t tensor[kPerTable];
   int64_t chunk[kPerTable];   // a tensor's first
-  int32_t first, count;
+  int32_t first;
 };
 
 __global__ __launch_bounds__(kThreads) void table_kernel(TableArgs a, AdamTable t) {
@@ -266,13 +266,13 @@ hipError_t launch_adamw_table(const loftq_adamw_tensor_t* tensors, int32_t count
   for (int32_t first = 0; first < count; first += kPerTable) {
     TableArgs a{};
     a.first = first;
-    a.count = count - first < kPerTable ? count - first : kPerTable;
-    for (int i = 0; i < a.count; ++i) {
+    const int here = count - first < kPerTable ? count - first : kPerTable;
+    for (int i = 0; i < here; ++i) {
       a.tensor[i] = tensors[first + i];
       a.chunk[i] = chunk;
       chunk += adam_chunks(tensors[first + i].n);
     }
-    LQ_LAUNCH("adamw_table", table_kernel, dim3(a.count), dim3(kThreads), 0, s, a, t);
+    LQ_LAUNCH("adamw_table", table_kernel, dim3(here), dim3(kThreads), 0, s, a, t);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -9,25 +9,16 @@
 // is as many bytes as four 16-token tiles of dY), their sums 8 us, dB and dA 27 us (62 MB of dY
 // and X), their sums 6 us.  8192 tokens x (4096 x 11008), r = 16: 37, 81, 5, 47 and 5 us, X's
 // mask being drawn twice.
-//
-// v_mfma_f32_16x16x32_bf16: lane L supplies A[L%16][8(L/16) + j] and
-// B[8(L/16) + j][L%16] (j = 0..7) and receives D[4(L/16) + v][L%16] in element v.
 #include "buffer.h"
 #include "layer.h"
+#include "thin.h"
 
 namespace loftq {
 namespace {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kThreads = 256;
-
-__device__ __forceinline__ f32x4 mfma16(u32x4 a, u32x4 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
 
 // ---- what a call's products read, in one launch ----
 // Work of thread i of the adapter's operands, eight elements each, zeros past r (and past
@@ -226,16 +217,6 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Src src, Levels lv, P
   *reinterpret_cast<bf16x8*>(p.padded + row * p.a.rows_pad + c) = o;
 }
 
-// 8 values of a masked row, elements e .. e + 7 of the flattening (e % 8 == 0)
-__device__ __forceinline__ u32x4 drop8(u32x4 v, uint64_t key, uint64_t e, uint32_t thr) {
-  const uint64_t w0 = drop_word(key, e >> 2), w1 = drop_word(key, (e >> 2) + 1);
-  v[0] = drop_pair(v[0], w0, 0, thr);
-  v[1] = drop_pair(v[1], w0, 2, thr);
-  v[2] = drop_pair(v[2], w1, 0, thr);
-  v[3] = drop_pair(v[3], w1, 2, thr);
-  return v;
-}
-
 // ---- thin product over the features: partial q of keep(X) M^T over the q-th K range ----
 // A workgroup takes 32 tokens and one range, which its four waves share U steps of 32 at a
 // time; M (rank-major, K along its rows) serves both 16-token tiles.  All loads of U steps
@@ -313,18 +294,8 @@ __global__ __launch_bounds__(kThreads) void down_kernel(DownJobs jobs, int64_t n
       }
 }
 
-// The sum of the partials in split order, as three bf16 pieces x = h0 + h1 + h2 (each the
-// rounding of what the ones before leave: the three hold 24 bits, so the products they
-// enter lose nothing against fp32; an infinity or NaN is all in the first).  Ranks past r
-// and tokens past n are zeros.  A workgroup takes 32 tokens and 16 ranks; the rank-major
-// form is turned round in LDS.
-__device__ __forceinline__ void split3(float x, __bf16 (&h)[3]) {
-#pragma unroll
-  for (int q = 0; q < 3; ++q) {
-    h[q] = static_cast<__bf16>(x);
-    x = __builtin_isfinite(static_cast<float>(h[q])) ? x - static_cast<float>(h[q]) : 0.f;
-  }
-}
+// The sum of the partials in split order, as three bf16 pieces.  Ranks past r and tokens past n are
+// zeros.  A workgroup takes 32 tokens and 16 ranks; the rank-major form is turned round in LDS.
 __global__ __launch_bounds__(kThreads) void down_sum_kernel(DownSumJobs jobs, int64_t n, int r, int rp, int ld,
                                                             int64_t n_pad) {
   __shared__ __align__(4) __bf16 turned[3 * 16][32 + 2];

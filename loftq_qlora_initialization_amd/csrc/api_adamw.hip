@@ -4,7 +4,7 @@
 #include <new>
 
 #include "adamw.h"
-#include "layer.h"
+#include "entry.h"
 
 using namespace loftq;
 
@@ -12,8 +12,6 @@ namespace {
 
 constexpr int32_t kMostTensors = 65536;
 constexpr int64_t kMostElements = int64_t(1) << 36;
-
-bool dtype_ok(loftq_dtype_t t) { return t == LOFTQ_F32 || t == LOFTQ_BF16; }
 
 // Chunks of all tensors; -1 where there are more elements than a step takes, -2 for a negative length.
 int64_t count_chunks(const loftq_adamw_tensor_t* tensors, int32_t count) {

@@ -1,31 +1,15 @@
 // C-ABI entry points of many adapters beside one shared weight: argument validation, workspace
 // layout, then launches.
-#include <cmath>
-
 #include "adapters.h"
-#include "layer.h"
+#include "entry.h"
 
 using namespace loftq;
 
 namespace {
 
-typedef int64_t i64;
-
 constexpr i64 kMostTokens = i64(1) << 25, kMostWidth = i64(1) << 22, kMostWorkgroups = i64(1) << 22;
 constexpr i64 kFewAdapterTokens = 256;
 
-struct Arena {
-  char* base;
-  size_t used = 0;
-  template <typename T>
-  T* take(i64 count) {
-    T* p = base != nullptr ? reinterpret_cast<T*>(base + used) : nullptr;
-    used += (static_cast<size_t>(count) * sizeof(T) + 255) / 256 * 256;
-    return p;
-  }
-};
-
-int rank_pad(int r) { return (r + 15) / 16 * 16; }
 i64 pad8(i64 n) { return (n + 7) / 8 * 8; }
 
 bool plan_sizes_ok(i64 n, int slots) { return n < kMostTokens && slots <= kMostSlots; }
@@ -93,19 +77,7 @@ BackwardSpace backward_space(void* ws, i64 n, i64 rows, i64 cols, int slots, int
   return f;
 }
 
-bool dtype_ok(loftq_dtype_t t) { return t == LOFTQ_F32 || t == LOFTQ_BF16; }
 bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-bool drop_ok(const loftq_dropout_t* d) {
-  return d == nullptr || (std::isfinite(d->p) && d->p >= 0.f && d->p <= 1.f &&
-                          (reinterpret_cast<uintptr_t>(d->step) & 7u) == 0);
-}
-DropArg drop_arg(const loftq_dropout_t* d) {
-  if (d == nullptr) return DropArg{0, 0, nullptr, 0, 1.f};
-  const uint32_t thr = static_cast<uint32_t>(static_cast<double>(d->p) * 65536.0 + 0.5);
-  const float scale = thr >= 65536u ? 0.f : static_cast<float>(65536.0 / (65536.0 - thr));
-  return DropArg{d->seed, d->offset, d->step, thr, scale};
-}
 
 // Sizes, types and numbers of a call; then, where it has work, its pool.
 loftq_status_t check_call(i64 n, i64 rows, i64 cols, const loftq_adapters_t* ad, const loftq_dropout_t* drop) {
@@ -122,12 +94,6 @@ loftq_status_t check_pool(const loftq_adapters_t* ad, const int32_t* plan, size_
 Pool pool_of(const loftq_adapters_t* ad, const DropArg& d) {
   return Pool{ad->B, ad->A, ad->dt, ad->slots, ad->rank, rank_pad(ad->rank), ad->ranks, ad->gains, ad->alpha * d.scale};
 }
-
-#define LQ_TRY(call)                                  \
-  do {                                                \
-    const hipError_t lq_e_ = (call);                  \
-    if (lq_e_ != hipSuccess) return LOFTQ_ERR_HIP;    \
-  } while (0)
 
 bool query_ok(i64 n, i64 rows, i64 cols, int32_t slots, int32_t rank, bool backward) {
   return shape_ok(rows, cols) && n >= 0 && n < (i64(1) << 31) && slots >= 1 && rank >= 1 &&

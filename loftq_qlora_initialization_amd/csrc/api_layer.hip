@@ -1,28 +1,12 @@
 // C-ABI entry points of the adapted layer's training and serving path (dropout, MXFP4, the
 // training forward, the gradient): argument validation, workspace layout, then launches.
-#include <cmath>
-
+#include "entry.h"
 #include "layer.h"
 
 using namespace loftq;
 
 namespace {
 
-typedef int64_t i64;
-
-// Consecutive 256-byte aligned pieces of a workspace; with a null base it only counts.
-struct Arena {
-  char* base;
-  size_t used = 0;
-  template <typename T>
-  T* take(i64 count) {
-    T* p = base != nullptr ? reinterpret_cast<T*>(base + used) : nullptr;
-    used += (static_cast<size_t>(count) * sizeof(T) + 255) / 256 * 256;
-    return p;
-  }
-};
-
-int rank_pad(int r) { return (r + 15) / 16 * 16; }
 i64 pad_to(i64 n, i64 m) { return (n + m - 1) / m * m; }
 
 // The pieces of a call's workspace.  Each is as large as any call of up to n tokens and of
@@ -111,24 +95,10 @@ bool layer_shape_ok(i64 n, i64 rows, i64 cols, int r) {
   return (base > codes ? base : codes) + pad + operands < limit && pad_to(n, 64) * 128 < limit && rows < limit / 64;
 }
 
-bool drop_ok(const loftq_dropout_t* d) {
-  return d == nullptr || (std::isfinite(d->p) && d->p >= 0.f && d->p <= 1.f &&
-                          (reinterpret_cast<uintptr_t>(d->step) & 7u) == 0);
-}
-
-DropArg drop_arg(const loftq_dropout_t* d) {
-  if (d == nullptr) return DropArg{0, 0, nullptr, 0, 1.f};
-  const uint32_t thr = static_cast<uint32_t>(static_cast<double>(d->p) * 65536.0 + 0.5);
-  const float scale = thr >= 65536u ? 0.f : static_cast<float>(65536.0 / (65536.0 - thr));
-  return DropArg{d->seed, d->offset, d->step, thr, scale};
-}
-
 // Both factors or none; one of no elements may have no address.
 bool factors_ok(const float* B, const float* A, i64 rows, i64 cols) {
   return rows == 0 || cols == 0 || (B == nullptr) == (A == nullptr);
 }
-
-bool dtype_ok(loftq_dtype_t t) { return t == LOFTQ_F32 || t == LOFTQ_BF16; }
 
 // What the training calls share: sizes, the base, the adapter, the dropout.
 loftq_status_t check_layer(i64 n, i64 rows, i64 cols, const Base4& b, bool mx, const float* B, const float* A, int r,
@@ -160,12 +130,6 @@ loftq_status_t check_layer_buffers(i64 n, i64 rows, i64 cols, const Base4& b, bo
   if (B && (!aligned16(B) || !aligned16(A))) return LOFTQ_ERR_INVALID_ARG;
   return LOFTQ_OK;
 }
-
-#define LQ_TRY(call)                                  \
-  do {                                                \
-    const hipError_t lq_e_ = (call);                  \
-    if (lq_e_ != hipSuccess) return LOFTQ_ERR_HIP;    \
-  } while (0)
 
 loftq_status_t layer_forward(const void* X, i64 n, i64 rows, i64 cols, const Base4& base, bool mx, const float* B,
                              const float* A, int r, float alpha, const loftq_dropout_t* drop, void* Y,

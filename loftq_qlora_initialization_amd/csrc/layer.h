@@ -153,8 +153,4 @@ hipError_t launch_mx_dequantize(const uint8_t* packed, const uint8_t* scales, in
 
 hipError_t launch_dropout(const void* X, loftq_dtype_t dt, int64_t n, const DropArg& d, void* Y, hipStream_t s);
 
-bool aligned16(const void* p);
-bool shape_ok(int64_t rows, int64_t cols);
-loftq_status_t from_hip(hipError_t e);
-
 }  // namespace loftq
