@@ -790,8 +790,9 @@ __global__ __launch_bounds__(kThreads) void pad_kernel(const __bf16* __restrict_
 unsigned blocks_for(int64_t threads) { return static_cast<unsigned>((threads + kThreads - 1) / kThreads); }
 
 // K ranges for about `tiles` tiles: workgroups for every CU several times over (8192 tokens of 11008 columns at rank 16:
-// 81 us with 256 workgroups in all, 61 with 400, 57 with 1100), fewer of them where the waves' sums are larger (2048
-// tokens of 11008 + 4096 columns at rank 64: 37 us with 256, 48 with 550); each range has a step for every wave
+// 62 us with 133 workgroups in all, 50 with 399, 47 with 931, 53 with 1995), fewer of them where the waves' sums are larger
+// (2048 tokens of 11008 + 4096 columns at rank 64: 57 us with 74, 34 with 148, 32 with 518, 36 with 814); each range has a
+// step for every wave
 int splits_for(int64_t tiles, int64_t K, int rp) {
   int64_t ks = 1024 / (rp / 16) / tiles;
   const int64_t most = (K + kDownStep - 1) / kDownStep / kDownWaves;

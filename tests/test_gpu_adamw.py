@@ -413,3 +413,43 @@ def test_scales_are_the_products(lib, grad):
         want = np.where(amax < np.float32(2.0 ** -100), np.float32(0), amax * (np.float32(1) / np.float32(oracle.STATE_FORMATS[kind][3])))
         assert kind == "m" or ((want == 0).any() and (want > 0).any())
         assert np.array_equal(scale.cpu().numpy(), want.astype(np.float32))
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_offsets_past_32_bits(lib, bits):
+    """The last elements of a tensor of more than 2^32 are stepped as those of a tensor of their own."""
+    n, tail = (1 << 32) + 4096 + 77, 512 + 77
+    g = torch.Generator(device="cuda").manual_seed(8)
+    end = dict(params=torch.randn(tail, generator=g, device="cuda"), grads=torch.randn(tail, generator=g, device="cuda"))
+
+    def large(x):
+        out = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+        out[-tail:] = x
+        return [out]
+
+    big = {k: large(x) for k, x in end.items()}
+    small = {k: [x.bfloat16()] for k, x in end.items()}
+    a, b = (lib.AdamWTensors(x["params"], x["grads"], bits=bits) for x in (big, small))
+    for t in (1, 2):
+        norms = [lib.loftq_adamw(x, t=t, max_norm=0.5, **HOW) for x in (a, b)]
+        assert torch.equal(*norms)
+    assert torch.equal(big["params"][0][-tail:], small["params"][0]) and not big["params"][0][:-tail].any()
+    for x, y in ((a.m, b.m), (a.v, b.v)):
+        assert torch.equal(x[0][-tail:].view(torch.uint8), y[0].view(torch.uint8))
+    if bits == 8:
+        assert torch.equal(a.m_scale[0][-3:], b.m_scale[0]) and torch.equal(a.v_scale[0][-3:], b.v_scale[0])
+
+
+def test_as_many_tensors_as_a_step_takes(lib):
+    count = 65536
+    p, g = (torch.randn(count, 4, generator=torch.Generator(device="cuda").manual_seed(k), device="cuda") for k in (1, 2))
+    q, m, v, m1, v1 = p.clone(), *(torch.zeros_like(p) for _ in range(4))
+    for tensors in (lib.AdamWTensors(list(p), list(g), m=list(m), v=list(v)), lib.AdamWTensors([q], [g], m=[m1], v=[v1])):
+        norm = lib.loftq_adamw(tensors, max_norm=1.0, **HOW)
+    assert abs(float(norm) - float(g.double().norm())) <= 2 * U * float(norm)
+    # the norms may be added in another order, which an element's rounding can show
+    for x, y in ((p, q), (m, m1), (v, v1)):
+        assert ((x - y).abs() <= 8 * U * y.abs()).all()
+    with pytest.raises(lib.LoftqError) as e:
+        lib.AdamWTensors([*p, q[0]], [*g, g[0]])
+    assert e.value.status == 2
