@@ -787,7 +787,8 @@ def loftq_adapters_backward(dY: torch.Tensor, X: Optional[torch.Tensor], B: torc
 
 class AdamWTensors:
     """The tensors that loftq_adamw steps over: parameters, their gradients and states, laid out once for the kernels.
-    Keeps the tensors; their memory must stay where it is.
+    Keeps the tensors; their memory must stay where it is.  A step reads the gradients given here: a training loop fills
+    them in place (torch's zero_grad(set_to_none=False)), or makes this anew for new ones.
 
     params, grads     lists of contiguous device tensors, each list of one type (float32 or bfloat16), each parameter once
     bits              32 (states in float32) or 8 (m in float8_e4m3fn, v in float8_e5m2, a float32 scale per 256)

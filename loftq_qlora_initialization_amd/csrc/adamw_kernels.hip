@@ -5,9 +5,9 @@
 // by exchanges within the wave and its scale is read and written once.
 //
 // Bound by memory: every number is read once and written once, gradients that are clipped are read twice (the
-// norm has to be known first).  Of 40 million elements the step with fp32 states moves 1.12 GB in 190 us (5.9 TB/s)
+// norm has to be known first).  Of 40 million elements the step with fp32 states moves 1.12 GB in 192 us (5.8 TB/s)
 // and the norm 0.16 GB in about 50; of 160 million with 8-bit states, fp32 parameters and a bf16 copy the step
-// moves 2.9 GB in 538 us (5.4 TB/s) and the norm 0.64 GB in 150.  Elements of one tensor in a chunk keep a workgroup's
+// moves 2.9 GB in 540 to 555 us (5.3 TB/s) and the norm 0.64 GB in 150.  Elements of one tensor in a chunk keep a workgroup's
 // scalars the same; 4096 of them are four loads a lane and give one layer's factors 305 workgroups.
 #include <cmath>
 

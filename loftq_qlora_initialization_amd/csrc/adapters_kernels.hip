@@ -140,7 +140,7 @@ __global__ __launch_bounds__(kThreads) void prepare_kernel(Prepare q, PlanView p
 // lies at place c ^ (i / 2 % 8), so that any 16 rows read at one k meet every bank once.  The waves' sums
 // meet in LDS.
 //
-// 8192 tokens of 11008 columns under a mask, rank 16: 48 us (3.7 TB/s), where the mask's 64-bit products, a word for
+// 8192 tokens of 11008 columns under a mask, rank 16: 49 us (3.7 TB/s), where the mask's 64-bit products, a word for
 // four elements, cost about as much as the loads; 2048 of 4096 columns at rank 64 in fp32 factors: 16 us.
 constexpr int kDownStep = 64;
 
@@ -344,7 +344,7 @@ __global__ __launch_bounds__(kThreads) void sum_kernel(AdapterSumJobs jobs, Prep
 // sums of H are added while they are staged in LDS in three bf16 pieces.  The factor is the first
 // operand, so a lane receives four consecutive features of a token.
 //
-// Bound by Y0 and Y: 8192 x 11008 in fp32 (dX, rank 16, masked) 127 us (5.7 TB/s), 8192 x 4096 in bf16 32 us (4.2 TB/s),
+// Bound by Y0 and Y: 8192 x 11008 in fp32 (dX, rank 16, masked) 129 us (5.6 TB/s), 8192 x 4096 in bf16 32 us (4.2 TB/s),
 // 2048 x 11008 in fp32 at rank 64 47 us (3.8 TB/s: 45 KB of LDS let three workgroups share a CU, and the last round of
 // workgroups fills half of them).
 template <int KR, int G>
@@ -573,8 +573,8 @@ __global__ __launch_bounds__(kThreads) void up_any_kernel(AdapterUp u, PlanView 
 // a step, half of the ranks each.  kRankMajor (dA): S is the first operand, so a lane holds 8
 // consecutive features of a rank; else (dB) a lane's rank is L%16.
 //
-// 8192 tokens of 4096 + 11008 features at rank 16, X masked: 58 us (4.2 TB/s); 2048 of 11008 + 4096 at rank 64: 45 us, bound
-// by the loads' latency at two waves a SIMD (S's pieces a step ahead need more registers than there are: 54 us).
+// 8192 tokens of 4096 + 11008 features at rank 16, X masked: 62 us (4.0 TB/s); 2048 of 11008 + 4096 at rank 64: 38 us, bound
+// by the loads' latency at two waves a SIMD (S's pieces a step ahead need more registers than there are: a fifth longer).
 template <int NR, bool kRankMajor, bool kWide>
 __device__ __forceinline__ void grad_job(const AdapterGrad& jb, uint32_t group_at, int at_chunk, const PlanView& plan, const Pool& pool,
                                          float (*part)[8 * (NR > 2 ? 2 : NR) * 4 * 64]) {

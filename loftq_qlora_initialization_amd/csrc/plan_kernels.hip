@@ -3,8 +3,8 @@
 // consecutive tokens, its own counters, and ranks 64 of them at a time by ballots over the
 // bits of their slots.
 //
-// Bound by latency: 64 tokens are one workgroup's few dependent steps (5.1 us with the launch), 65536 of 512 slots two
-// launches of 16 workgroups (21 us), whose waves load eight tokens a lane at once (32 us with a load for each step).
+// Bound by latency: 64 tokens are one workgroup's few dependent steps (5.0 us with the launch), 65536 of 512 slots two
+// launches of 16 workgroups (22 us), whose waves load eight tokens a lane at once (32 us with a load for each step).
 #include "adapters.h"
 
 namespace loftq {
